@@ -36,7 +36,7 @@
  *    was launched (except SSN_E_HIP, where a launch itself failed) and ssn_last_error() gives a
  *    thread-local message.
  *  - Sizes: N, M >= 0 (a zero size is a no-op that returns SSN_OK); K % 32 == 0 for the
- *    NVFP4/2:4 calls (so a 32-bit word of meta covers whole groups and rows of every array
+ *    NVFP4/2:4 and integer 4-bit calls (so a 32-bit word of meta covers whole groups and rows of every array
  *    are 2-byte aligned). Device pointers to tensors (activations, codes, scales, vals, meta,
  *    outputs) must be 16-byte aligned; pointers to single scalars and to int32/f32 index or
  *    weight arrays (tensor scales, counters, routing arrays, combine weights) only need the
@@ -66,7 +66,9 @@ typedef enum {
   SSN_E_RANGE = 7   /* an argument is outside its documented range (e.g. top-k, expert count) */
 } ssn_status;
 
-enum { SSN_F32 = 0, SSN_BF16 = 1 };
+/* SSN_F16 (IEEE half) is taken by the integer 4-bit calls and by moe_permute / moe_unpermute and their
+ * gradients; the other calls refuse it (DTYPE). */
+enum { SSN_F32 = 0, SSN_BF16 = 1, SSN_F16 = 2 };
 
 /* GEMM algorithms. Each call writes the one it ran to *algo_used (host int, nullable).
  * The matrix-core algorithms run decode-shaped kernels for M <= 16 (weights streamed once
@@ -359,6 +361,113 @@ int mxfp4_quantize(const void* V, int v_dtype, int64_t R, int64_t K, int layout,
 int gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const uint8_t* w_codes,
                const uint8_t* w_scales, int64_t N, int64_t K, void* Y, int y_dtype, int algo, int* algo_used,
                void* stream);
+
+/* =============================================================================================
+ * Integer 4-bit weights with group scales: the format most 4-bit checkpoints use, beside NVFP4.
+ * A group is `group` consecutive k of one row (a positive multiple of 32; the last group of a row is
+ * shorter when group does not divide K; group >= K gives one scale per row). With
+ * groups = ceil(K / group) and g = k / group:
+ *   codes   u8 [N, K/2]      q[n, k] in 0..15, k = 2j in the low nibble of byte j (as for NVFP4)
+ *   scales  bf16 or f16 [N, groups] (s_dtype)
+ *   zeros   u8 [N, groups], any value of a byte; or NULL: every zero point is 8 (symmetric)
+ *   W_hat[n, k] = scales[n, g] * (q[n, k] - zeros[n, g])
+ * Scales are 2-byte aligned and zeros any, so that one row's or one expert's part of a larger array can
+ * be passed; the other tensors are 16-byte aligned. K % 32 == 0.
+ * ============================================================================================= */
+
+/* ---------------------------------------------------------------------------------------------
+ * int4_quantize — codes, scales and zero points of W [N, K] (f32, bf16 or f16, w_dtype; finite).
+ * Per group, with s rounded to s_dtype (through f32, nearest-even, at most its largest finite value)
+ * before it is used:
+ *   zeros given: lo = min(0, min W), hi = max(0, max W), s = (hi - lo) / 15,
+ *                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(W / s) + z, 0, 15);
+ *   zeros NULL:  s = max|W| / 7, q = clamp(rne(W / s) + 8, 0, 15).
+ * A group whose s is 0 has q = z (z = 0 where zeros are given). rne rounds to the nearest whole number,
+ * halves to the even one; decisions are exact.
+ * Errors: NULL, SHAPE (K % 32), ALIGN, DTYPE, RANGE (group), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int int4_quantize(const void* W, int w_dtype, int64_t N, int64_t K, int64_t group, int s_dtype, uint8_t* codes,
+                  void* scales, uint8_t* zeros, void* stream);
+
+/* int4_dequantize — W_hat as above, the f32 product rounded once to out_dtype (f32, bf16 or f16).
+ * Errors: as int4_quantize. */
+int int4_dequantize(const uint8_t* codes, const void* scales, int s_dtype, const uint8_t* zeros, int64_t N, int64_t K,
+                    int64_t group, void* out, int out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * gemv_int4 — Y = X . W_hat^T for one token or a few: the weights stream from memory once per 64
+ * rows of X. Inside a group the sum runs over x (q - z) in f32, and the scale multiplies it once, so no
+ * weight is rounded. X [M, K] bf16 or f16 (x_dtype); Y [M, N] f32, bf16 or f16 (y_dtype, rounded to
+ * nearest even). Any M is computed; larger M than some 64 are a matrix product, which the tiles of
+ * gemm_nvfp4_dense are made for and this call is not. A non-finite X[m, k] makes row m of Y non-finite.
+ * algo: AUTO or MFMA, reported in *algo_used (host, nullable).
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE (group), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int gemv_int4(const void* X, int x_dtype, int64_t M, int64_t N, int64_t K, const uint8_t* codes, const void* scales,
+              int s_dtype, const uint8_t* zeros, int64_t group, void* Y, int y_dtype, int algo, int* algo_used,
+              void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_grouped_gemv_int4 — the same product for every expert's rows, in one launch:
+ *   Y[r, :] = X[src(r), :] . W_hat_e^T  for r in [offsets[e], offsets[e+1]),
+ * src(r) = row_token[r], or r where row_token is NULL; weights [E, N, ...] per expert. For routings with
+ * few rows per expert: an expert's weights stream once per 16 of its rows. Epilogue (SSN_EPI_NONE,
+ * SSN_EPI_SILU_GATE), x_rows, R and the clamping of offsets into [0, R] and of source rows into
+ * [0, x_rows) are those of moe_grouped_gemm_nvfp4; N need only be even for SILU_GATE, and the gate is
+ * formed from the f32 sums. Offsets must ascend, as moe_route writes them. Rows of Y that belong to no
+ * expert (r >= offsets[E]) are left as they were. algo: AUTO or STREAM, reported in *algo_used (host,
+ * nullable). Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE, HIP.
+ * ------------------------------------------------------------------------------------------- */
+int moe_grouped_gemv_int4(const void* X, int x_dtype, int64_t x_rows, const int32_t* row_token,
+                          const int32_t* expert_offsets, int E, int64_t R, int64_t N, int64_t K, const uint8_t* codes,
+                          const void* scales, int s_dtype, const uint8_t* zeros, int64_t group, int epilogue, void* Y,
+                          int y_dtype, int algo, int* algo_used, void* stream);
+
+/* =============================================================================================
+ * Tokens to expert order and back, with the routing weights applied, and both gradients: for experts that
+ * are not one of the grouped products above (adapters, exchanges between GPUs, training a router
+ * over frozen experts). The entry f = t*k + j of a routing owns row row_of[f] (as moe_route writes it); a
+ * value outside [0, R) means that the entry has no row (an invalid id, or a dropped one): nothing is
+ * written for it, it adds nothing, and its weight's gradient is 0. No two entries may own one row.
+ * topk_weights f32 [T, k]; NULL: every weight is 1. Sums are f32 in slot order. Rows and tokens are
+ * f32, bf16 or f16, each result rounded once; any D. Limits: 1 <= k <= 64, T*k < 2^31. Outputs must
+ * not overlap inputs.
+ * ============================================================================================= */
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_permute — Xp[row_of[f], :] = topk_weights[f] * X[t, :]. X [T, D], Xp [R, D] of dtype. Rows that no
+ * entry owns are left as they were. Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (k), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int moe_permute(const void* X, int dtype, int64_t T, int k, int64_t D, const int32_t* row_of,
+                const float* topk_weights, int64_t R, void* Xp, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_permute_backward — from dXp [R, D], the gradient of Xp: dX[t, :] = sum_j topk_weights[f] *
+ * dXp[row_of[f], :] and, where dweights (f32 [T, k]) is given, dweights[f] = <X[t, :], dXp[row_of[f], :]>
+ * (X is needed for that only, else NULL). dXp, X and dX of dtype.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (k), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int moe_permute_backward(const void* dXp, int dtype, int64_t R, const int32_t* row_of, const float* topk_weights,
+                         int64_t T, int k, int64_t D, const void* X, void* dX, float* dweights, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_unpermute — out[t, :] = sum_j topk_weights[f] * Yp[row_of[f], :]: moe_combine for rows and results
+ * of any of the three types, and without weights. Yp [R, D] of yp_dtype; out [T, D] of out_dtype, which
+ * is yp_dtype or f32. Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (k), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int moe_unpermute(const void* Yp, int yp_dtype, int64_t R, const int32_t* row_of, const float* topk_weights, int64_t T,
+                  int k, int64_t D, void* out, int out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_unpermute_backward — from dout [T, D] of out_dtype, the gradient of out: dYp[row_of[f], :] =
+ * topk_weights[f] * dout[t, :] (of yp_dtype; rows that no entry owns are left as they were) and, where
+ * dweights (f32 [T, k]) is given, dweights[f] = <dout[t, :], Yp[row_of[f], :]> (Yp of yp_dtype, needed
+ * for that only, else NULL). out_dtype is yp_dtype or f32. The gradient of moe_combine too, with
+ * out_dtype f32. Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (k), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, int64_t D, const int32_t* row_of,
+                           const float* topk_weights, int64_t R, const void* Yp, void* dYp, int yp_dtype,
+                           float* dweights, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Calibration (measurement only; no product path calls it). The roofline of the compute-bound

@@ -16,7 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssnvfp4.so")
 
 SSN_OK, SSN_E_NULL, SSN_E_SHAPE, SSN_E_ALIGN, SSN_E_DTYPE, SSN_E_ALGO, SSN_E_HIP, SSN_E_RANGE = range(8)
-SSN_F32, SSN_BF16 = 0, 1
+SSN_F32, SSN_BF16, SSN_F16 = 0, 1, 2
 ALGO_AUTO, ALGO_VALU, ALGO_MFMA, ALGO_SMFMAC, ALGO_GATHER, ALGO_DECOMPRESS_MFMA, ALGO_STREAM = 0, 1, 2, 3, 4, 5, 6
 ALGO_NAMES = {ALGO_AUTO: "auto", ALGO_VALU: "valu", ALGO_MFMA: "mfma", ALGO_SMFMAC: "smfmac", ALGO_GATHER: "gather",
               ALGO_DECOMPRESS_MFMA: "decompress_mfma", ALGO_STREAM: "stream"}
@@ -52,6 +52,15 @@ _SIGS = {
     "gemm_mxfp4": ([_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _int, _vp, _vp], _int),
     "moe_nvfp4_ffn_noalloc": ([_vp, _i64, _i64, _vp, _vp, _int, _int, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp,
                                _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "int4_quantize": ([_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp], _int),
+    "int4_dequantize": ([_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _int, _vp], _int),
+    "gemv_int4": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _vp], _int),
+    "moe_grouped_gemv_int4": ([_vp, _int, _i64, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _vp, _i64, _int,
+                               _vp, _int, _int, _vp, _vp], _int),
+    "moe_permute": ([_vp, _int, _i64, _int, _i64, _vp, _vp, _i64, _vp, _vp], _int),
+    "moe_permute_backward": ([_vp, _int, _i64, _vp, _vp, _i64, _int, _i64, _vp, _vp, _vp, _vp], _int),
+    "moe_unpermute": ([_vp, _int, _i64, _vp, _vp, _i64, _int, _i64, _vp, _int, _vp], _int),
+    "moe_unpermute_backward": ([_vp, _int, _i64, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _vp], _int),
     "mfma_probe_sink_floats": ([], _i64),
     "mfma_probe": ([_int, _int, _int, ctypes.c_uint32, _vp, _vp, _vp], _int),
 }
@@ -490,6 +499,226 @@ def moe_nvfp4_ffn_noalloc(X, topk_ids, topk_weights, E, up, down, out, bad_ids, 
                                        _ptr(down[0]), _ptr(down[1]), _ptr(down[2]), _ptr(down[3]), _ptr(out),
                                        _ptr(bad_ids), _stream(X.device)))
     return out, bad_ids
+
+
+# ------------------------------------------------------------------------------------------------
+# integer 4-bit weights with group scales
+
+_DTYPES = {torch.float32: SSN_F32, torch.bfloat16: SSN_BF16, torch.float16: SSN_F16}
+_HALVES = (torch.bfloat16, torch.float16)
+_ANY = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _dtype(t, name, allowed):
+    dt = t if isinstance(t, torch.dtype) else getattr(t, "dtype", None)
+    if dt not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(a)[6:] for a in allowed)}, got {dt}")
+    return _DTYPES[dt]
+
+
+def _dims(t, n, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _run_on(dev, fname, cargs, prepare, keep, result):
+    """_run with `dev` current for the launch, after a check that every tensor is on it. A prepared call
+    launches on the device that is current when it is called."""
+    for t in (*keep, *(result if isinstance(result, tuple) else (result,))):
+        if isinstance(t, torch.Tensor) and t.device != dev:
+            raise ValueError(f"{fname}: tensors on {dev} and {t.device}")
+    if prepare or dev.index == torch.cuda.current_device():
+        return _run(fname, cargs, prepare, keep, result)
+    with torch.cuda.device(dev):
+        return _run(fname, cargs, prepare, keep, result)
+
+
+def _int4_group(K, group):
+    if isinstance(group, bool) or not isinstance(group, int) or group < 32 or group % 32:
+        raise ValueError(f"group must be a positive multiple of 32, got {group}")
+    return -(-K // group)
+
+
+def int4_quantize(W, group=128, symmetric=False, scale_dtype=torch.bfloat16, codes=None, scales=None, zeros=None,
+                  prepare=False):
+    """4-bit codes of W [N, K] (f32, bf16 or f16) with a scale, and unless symmetric a zero point, per `group`
+    consecutive k. Returns (codes u8 [N, K/2], scales of scale_dtype [N, ceil(K/group)], zeros u8 of that shape
+    or None)."""
+    N, K = _dims(W, 2, "W")
+    wdt = _dtype(_need(W, W.dtype, "W"), "W", _ANY)
+    groups = _int4_group(K, group)
+    dev = W.device
+    if symmetric and zeros is not None:
+        raise ValueError("symmetric quantisation has no zeros")
+    codes = codes if codes is not None else torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+    scales = scales if scales is not None else torch.empty((N, groups), dtype=scale_dtype, device=dev)
+    if not symmetric and zeros is None:
+        zeros = torch.empty((N, groups), dtype=torch.uint8, device=dev)
+    sdt = _dtype(scales, "scales", _HALVES)
+    _need(codes, torch.uint8, "codes", (N, K // 2)); _need(scales, scales.dtype, "scales", (N, groups))
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", (N, groups))
+    cargs = (_ptr(W), wdt, N, K, group, sdt, _ptr(codes), _ptr(scales), _ptr(zeros), _stream(dev))
+    return _run_on(dev, "int4_quantize", cargs, prepare, (W,), (codes, scales, zeros))
+
+
+def int4_dequantize(codes, scales, zeros=None, group=128, out_dtype=torch.float32, out=None, prepare=False):
+    """W_hat [N, K] = scales * (codes - zeros) (zeros None: 8), f32, bf16 or f16."""
+    N, Kh = _dims(codes, 2, "codes")
+    K = 2 * Kh
+    groups = _int4_group(K, group)
+    sdt = _dtype(scales, "scales", _HALVES)
+    _need(codes, torch.uint8, "codes"); _need(scales, scales.dtype, "scales", (N, groups))
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", (N, groups))
+    out = out if out is not None else torch.empty((N, K), dtype=out_dtype, device=codes.device)
+    odt = _dtype(out, "out", _ANY)
+    _need(out, out.dtype, "out", (N, K))
+    cargs = (_ptr(codes), _ptr(scales), sdt, _ptr(zeros), N, K, group, _ptr(out), odt, _stream(codes.device))
+    return _run_on(codes.device, "int4_dequantize", cargs, prepare, (codes, scales, zeros), out)
+
+
+def gemv_int4(X, codes, scales, zeros=None, group=128, y_dtype=torch.float32, algo=ALGO_AUTO, Y=None, prepare=False):
+    """Y = X . W_hat^T for a few rows of X (bf16 or f16 [M, K]) and integer 4-bit weights: codes u8 [N, K/2],
+    scales bf16 or f16 and zeros u8 (or None: 8) [N, ceil(K/group)]. Returns (Y, algorithm that ran)."""
+    M, K = _dims(X, 2, "X")
+    N, _ = _dims(codes, 2, "codes")
+    groups = _int4_group(K, group)
+    xdt, sdt = _dtype(X, "X", _HALVES), _dtype(scales, "scales", _HALVES)
+    _need(X, X.dtype, "X"); _need(codes, torch.uint8, "codes", (N, K // 2))
+    _need(scales, scales.dtype, "scales", (N, groups))
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", (N, groups))
+    dev = X.device
+    Y = Y if Y is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+    ydt = _dtype(Y, "Y", _ANY)
+    _need(Y, Y.dtype, "Y", (M, N))
+    used = ctypes.c_int(-1)
+    cargs = (_ptr(X), xdt, M, N, K, _ptr(codes), _ptr(scales), sdt, _ptr(zeros), group, _ptr(Y), ydt, algo,
+             ctypes.byref(used), _stream(dev))
+    out = _run_on(dev, "gemv_int4", cargs, prepare, (X, codes, scales, zeros, used), Y)
+    return (out[0], (Y, used)) if prepare else (Y, used.value)
+
+
+def moe_grouped_gemv_int4(X, row_token, expert_offsets, R, codes, scales, zeros=None, group=128, epilogue=EPI_NONE,
+                          y_dtype=torch.float32, algo=ALGO_AUTO, Y=None, prepare=False):
+    """Every expert's integer 4-bit product in one launch, for routings with few rows per expert. X bf16 or f16
+    [x_rows, K]; row_token int32 [R] or None (identity); expert_offsets int32 [E+1]; codes u8 [E, N, K/2], scales
+    bf16 or f16 and zeros u8 (or None: 8) [E, N, ceil(K/group)]. Returns (Y [R, N], or [R, N/2] for
+    EPI_SILU_GATE, algorithm that ran); rows of no expert keep what Y held."""
+    x_rows, K = _dims(X, 2, "X")
+    E, N, _ = _dims(codes, 3, "codes")
+    groups = _int4_group(K, group)
+    xdt, sdt = _dtype(X, "X", _HALVES), _dtype(scales, "scales", _HALVES)
+    _need(X, X.dtype, "X"); _need(expert_offsets, torch.int32, "expert_offsets", (E + 1,))
+    if row_token is not None:
+        _need(row_token, torch.int32, "row_token", (R,))
+    _need(codes, torch.uint8, "codes", (E, N, K // 2)); _need(scales, scales.dtype, "scales", (E, N, groups))
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", (E, N, groups))
+    dev = X.device
+    ncols = N // 2 if epilogue == EPI_SILU_GATE else N
+    Y = Y if Y is not None else torch.empty((R, ncols), dtype=y_dtype, device=dev)
+    ydt = _dtype(Y, "Y", _ANY)
+    _need(Y, Y.dtype, "Y", (R, ncols))
+    used = ctypes.c_int(-1)
+    cargs = (_ptr(X), xdt, x_rows, _ptr(row_token), _ptr(expert_offsets), E, R, N, K, _ptr(codes), _ptr(scales), sdt,
+             _ptr(zeros), group, epilogue, _ptr(Y), ydt, algo, ctypes.byref(used), _stream(dev))
+    out = _run_on(dev, "moe_grouped_gemv_int4", cargs, prepare,
+                  (X, row_token, expert_offsets, codes, scales, zeros, used), Y)
+    return (out[0], (Y, used)) if prepare else (Y, used.value)
+
+
+# ------------------------------------------------------------------------------------------------
+# tokens to expert order and back, and the gradients
+
+
+def _entries(row_of, T, topk_weights):
+    """k of a routing of T tokens, from its row_of [T*k] and weights [T, k]."""
+    F, = _dims(_need(row_of, torch.int32, "row_of"), 1, "row_of")
+    if topk_weights is not None:
+        k = _dims(topk_weights, 2, "topk_weights")[1]
+        _need(topk_weights, torch.float32, "topk_weights", (T, k))
+    else:
+        k = F // T if T > 0 else 1
+    if F != T * k:
+        raise ValueError(f"row_of has {F} entries, not {T} tokens times {k}")
+    return k
+
+
+def moe_permute(X, row_of, topk_weights=None, R=None, Xp=None, prepare=False):
+    """Tokens to expert order: Xp[row_of[t*k+j]] = topk_weights[t, j] * X[t] (no weights: a copy). X f32, bf16 or
+    f16 [T, D]; row_of int32 [T*k] as moe_route gives it (entries outside [0, R) have no row). Returns Xp [R, D]
+    of X's type, R = T*k unless given; rows that no entry owns keep what Xp held."""
+    T, D = _dims(X, 2, "X")
+    k = _entries(row_of, T, topk_weights)
+    dt = _dtype(_need(X, X.dtype, "X"), "X", _ANY)
+    R = R if R is not None else (T * k if Xp is None else Xp.shape[0])
+    Xp = Xp if Xp is not None else torch.empty((R, D), dtype=X.dtype, device=X.device)
+    _need(Xp, X.dtype, "Xp", (R, D))
+    cargs = (_ptr(X), dt, T, k, D, _ptr(row_of), _ptr(topk_weights), R, _ptr(Xp), _stream(X.device))
+    return _run_on(X.device, "moe_permute", cargs, prepare, (X, row_of, topk_weights), Xp)
+
+
+def moe_permute_backward(dXp, row_of, T, topk_weights=None, X=None, dX=None, dweights=None, prepare=False):
+    """Gradient of moe_permute for T tokens from dXp [R, D]: (dX [T, D] of dXp's type, dweights f32 [T, k]).
+    The weights' gradient needs the forward's X; without X it is None."""
+    R, D = _dims(dXp, 2, "dXp")
+    k = _entries(row_of, T, topk_weights)
+    dt = _dtype(_need(dXp, dXp.dtype, "dXp"), "dXp", _ANY)
+    dev = dXp.device
+    dX = dX if dX is not None else torch.empty((T, D), dtype=dXp.dtype, device=dev)
+    _need(dX, dXp.dtype, "dX", (T, D))
+    dweights = _dweights(dweights, X, "X", dXp.dtype, (T, D), T, k, dev)
+    cargs = (_ptr(dXp), dt, R, _ptr(row_of), _ptr(topk_weights), T, k, D, _ptr(X), _ptr(dX), _ptr(dweights),
+             _stream(dev))
+    return _run_on(dev, "moe_permute_backward", cargs, prepare, (dXp, row_of, topk_weights, X), (dX, dweights))
+
+
+def _dweights(dweights, other, name, dtype, shape, T, k, dev):
+    if other is None:
+        if dweights is not None:
+            raise ValueError(f"dweights needs {name}")
+        return None
+    _need(other, dtype, name, shape)
+    dweights = dweights if dweights is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    return _need(dweights, torch.float32, "dweights", (T, k))
+
+
+def moe_unpermute(Yp, row_of, T, topk_weights=None, out_dtype=None, out=None, prepare=False):
+    """Expert rows back to T tokens: out[t] = sum_j topk_weights[t, j] * Yp[row_of[t*k+j]] (no weights: the plain
+    sum), summed in f32. Yp f32, bf16 or f16 [R, D]; out [T, D] of Yp's type unless out_dtype is float32."""
+    R, D = _dims(Yp, 2, "Yp")
+    k = _entries(row_of, T, topk_weights)
+    ydt = _dtype(_need(Yp, Yp.dtype, "Yp"), "Yp", _ANY)
+    if out is None:
+        out = torch.empty((T, D), dtype=out_dtype if out_dtype is not None else Yp.dtype, device=Yp.device)
+    odt = _dtype(_need(out, out.dtype, "out", (T, D)), "out", (torch.float32, Yp.dtype))
+    cargs = (_ptr(Yp), ydt, R, _ptr(row_of), _ptr(topk_weights), T, k, D, _ptr(out), odt, _stream(Yp.device))
+    return _run_on(Yp.device, "moe_unpermute", cargs, prepare, (Yp, row_of, topk_weights), out)
+
+
+def moe_unpermute_backward(dout, row_of, R, topk_weights=None, Yp=None, y_dtype=None, dYp=None, dweights=None,
+                           prepare=False):
+    """Gradient of moe_unpermute (and of moe_combine) from dout [T, D]: (dYp [R, D], dweights f32 [T, k]). dYp has
+    y_dtype (dout's type unless given), or Yp's type; the weights' gradient needs the forward's Yp; without Yp it
+    is None. Rows that no entry owns keep what dYp held."""
+    T, D = _dims(dout, 2, "dout")
+    k = _entries(row_of, T, topk_weights)
+    dev = dout.device
+    if y_dtype is None:
+        y_dtype = Yp.dtype if Yp is not None else dYp.dtype if dYp is not None else dout.dtype
+    ydt = _dtype(y_dtype, "dYp", _ANY)
+    odt = _dtype(_need(dout, dout.dtype, "dout"), "dout", (torch.float32, y_dtype))
+    dYp = dYp if dYp is not None else torch.empty((R, D), dtype=y_dtype, device=dev)
+    _need(dYp, y_dtype, "dYp", (R, D))
+    dweights = _dweights(dweights, Yp, "Yp", y_dtype, (R, D), T, k, dev)
+    cargs = (_ptr(dout), odt, T, k, D, _ptr(row_of), _ptr(topk_weights), R, _ptr(Yp), _ptr(dYp), ydt, _ptr(dweights),
+             _stream(dev))
+    return _run_on(dev, "moe_unpermute_backward", cargs, prepare, (dout, row_of, topk_weights, Yp), (dYp, dweights))
 
 
 def mfma_probe_sink_floats():

@@ -471,6 +471,195 @@ int gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const
 }  // extern "C"
 
 // ---------------------------------------------------------------------------------------------
+// Integer 4-bit weights with group scales
+namespace {
+
+int check_type(const char* fn, int dt, const char* name, bool f32_too) {
+  if (dt == SSN_BF16 || dt == SSN_F16 || (f32_too && dt == SSN_F32)) return SSN_OK;
+  return fail(SSN_E_DTYPE, "%s: %s code %d is not %sSSN_BF16 or SSN_F16", fn, name, dt, f32_too ? "SSN_F32, " : "");
+}
+
+int check_group(const char* fn, int64_t group) {
+  if (group < 32 || group % 32)
+    return fail(SSN_E_RANGE, "%s: group=%lld is not a positive multiple of 32", fn, (long long)group);
+  return SSN_OK;
+}
+
+int check_scales(const char* fn, const uint16_t* scales) {
+  REQUIRE_ELEM_PTR(scales);
+  return SSN_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+
+int gemv_int4_common(const char* fn, ssn::Int4GemvArgs a, void* stream) {
+  int st;
+  if ((st = check_nk(fn, a.N, a.K))) return st;
+  if (a.M < 0 || a.M > kMaxRows || a.x_rows < 0 || a.x_rows > kMaxRows)
+    return fail(SSN_E_SHAPE, "%s: bad row counts (%lld of Y, %lld of X)", fn, (long long)a.M, (long long)a.x_rows);
+  if ((st = check_group(fn, a.group))) return st;
+  if ((st = check_type(fn, a.x_type, "x_dtype", false)) || (st = check_type(fn, a.s_type, "s_dtype", false)) ||
+      (st = check_type(fn, a.y_type, "y_dtype", true)))
+    return st;
+  if (a.M == 0 || a.N == 0) return ok();
+  if (a.K == 0) return fail(SSN_E_SHAPE, "%s: K must be positive when Y has elements", fn);
+  if (a.x_rows == 0) return fail(SSN_E_SHAPE, "%s: x_rows must be positive when Y has rows", fn);
+  if (a.N * (a.K / 2) > ((int64_t)1 << 40) / a.E) return fail(SSN_E_SHAPE, "%s: weights too large", fn);
+  const void *X = a.X, *codes = a.codes, *Y = a.Y;
+  REQUIRE_PTR(X); REQUIRE_PTR(codes); REQUIRE_PTR(Y);
+  if ((st = check_scales(fn, a.scales))) return st;   // the zero points are bytes: any alignment, or none
+  a.groups = ceil_div(a.K, a.group);
+  return hip_status(ssn::launch_int4_gemv(a, as_stream(stream)), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+int int4_quantize(const void* W, int w_dtype, int64_t N, int64_t K, int64_t group, int s_dtype, uint8_t* codes,
+                  void* scales, uint8_t* zeros, void* stream) {
+  const char* fn = "int4_quantize";
+  int st;
+  if ((st = check_nk(fn, N, K)) || (st = check_group(fn, group))) return st;
+  if ((st = check_type(fn, w_dtype, "w_dtype", true)) || (st = check_type(fn, s_dtype, "s_dtype", false))) return st;
+  if (N == 0 || K == 0) return ok();
+  REQUIRE_PTR(W); REQUIRE_PTR(codes);
+  uint16_t* const s16 = (uint16_t*)scales;
+  if ((st = check_scales(fn, s16))) return st;
+  return hip_status(ssn::launch_int4_quantize(W, w_dtype, N, K, group, codes, s16, s_dtype, zeros, as_stream(stream)), fn);
+}
+
+int int4_dequantize(const uint8_t* codes, const void* scales, int s_dtype, const uint8_t* zeros, int64_t N, int64_t K,
+                    int64_t group, void* out, int out_dtype, void* stream) {
+  const char* fn = "int4_dequantize";
+  int st;
+  if ((st = check_nk(fn, N, K)) || (st = check_group(fn, group))) return st;
+  if ((st = check_type(fn, s_dtype, "s_dtype", false)) || (st = check_type(fn, out_dtype, "out_dtype", true))) return st;
+  if (N == 0 || K == 0) return ok();
+  REQUIRE_PTR(codes); REQUIRE_PTR(out);
+  const uint16_t* const s16 = (const uint16_t*)scales;
+  if ((st = check_scales(fn, s16))) return st;
+  return hip_status(ssn::launch_int4_dequantize(codes, s16, s_dtype, zeros, N, K, group, out, out_dtype,
+                                                as_stream(stream)), fn);
+}
+
+int gemv_int4(const void* X, int x_dtype, int64_t M, int64_t N, int64_t K, const uint8_t* codes, const void* scales,
+              int s_dtype, const uint8_t* zeros, int64_t group, void* Y, int y_dtype, int algo, int* algo_used,
+              void* stream) {
+  const char* fn = "gemv_int4";
+  if (algo != SSN_ALGO_AUTO && algo != SSN_ALGO_MFMA)
+    return fail(SSN_E_ALGO, "%s: algorithm %d is not available (MFMA only)", fn, algo);
+  ssn::Int4GemvArgs a{X, M, M, N, K, group, 0, codes, (const uint16_t*)scales, zeros, nullptr, nullptr, Y, 1, x_dtype,
+                      s_dtype, y_dtype, 0};
+  const int st = gemv_int4_common(fn, a, stream);
+  if (!st && algo_used) *algo_used = SSN_ALGO_MFMA;
+  return st;
+}
+
+int moe_grouped_gemv_int4(const void* X, int x_dtype, int64_t x_rows, const int32_t* row_token,
+                          const int32_t* expert_offsets, int E, int64_t R, int64_t N, int64_t K, const uint8_t* codes,
+                          const void* scales, int s_dtype, const uint8_t* zeros, int64_t group, int epilogue, void* Y,
+                          int y_dtype, int algo, int* algo_used, void* stream) {
+  const char* fn = "moe_grouped_gemv_int4";
+  if (E < 1 || E > kMaxExperts) return fail(SSN_E_RANGE, "%s: E=%d outside [1, %d]", fn, E, kMaxExperts);
+  if (epilogue != SSN_EPI_NONE && epilogue != SSN_EPI_SILU_GATE)
+    return fail(SSN_E_RANGE, "%s: unknown epilogue %d", fn, epilogue);
+  if (epilogue == SSN_EPI_SILU_GATE && N % 2) return fail(SSN_E_SHAPE, "%s: SILU_GATE needs N even (N=%lld)", fn, (long long)N);
+  if (algo != SSN_ALGO_AUTO && algo != SSN_ALGO_STREAM)
+    return fail(SSN_E_ALGO, "%s: algorithm %d is not available (STREAM only)", fn, algo);
+  if (R > 0 && N > 0) { REQUIRE_ELEM_PTR(expert_offsets); REQUIRE_OPT_ELEM_PTR(row_token); }
+  ssn::Int4GemvArgs a{X, x_rows, R, N, K, group, 0, codes, (const uint16_t*)scales, zeros, row_token, expert_offsets, Y,
+                      E, x_dtype, s_dtype, y_dtype, epilogue == SSN_EPI_SILU_GATE};
+  const int st = gemv_int4_common(fn, a, stream);
+  if (!st && algo_used) *algo_used = SSN_ALGO_STREAM;
+  return st;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Tokens to expert order and back
+namespace {
+
+int check_permute(const char* fn, int64_t T, int k, int64_t D, int64_t R) {
+  if (T < 0 || D < 0 || R < 0 || R > kMaxRows || T > kMaxRows || D > ((int64_t)1 << 30))
+    return fail(SSN_E_SHAPE, "%s: bad sizes (T=%lld, D=%lld, R=%lld)", fn, (long long)T, (long long)D, (long long)R);
+  if (k < 1 || k > kMaxTopK) return fail(SSN_E_RANGE, "%s: k=%d outside [1, %d]", fn, k, kMaxTopK);
+  if (T * k >= ((int64_t)1 << 31) - 1024) return fail(SSN_E_SHAPE, "%s: T*k=%lld too large", fn, (long long)(T * k));
+  return SSN_OK;
+}
+
+// the token side may be f32 beside 16-bit rows; otherwise both sides have one type
+int check_side_types(const char* fn, int rows, int tokens, const char* name) {
+  int st;
+  if ((st = check_type(fn, rows, "row dtype", true)) || (st = check_type(fn, tokens, name, true))) return st;
+  if (tokens != rows && tokens != SSN_F32)
+    return fail(SSN_E_DTYPE, "%s: %s code %d is neither SSN_F32 nor the rows' code %d", fn, name, tokens, rows);
+  return SSN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_permute(const void* X, int dtype, int64_t T, int k, int64_t D, const int32_t* row_of,
+                const float* topk_weights, int64_t R, void* Xp, void* stream) {
+  const char* fn = "moe_permute";
+  int st;
+  if ((st = check_permute(fn, T, k, D, R)) || (st = check_type(fn, dtype, "dtype", true))) return st;
+  if (T == 0 || D == 0 || R == 0) return ok();
+  REQUIRE_PTR(X); REQUIRE_ELEM_PTR(row_of); REQUIRE_OPT_ELEM_PTR(topk_weights); REQUIRE_PTR(Xp);
+  ssn::PermuteArgs a{T, D, R, k, dtype, dtype, row_of, topk_weights, X, nullptr, nullptr, Xp, nullptr};
+  return hip_status(ssn::launch_moe_scatter(a, as_stream(stream)), fn);
+}
+
+int moe_permute_backward(const void* dXp, int dtype, int64_t R, const int32_t* row_of, const float* topk_weights,
+                         int64_t T, int k, int64_t D, const void* X, void* dX, float* dweights, void* stream) {
+  const char* fn = "moe_permute_backward";
+  int st;
+  if ((st = check_permute(fn, T, k, D, R)) || (st = check_type(fn, dtype, "dtype", true))) return st;
+  if (T == 0) return ok();
+  REQUIRE_ELEM_PTR(row_of); REQUIRE_OPT_ELEM_PTR(topk_weights); REQUIRE_OPT_ELEM_PTR(dweights);
+  if (D > 0) {
+    REQUIRE_PTR(dX);
+    if (R > 0) REQUIRE_PTR(dXp);
+    if (dweights) REQUIRE_PTR(X);
+  } else if (!dweights) return ok();
+  ssn::PermuteArgs a{T, D, R, k, dtype, dtype, row_of, topk_weights, X, dXp, dX, nullptr, dweights};
+  return hip_status(ssn::launch_moe_gather(a, as_stream(stream)), fn);
+}
+
+int moe_unpermute(const void* Yp, int yp_dtype, int64_t R, const int32_t* row_of, const float* topk_weights, int64_t T,
+                  int k, int64_t D, void* out, int out_dtype, void* stream) {
+  const char* fn = "moe_unpermute";
+  int st;
+  if ((st = check_permute(fn, T, k, D, R)) || (st = check_side_types(fn, yp_dtype, out_dtype, "out_dtype"))) return st;
+  if (T == 0 || D == 0) return ok();
+  REQUIRE_ELEM_PTR(row_of); REQUIRE_OPT_ELEM_PTR(topk_weights); REQUIRE_PTR(out);
+  if (R > 0) REQUIRE_PTR(Yp);
+  ssn::PermuteArgs a{T, D, R, k, out_dtype, yp_dtype, row_of, topk_weights, nullptr, Yp, out, nullptr, nullptr};
+  return hip_status(ssn::launch_moe_gather(a, as_stream(stream)), fn);
+}
+
+int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, int64_t D, const int32_t* row_of,
+                           const float* topk_weights, int64_t R, const void* Yp, void* dYp, int yp_dtype,
+                           float* dweights, void* stream) {
+  const char* fn = "moe_unpermute_backward";
+  int st;
+  if ((st = check_permute(fn, T, k, D, R)) || (st = check_side_types(fn, yp_dtype, out_dtype, "out_dtype"))) return st;
+  if (T == 0) return ok();
+  REQUIRE_ELEM_PTR(row_of); REQUIRE_OPT_ELEM_PTR(topk_weights); REQUIRE_OPT_ELEM_PTR(dweights);
+  if (D > 0 && R > 0) {
+    REQUIRE_PTR(dout); REQUIRE_PTR(dYp);
+    if (dweights) REQUIRE_PTR(Yp);
+  } else if (!dweights) return ok();   // no row: only the weights' gradients, all 0, are left to write
+  ssn::PermuteArgs a{T, D, R, k, out_dtype, yp_dtype, row_of, topk_weights, dout, Yp, nullptr, dYp, dweights};
+  return hip_status(ssn::launch_moe_scatter(a, as_stream(stream)), fn);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
 // Calibration
 extern "C" {
 

@@ -85,6 +85,41 @@ hipError_t launch_mx_quantize(const void* V, int v_bf16, int64_t R, int64_t K, i
 hipError_t launch_gemm_mx(const uint8_t* xc, const uint8_t* xs, int64_t M, const uint8_t* wc, const uint8_t* ws,
                           int64_t N, int64_t K, void* Y, int y_bf16, hipStream_t s);
 
+// integer 4-bit weights with group scales. Types are the codes of include/ssnvfp4.h (f32 0, bf16 1, f16 2);
+// scales are 16-bit (s_type bf16 or f16), zeros nullable (then every zero point is 8)
+hipError_t launch_int4_quantize(const void* W, int w_type, int64_t N, int64_t K, int64_t group, uint8_t* codes,
+                                uint16_t* scales, int s_type, uint8_t* zeros, hipStream_t s);
+hipError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, int s_type, const uint8_t* zeros,
+                                  int64_t N, int64_t K, int64_t group, void* out, int out_type, hipStream_t s);
+struct Int4GemvArgs {
+  const void* X;            // [x_rows, K] bf16 or f16
+  int64_t x_rows, M, N, K;  // M: rows of Y; N: weight rows (per expert)
+  int64_t group, groups;    // groups = ceil(K / group)
+  const uint8_t* codes;     // [E, N, K/2]
+  const uint16_t* scales;   // [E, N, groups]
+  const uint8_t* zeros;     // [E, N, groups] or nullptr
+  const int32_t* row_token; // grouped: source row of each row, or nullptr (identity)
+  const int32_t* offsets;   // grouped: [E + 1] device; nullptr: one weight for every row
+  void* Y;                  // [M, N] (or [M, N/2] for the SiLU-gate form)
+  int E, x_type, s_type, y_type, silu;
+};
+hipError_t launch_int4_gemv(const Int4GemvArgs& a, hipStream_t s);
+
+// tokens to expert order and back: row_of[t k + j] is the row of entry (t, j), none outside [0, R)
+struct PermuteArgs {
+  int64_t T, D, R;
+  int k, a_type, b_type;
+  const int32_t* row_of;    // [T k]
+  const float* w;           // [T k] or nullptr (every weight 1)
+  const void* A;            // token side [T, D]: scatter's input; gather: only for dw
+  const void* B;            // row side [R, D]: gather's input; scatter: only for dw
+  void* A_out;              // gather's output
+  void* B_out;              // scatter's output
+  float* dw;                // [T k] or nullptr: <A[t], B[row]> of every entry, 0 without a row
+};
+hipError_t launch_moe_scatter(const PermuteArgs& a, hipStream_t s);
+hipError_t launch_moe_gather(const PermuteArgs& a, hipStream_t s);
+
 // calibration: register-resident matrix ops on random operands (cu_count() * waves_per_simd
 // workgroups of 256 threads; sink holds one float per thread)
 hipError_t launch_mfma_probe(int kind, int waves_per_simd, int iters, uint32_t seed, float* sink, hipStream_t s);
