@@ -492,6 +492,9 @@ int check_scales(const char* fn, const uint16_t* scales) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
+// the products address 16 weight rows with 32-bit byte offsets
+constexpr int64_t kMaxInt4K = (int64_t)1 << 20;
+
 int gemv_int4_common(const char* fn, ssn::Int4GemvArgs a, void* stream) {
   int st;
   if ((st = check_nk(fn, a.N, a.K))) return st;
@@ -503,6 +506,7 @@ int gemv_int4_common(const char* fn, ssn::Int4GemvArgs a, void* stream) {
     return st;
   if (a.M == 0 || a.N == 0) return ok();
   if (a.K == 0) return fail(SSN_E_SHAPE, "%s: K must be positive when Y has elements", fn);
+  if (a.K > kMaxInt4K) return fail(SSN_E_SHAPE, "%s: K=%lld beyond %lld", fn, (long long)a.K, (long long)kMaxInt4K);
   if (a.x_rows == 0) return fail(SSN_E_SHAPE, "%s: x_rows must be positive when Y has rows", fn);
   if (a.N * (a.K / 2) > ((int64_t)1 << 40) / a.E) return fail(SSN_E_SHAPE, "%s: weights too large", fn);
   const void *X = a.X, *codes = a.codes, *Y = a.Y;
