@@ -342,72 +342,82 @@ __global__ __launch_bounds__(WAVES * 64) void k_int4_gemv(Int4GemvArgs a, int ng
 }
 
 // ---- up to 16 rows of Y: activations stay in registers
-// One workgroup of W waves serves one set of up to 16 rows of Y and walks over units of 16 weight rows. Wave
-// w owns chunks [nch w / W, nch (w + 1) / W) of K, at most C of them, and keeps their activations as
-// operands in registers for its whole life, so that the loop reads only weights. Codes, scales and
+// One workgroup of W waves serves one set of up to 16 / P rows of Y and walks over units of 16 weight
+// rows. Wave w owns chunks [nch w / W, nch (w + 1) / W) of K, at most C of them, and keeps their activations
+// as operands in registers for its whole life, so that the loop reads only weights. Codes, scales and
 // zero points come through buffer resources set to the unit's rows: what lies outside (rows past the
-// last, k past the end, the chunk that a wave has not, the unit after the last) reads as zero without a
+// last, k past the end, a chunk that the wave has not, the unit after the last) reads as zero without a
 // branch and without traffic, and adds nothing. D units are in flight; a chunk's registers are refilled
-// as soon as its codes are decoded. FOLD: steps of 32 k that share a scale (4: groups of a multiple of
-// 128, whose chunks need no transposition, and whose sums of x are formed once).
+// as soon as its codes are decoded.
+//
+// A span is FOLD steps of 32 k that share a scale (4: groups of a multiple of 128, whose chunks need no
+// transposition). With few rows of Y the operand's 16 rows hold P spans of 16 / P rows each: row block p
+// of pack j is span P j + p. Every span's codes multiply the whole operand, and of the result only the
+// row block of that span is kept, which lies in its own lanes, where one fold serves P spans.
+// The activations then take 1 / P of the registers.
 constexpr uint32_t kOutside = 0x80000000u;   // a byte offset past the end of every resource
 
 template <int C, int FOLD>
 struct UnitLoads {
+  static constexpr int kScales = (4 * C / FOLD + 3) / 4;
   u32x4 w[C];
-  // lane group g: the scale and zero point of chunk g (FOLD 4), or of step g of the chunk
-  uint32_t s[FOLD == 4 ? 1 : C], z[FOLD == 4 ? 1 : C];
+  uint32_t s[kScales], z[kScales];           // four spans, one per lane group
 };
 
-template <bool F16X, int C, int FOLD, int D, bool SILU>
-__global__ __launch_bounds__(1024) void k_int4_rows16(Int4GemvArgs a, int tiles, int per_slot) {
-  static_assert(C <= 4, "the scales of a wave's chunks share a register across four lane groups");
+template <bool F16X, int P, int C, int FOLD, int D, bool SILU>
+__global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, int per_slot) {
   constexpr int H = SILU ? 2 : 1;             // units per tile of 16 outputs: gate and up
-  constexpr int SC = FOLD == 4 ? 1 : C;
+  constexpr int SPANS = 4 * C / FOLD, PACKS = SPANS / P, ROWS = 16 / P;
+  static_assert(SPANS % P == 0, "whole packs");
+  using Loads = UnitLoads<C, FOLD>;
   // whether the sums of x stay in registers too, or are formed again for every unit (one more matrix
   // instruction per step: the matrix cores have the time, the registers are full)
-  constexpr bool KEEP = FOLD == 4 && C <= (SILU ? 2 : 3);
-  extern __shared__ f32x4 red[];              // [2][W][H][64]
+  constexpr bool KEEP = PACKS <= (SILU ? 2 : 3);
+  extern __shared__ f32x4 red[];              // [2][W][H][4 ROWS]
   const int W = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
   const int No = (int)(SILU ? a.N / 2 : a.N);
   const int K = (int)a.K, nch = (K + kChunk - 1) / kChunk, g32 = (int)(a.group / 32), groups = (int)a.groups;
   const int c_lo = nch * wave / W, nc = nch * (wave + 1) / W - c_lo;
+  const int k_end = min(K, kChunk * (c_lo + nc));
   const int slot = blockIdx.x / per_slot;
-  int e = 0, r0 = 16 * slot, cnt = (int)min(a.M - r0, (int64_t)16);
+  int e = 0, r0 = ROWS * slot, cnt = (int)min(a.M - r0, (int64_t)ROWS);
   if (a.offsets) {
-    if (!find_slot(a.offsets, a.E, (int)a.M, slot, 16, e, r0, cnt)) return;
+    if (!find_slot(a.offsets, a.E, (int)a.M, slot, ROWS, e, r0, cnt)) return;
     e = __builtin_amdgcn_readfirstlane(e);
     r0 = __builtin_amdgcn_readfirstlane(r0);
     cnt = __builtin_amdgcn_readfirstlane(cnt);
   }
+  // the first k of a span of the wave
+  auto span_k = [&](int u) { return kChunk * c_lo + 32 * FOLD * u; };
   // where this lane's codes, scales and zero points lie in its row of a unit: the same for every unit
-  uint32_t koff[C], goff[SC];
+  uint32_t koff[C], goff[Loads::kScales];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int k = kChunk * (c_lo + c) + 32 * kq;
-    koff[c] = c < nc && k < K ? (uint32_t)(r16 * (K / 2) + k / 2) : kOutside;
+    koff[c] = k < k_end ? (uint32_t)(r16 * (K / 2) + k / 2) : kOutside;
   }
 #pragma unroll
-  for (int c = 0; c < SC; ++c) {
-    const int k32 = FOLD == 4 ? 4 * (c_lo + kq) : 4 * (c_lo + c) + kq;
-    goff[c] = (FOLD == 4 ? kq : c) < nc && 32 * k32 < K ? (uint32_t)(r16 * groups + k32 / g32) : kOutside / 2;
+  for (int i = 0; i < Loads::kScales; ++i) {
+    // lane group g loads span 4 i + g; with P = 2, groups 1 and 2 change places, for the swap that follows
+    const int u = 4 * i + (P == 2 ? (kq >> 1) | (kq & 1) << 1 : kq), k = span_k(u);
+    goff[i] = u < SPANS && k < k_end ? (uint32_t)(r16 * groups + k / 32 / g32) : kOutside / 2;
   }
   const uint32_t z_add = a.zeros ? 0u : 8u;
-  auto load_unit = [&](UnitLoads<C, FOLD>& o, int tile, int half, int c) __attribute__((always_inline)) {
+  auto load_unit = [&](Loads& o, int tile, int half, int c) __attribute__((always_inline)) {
     const int rows = tile < tiles ? min(16, No - 16 * tile) : 0;
     const int64_t row = (int64_t)e * a.N + (int64_t)half * No + 16 * tile;
     const auto wr = buf_rsrc(a.codes + row * (K / 2), rows * (K / 2));
     o.w[c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, koff[c], 0, 0));
-    if (FOLD != 4 || c == 0) {
+    if (c % FOLD == 0) {                      // the chunk whose first span starts scale register c / FOLD
       const auto sr = buf_rsrc(a.scales + row * groups, rows * groups * 2);
       const auto zr = buf_rsrc(a.zeros + row * groups, a.zeros ? rows * groups : 0);
-      o.s[c] = __builtin_amdgcn_raw_buffer_load_b16(sr, 2 * goff[c], 0, 0);
-      o.z[c] = __builtin_amdgcn_raw_buffer_load_b8(zr, goff[c], 0, 0);
+      o.s[c / FOLD] = __builtin_amdgcn_raw_buffer_load_b16(sr, 2 * goff[c / FOLD], 0, 0);
+      o.z[c / FOLD] = __builtin_amdgcn_raw_buffer_load_b8(zr, goff[c / FOLD], 0, 0);
     }
   };
-  UnitLoads<C, FOLD> buf[D];
+  Loads buf[D];
   int tile = blockIdx.x - slot * per_slot;
 #pragma unroll
   for (int d = 0; d < D; ++d)
@@ -418,60 +428,85 @@ __global__ __launch_bounds__(1024) void k_int4_rows16(Int4GemvArgs a, int tiles,
   const uint32_t one = F16X ? 0x3C003C00u : 0x3F803F80u;
   u32x4 ones = {one, one, one, one};
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
-  u32x4 x[C][4];
-  f32x4 xs[KEEP ? C : 1];
+  u32x4 x[PACKS][FOLD];
+  f32x4 xs[KEEP ? PACKS : 1];
   {
-    int64_t src = r0 + min(r16, cnt - 1);
+    int64_t src = r0 + min(r16 % ROWS, cnt - 1);
     if (a.offsets) src = min(max(a.row_token ? (int64_t)a.row_token[src] : src, (int64_t)0), a.x_rows - 1);
     const uint16_t* xp = (const uint16_t*)a.X + src * K;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int j = 0; j < PACKS; ++j)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int k = kChunk * (c_lo + c) + (FOLD == 4 ? 32 * kq + 8 * s : 32 * s + 8 * kq);
-        const bool in = c < nc && k < K;
-        x[c][s] = *(const u32x4*)(xp + (in ? k : 0));
-        if (!in) x[c][s] = u32x4{0u, 0u, 0u, 0u};
+      for (int t = 0; t < FOLD; ++t) {
+        const int k = span_k(P * j + r16 / ROWS) + (FOLD == 4 ? 32 * kq + 8 * t : 32 * t + 8 * kq);
+        x[j][t] = *(const u32x4*)(xp + (k < k_end ? k : 0));
+        if (k >= k_end) x[j][t] = u32x4{0u, 0u, 0u, 0u};
       }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (KEEP) xs[c] = zero4;
+    for (int j = 0; j < PACKS; ++j) {
+      if (KEEP) xs[j] = zero4;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        x[c][s] = x_operand(x[c][s]);
-        if (KEEP) xs[c] = mfma16<F16X>(x[c][s], ones, xs[c]);
+      for (int t = 0; t < FOLD; ++t) {
+        x[j][t] = x_operand(x[j][t]);
+        if (KEEP) xs[j] = mfma16<F16X>(x[j][t], ones, xs[j]);
       }
     }
   }
 
   // multiplies the unit in b and refills b with the unit of (next, half) as its registers come free
-  auto work = [&](UnitLoads<C, FOLD>& b, int next, int half) __attribute__((always_inline)) -> f32x4 {
+  auto work = [&](Loads& b, int next, int half) __attribute__((always_inline)) -> f32x4 {
     f32x4 tot = zero4;
     if (!KEEP) asm volatile("" : "+v"(ones));   // or the compiler forms the sums once, and spills them
-    auto fold = [&](f32x4 acc, f32x4 sum, uint32_t sz) {
-      const float s = float16_of((uint16_t)(sz & 0xFFFFu), a.s_type), z = (float)(sz >> 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tot[i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[i], acc[i]), tot[i]);
-    };
-    u32x4 szs;
+    u32x4 szs = {};
+    f32x4 part[P];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (FOLD != 4 || c == 0) szs = spread4(b.s[c] | (b.z[c] + z_add) << 16);
-      u32x4 w = FOLD == 4 ? b.w[c] : transpose4(b.w[c]);
-      f32x4 acc = zero4, sum = zero4;
+      const u32x4 w = FOLD == 4 ? b.w[c] : transpose4(b.w[c]);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        acc = mfma16<F16X>(x[c][s], codes_operand<F16X>(w[s]), acc);
-        if (!KEEP) sum = mfma16<F16X>(x[c][s], ones, sum);
-        if ((s + 1) % FOLD == 0) {
-          fold(acc, KEEP ? xs[c] : sum, szs[FOLD == 4 ? c : s + 1 - FOLD]);
-          asm volatile("" : "+v"(tot));       // here, or every step's sums are held to the end
-          acc = sum = zero4;
+      for (int v = 0; v < 4 / FOLD; ++v) {
+        const int u = c * (4 / FOLD) + v, j = u / P;   // span and pack
+        if (u % 4 == 0) {
+          const uint32_t sz = b.s[u / 4] | (b.z[u / 4] + z_add) << 16;
+          if (P == 4) {
+            szs[0] = sz;
+          } else if (P == 2) {
+            const auto r = __builtin_amdgcn_permlane16_swap(sz, sz, false, false);
+            szs[0] = r[0];
+            szs[1] = r[1];
+          } else {
+            szs = spread4(sz);
+          }
         }
+        part[u % P] = zero4;
+#pragma unroll
+        for (int t = 0; t < FOLD; ++t)
+          part[u % P] = mfma16<F16X>(x[j][t], codes_operand<F16X>(w[FOLD * v + t]), part[u % P]);
+        if (u % P != P - 1) continue;
+        f32x4 sum = zero4;
+        if (KEEP) sum = xs[j];
+        else
+#pragma unroll
+          for (int t = 0; t < FOLD; ++t) sum = mfma16<F16X>(x[j][t], ones, sum);
+        const uint32_t sz = szs[P == 1 ? u % 4 : P == 2 ? u / 2 % 2 : 0];
+        const float s = float16_of((uint16_t)(sz & 0xFFFFu), a.s_type), z = (float)(sz >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float acc = part[0][i];
+          if (P == 2) acc = kq >= 2 ? part[P - 1][i] : acc;
+          if (P == 4) acc = kq == 0 ? acc : kq == 1 ? part[1 % P][i] : kq == 2 ? part[2 % P][i] : part[P - 1][i];
+          tot[i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[i], acc), tot[i]);
+        }
+        asm volatile("" : "+v"(tot));         // here, or every pack's sums are held to the end
       }
       __builtin_amdgcn_sched_barrier(0);      // the refill goes out here, not further down
       load_unit(b, next, half, c);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    // the row blocks' shares meet in the first
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (P >= 2) tot[i] += __shfl_xor(tot[i], 32, 64);
+      if (P == 4) tot[i] += __shfl_xor(tot[i], 16, 64);
     }
     return tot;
   };
@@ -479,22 +514,24 @@ __global__ __launch_bounds__(1024) void k_int4_rows16(Int4GemvArgs a, int tiles,
   // waves take turns at it
   int turn = 0;
   auto finish = [&](const f32x4* tot) __attribute__((always_inline)) {
-    f32x4* part = red + (turn & 1) * W * H * 64;
+    f32x4* part = red + (turn & 1) * W * H * 4 * ROWS;
     if (4 * kq < cnt)
 #pragma unroll
-      for (int h = 0; h < H; ++h) part[(wave * H + h) * 64 + lane] = tot[h];
+      for (int h = 0; h < H; ++h) part[(wave * H + h) * 4 * ROWS + lane] = tot[h];
     __builtin_amdgcn_s_waitcnt(0xC07F);       // the LDS writes; the loads under way stay so
     stage_barrier();
-    int o = (int)threadIdx.x - 256 * turn % (int)blockDim.x;
+    const int first = 64 * (turn * (ROWS / 4) % W);
+    int o = (int)threadIdx.x - first;
     if (o < 0) o += blockDim.x;
-    const int n16 = o & 15, m = o >> 4, n = 16 * tile + n16;
-    if (m < cnt && n < No) {
+    for (; o < 16 * ROWS; o += blockDim.x) {
+      const int n16 = o & 15, m = o >> 4, n = 16 * tile + n16;
+      if (m >= cnt || n >= No) continue;
       const float* p = (const float*)(part + 16 * (m >> 2) + n16) + (m & 3);
       float y = 0.f, u = 0.f;
 #pragma unroll 4
       for (int w = 0; w < W; ++w) {
-        y += p[w * H * 256];
-        if (SILU) u += p[(w * H + 1) * 256];
+        y += p[w * H * 16 * ROWS];
+        if (SILU) u += p[(w * H + 1) * 16 * ROWS];
       }
       if (SILU) y = silu(y) * u;
       store_elem(a.Y, a.y_type, (int64_t)(r0 + m) * No + n, y);
@@ -555,46 +592,60 @@ hipError_t launch_gemv_t(const Int4GemvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool F16X, int C, int FOLD, bool SILU>
-hipError_t launch_rows16_t(const Int4GemvArgs& a, int W, hipStream_t s) {
+#ifndef WG_CU
+#define WG_CU (16 / W > 0 ? 16 / W : 1)
+#endif
+#ifndef GP
+#define GP 4
+#endif
+#ifndef D4
+#define D4 2
+#endif
+#ifndef D2
+#define D2 1
+#endif
+template <bool F16X, int P, int C, int FOLD, int D, bool SILU>
+hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
+  constexpr int ROWS = 16 / P;
+  const int nch = (int)((a.K + kChunk - 1) / kChunk), W = (nch + C - 1) / C;
   const int64_t No = SILU ? a.N / 2 : a.N;
   const int tiles = (int)((No + 15) / 16);
-  const int64_t slots = a.offsets ? std::min<int64_t>(a.E, a.M) + a.M / 16 : 1;
-  const int64_t wgs = (int64_t)cu_count() * (16 / W) * (a.offsets ? 2 : 1);
+  const int64_t slots = a.offsets ? std::min<int64_t>(a.E, a.M) + a.M / ROWS : 1;
+  const int64_t wgs = (int64_t)cu_count() * WG_CU * (a.offsets ? 2 : 1);
   const int per_slot = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, wgs / slots));
-  constexpr int D = C <= 3 ? 2 : 1;
-  hipLaunchKernelGGL((k_int4_rows16<F16X, C, FOLD, D, SILU>), dim3((unsigned)(slots * per_slot)), dim3(W * 64),
-                     2 * W * (SILU ? 2 : 1) * 1024, s, a, tiles, per_slot);
+  hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, SILU>), dim3((unsigned)(slots * per_slot)), dim3(W * 64),
+                     2 * W * (SILU ? 2 : 1) * 4 * ROWS * 16, s, a, tiles, per_slot);
   return hipGetLastError();
 }
 
 template <bool F16X, int FOLD, bool SILU>
-hipError_t launch_rows16_c(const Int4GemvArgs& a, hipStream_t s) {
+hipError_t launch_rows_c(const Int4GemvArgs& a, hipStream_t s) {
   const int nch = (int)((a.K + kChunk - 1) / kChunk);
-  const int W = nch <= 8 ? 4 : nch <= 16 ? 8 : 16;
-  switch ((nch + W - 1) / W) {
-    case 1: return launch_rows16_t<F16X, 1, FOLD, SILU>(a, W, s);
-    case 2: return launch_rows16_t<F16X, 2, FOLD, SILU>(a, W, s);
-    case 3: return launch_rows16_t<F16X, 3, FOLD, SILU>(a, W, s);
-    default: return launch_rows16_t<F16X, 4, FOLD, SILU>(a, W, s);
+  if (a.M <= 4 || (a.offsets && GP == 4)) {
+    if (nch <= 64) return launch_rows_t<F16X, 4, 4, FOLD, D4, SILU>(a, s);
+    return launch_rows_t<F16X, 4, 8, FOLD, 1, SILU>(a, s);
   }
+  if (a.M <= 8 || (a.offsets && GP == 2)) return launch_rows_t<F16X, 2, 4, FOLD, D2, SILU>(a, s);
+  if (nch <= 32) return launch_rows_t<F16X, 1, 2, FOLD, 2, SILU>(a, s);
+  if (nch <= 48) return launch_rows_t<F16X, 1, 3, FOLD, 2, SILU>(a, s);
+  return launch_rows_t<F16X, 1, 4, FOLD, 1, SILU>(a, s);
 }
 
 template <bool F16X, int FOLD>
-hipError_t launch_rows16_s(const Int4GemvArgs& a, hipStream_t s) {
-  return a.silu ? launch_rows16_c<F16X, FOLD, true>(a, s) : launch_rows16_c<F16X, FOLD, false>(a, s);
+hipError_t launch_rows_s(const Int4GemvArgs& a, hipStream_t s) {
+  return a.silu ? launch_rows_c<F16X, FOLD, true>(a, s) : launch_rows_c<F16X, FOLD, false>(a, s);
 }
 
 template <bool F16X>
-hipError_t launch_rows16(const Int4GemvArgs& a, hipStream_t s) {
-  if (a.group % 128 == 0) return launch_rows16_s<F16X, 4>(a, s);
-  return a.group % 64 == 0 ? launch_rows16_s<F16X, 2>(a, s) : launch_rows16_s<F16X, 1>(a, s);
+hipError_t launch_rows(const Int4GemvArgs& a, hipStream_t s) {
+  if (a.group % 128 == 0) return launch_rows_s<F16X, 4>(a, s);
+  return a.group % 64 == 0 ? launch_rows_s<F16X, 2>(a, s) : launch_rows_s<F16X, 1>(a, s);
 }
 
 template <bool F16X, bool FINE>
 hipError_t launch_gemv_x(const Int4GemvArgs& a, hipStream_t s) {
-  const bool fits = a.K <= 64 * kChunk;
-  if (fits && (a.offsets || a.M <= 16)) return launch_rows16<F16X>(a, s);
+  const bool fits = a.K <= 64 * kChunk || (a.M <= 4 && a.K <= 128 * kChunk);
+  if (fits && (a.offsets || a.M <= 16)) return launch_rows<F16X>(a, s);
   if (a.offsets) return launch_gemv_t<F16X, 1, 2, 8, FINE, true>(a, s);
   if (a.M <= 16) return launch_gemv_t<F16X, 1, 2, 8, FINE, false>(a, s);
   if (a.M <= 32) return launch_gemv_t<F16X, 2, 2, 8, FINE, false>(a, s);
