@@ -141,50 +141,93 @@ __device__ __forceinline__ u32x4 spread4(uint32_t v) {
   return u32x4{b[0], b[1], c[0], c[1]};
 }
 
+// the sum of the two halves of the wave (of the two 16-lane groups of each half), in every lane
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_quarters(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// a where the mask's bits are set, else b (v_bfi_b32, where a conditional may become a branch)
+__device__ __forceinline__ float choose(uint32_t mask, float a, float b) {
+  return __uint_as_float((mask & __float_as_uint(a)) | (~mask & __float_as_uint(b)));
+}
+
 // silu(g) = g / (1 + exp(-g)) on the base-2 exponential and the reciprocal of the hardware; exp(-g) = inf
 // gives -0, exp(-g) = 0 gives g.
 __device__ __forceinline__ float silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-g * 1.44269504088896341f));
 }
 
-// The expert of the 16-row slot `slot` (slots of the experts in order, ceil(rows / 16) each), its first
-// row and its row count; false past the last slot. All threads of the workgroup take part.
-__device__ __forceinline__ bool find_slot(const int32_t* __restrict__ off, int E, int R, int slot, int rows_per_slot,
-                                          int& e_out, int& r0_out, int& cnt_out) {
-  __shared__ int waves[16], found[3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (E + (int)blockDim.x - 1) / (int)blockDim.x;
-  const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
-  int n = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int a = min(max(off[e], 0), R), b = min(max(off[e + 1], a), R);
-    n += (b - a + rows_per_slot - 1) / rows_per_slot;
-  }
-  int inc = n;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(inc, d, 64);
-    if (lane >= d) inc += v;
-  }
-  if (tid == 0) found[2] = 0;
-  if (lane == 63) waves[wave] = inc;
-  __syncthreads();
-  int first = inc - n;
-  for (int w = 0; w < wave; ++w) first += waves[w];
-  if (slot >= first && slot < first + n) {
-    for (int e = e0; e < e1; ++e) {
-      const int a = min(max(off[e], 0), R), b = min(max(off[e + 1], a), R);
-      const int m = (b - a + rows_per_slot - 1) / rows_per_slot;
-      if (slot < first + m) {
-        const int r0 = a + rows_per_slot * (slot - first);
-        found[0] = e; found[1] = r0; found[2] = min(rows_per_slot, b - r0);
-        break;
-      }
-      first += m;
+// Inclusive sum over the wave's lanes (row_shr 1, 2, 4, 8 inside the rows of 16 lanes, then row_bcast 15 and
+// 31 across them).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// What a workgroup of a grouped product does. The experts' rows, at most `rows` at a time, are slots in
+// the experts' order; the grid's workgroups are dealt out evenly to the slots that there are, which only
+// the device knows: workgroup b takes part `part` of the `parts` that share its slot. Every wave finds this for itself
+// from the offsets, without a barrier; the results are uniform.
+struct Slot {
+  int e, r0, cnt, part, parts;
+};
+__device__ __forceinline__ bool find_slot(const int32_t* __restrict__ off, int E, int R, int rows, int max_parts,
+                                          Slot& out) {
+  constexpr int kBatch = 8;                   // offsets per lane at a time: one round up to 512 experts
+  const int lane = threadIdx.x & 63;
+  int total = 0, lo[kBatch], hi[kBatch], inc[kBatch];
+  auto scan = [&](int e0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = min(e0 + 64 * i + lane, E);
+      lo[i] = off[e];
+      hi[i] = off[min(e + 1, E)];
     }
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      lo[i] = min(max(lo[i], 0), R);
+      hi[i] = min(max(hi[i], lo[i]), R);
+      inc[i] = sum + wave_scan((hi[i] - lo[i] + rows - 1) / rows);
+      sum = __builtin_amdgcn_readlane(inc[i], 63);
+    }
+    return sum;
+  };
+  const int rounds = (E + 64 * kBatch - 1) / (64 * kBatch);
+  for (int i = 0; i < rounds; ++i) total += scan(64 * kBatch * i);
+  if (total == 0) return false;
+  out.parts = max(1, min((int)gridDim.x / total, max_parts));
+  int slot = blockIdx.x / out.parts;
+  out.part = blockIdx.x - slot * out.parts;
+  if (slot >= total) return false;
+  for (int i = 0; i < rounds; ++i) {
+    if (rounds > 1) total = scan(64 * kBatch * i);
+    if (slot < total) {
+      for (int j = 0; j < kBatch; ++j) {
+        const unsigned long long beyond = __ballot(inc[j] > slot);
+        if (!beyond) continue;
+        const int l = __builtin_ctzll(beyond);
+        const int a = __builtin_amdgcn_readlane(lo[j], l), b = __builtin_amdgcn_readlane(hi[j], l);
+        const int left = __builtin_amdgcn_readlane(inc[j], l) - slot;   // this slot and the expert's slots behind it
+        out.e = 64 * (kBatch * i + j) + l;
+        out.r0 = a + rows * ((b - a + rows - 1) / rows - left);
+        out.cnt = min(rows, b - out.r0);
+        return true;
+      }
+    }
+    slot -= total;
   }
-  __syncthreads();
-  e_out = found[0]; r0_out = found[1]; cnt_out = found[2];
-  return cnt_out > 0;
+  return false;
 }
 
 constexpr int kChunk = 128;   // k per step of a wave's loop
@@ -206,12 +249,16 @@ __global__ __launch_bounds__(WAVES * 64) void k_int4_gemv(Int4GemvArgs a, int ng
   const int nch = (int)((a.K + kChunk - 1) / kChunk);
   const int c_lo = nch * wave / WAVES, c_hi = nch * (wave + 1) / WAVES;
   const int g32 = (int)(a.group / 32);
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  int e = 0, r0 = 0, cnt = 0;
+  int64_t item = blockIdx.x, step = gridDim.x;
+  if constexpr (GROUPED) {
+    Slot sl;
+    if (!find_slot(a.offsets, a.E, (int)a.M, kRows, ngroups, sl)) return;
+    e = sl.e; r0 = sl.r0; cnt = sl.cnt; item = sl.part; step = sl.parts;
+  }
+  for (; item < items; item += step) {
     const int ng = (int)(item % ngroups);
-    int e = 0, r0, cnt;
-    if constexpr (GROUPED) {
-      if (!find_slot(a.offsets, a.E, (int)a.M, (int)(item / ngroups), kRows, e, r0, cnt)) return;
-    } else {
+    if constexpr (!GROUPED) {
       r0 = (int)(item / ngroups) * kRows;
       cnt = (int)min(a.M - r0, (int64_t)kRows);
     }
@@ -364,8 +411,8 @@ struct UnitLoads {
   uint32_t s[kScales], z[kScales];           // four spans, one per lane group
 };
 
-template <bool F16X, int P, int C, int FOLD, int D, bool SILU>
-__global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, int per_slot) {
+template <bool F16X, int P, int C, int FOLD, int D, bool GROUPED, bool SILU>
+__global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles) {
   constexpr int H = SILU ? 2 : 1;             // units per tile of 16 outputs: gate and up
   constexpr int SPANS = 4 * C / FOLD, PACKS = SPANS / P, ROWS = 16 / P;
   static_assert(SPANS % P == 0, "whole packs");
@@ -373,7 +420,7 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
   // whether the sums of x stay in registers too, or are formed again for every unit (one more matrix
   // instruction per step: the matrix cores have the time, the registers are full)
   constexpr bool KEEP = PACKS <= (SILU ? 2 : 3);
-  extern __shared__ f32x4 red[];              // [2][W][H][4 ROWS]
+  extern __shared__ f32x4 red[];              // [2][W][H][4 ROWS]: the waves' shares
   const int W = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
@@ -381,16 +428,21 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
   const int K = (int)a.K, nch = (K + kChunk - 1) / kChunk, g32 = (int)(a.group / 32), groups = (int)a.groups;
   const int c_lo = nch * wave / W, nc = nch * (wave + 1) / W - c_lo;
   const int k_end = min(K, kChunk * (c_lo + nc));
-  const int slot = blockIdx.x / per_slot;
-  int e = 0, r0 = ROWS * slot, cnt = (int)min(a.M - r0, (int64_t)ROWS);
-  if (a.offsets) {
-    if (!find_slot(a.offsets, a.E, (int)a.M, slot, ROWS, e, r0, cnt)) return;
-    e = __builtin_amdgcn_readfirstlane(e);
-    r0 = __builtin_amdgcn_readfirstlane(r0);
-    cnt = __builtin_amdgcn_readfirstlane(cnt);
+  int e = 0, r0 = 0, cnt = (int)a.M, tile = blockIdx.x, stride = gridDim.x;
+  // this lane's row of X; rows past the last are copies of it, whose sums are dropped
+  int src;
+  if constexpr (GROUPED) {
+    Slot sl;
+    if (!find_slot(a.offsets, a.E, (int)a.M, ROWS, tiles, sl)) return;
+    e = sl.e; r0 = sl.r0; cnt = sl.cnt; tile = sl.part; stride = sl.parts;
+    src = r0 + min(r16 % ROWS, cnt - 1);
+    if (a.row_token) src = a.row_token[src];
+  } else {
+    src = min(r16 % ROWS, cnt - 1);
   }
   // the first k of a span of the wave
   auto span_k = [&](int u) { return kChunk * c_lo + 32 * FOLD * u; };
+  const uint32_t kq_0 = kq & 1 ? ~0u : 0u, kq_1 = kq & 2 ? ~0u : 0u;
   // where this lane's codes, scales and zero points lie in its row of a unit: the same for every unit
   uint32_t koff[C], goff[Loads::kScales];
 #pragma unroll
@@ -417,39 +469,41 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
       o.z[c / FOLD] = __builtin_amdgcn_raw_buffer_load_b8(zr, goff[c / FOLD], 0, 0);
     }
   };
-  Loads buf[D];
-  int tile = blockIdx.x - slot * per_slot;
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-#pragma unroll
-    for (int c = 0; c < C; ++c) load_unit(buf[d], tile + (d / H) * per_slot, d % H, c);
-
-  // the activations; zeros where the wave has no k
+  // The activations, zeros where the wave has no k. Without experts their loads go out first: they come
+  // from the L2, and are put in order while the first weights are on their way. With experts they wait for
+  // the row's token, and the weights do not.
   const uint32_t one = F16X ? 0x3C003C00u : 0x3F803F80u;
   u32x4 ones = {one, one, one, one};
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
   u32x4 x[PACKS][FOLD];
-  f32x4 xs[KEEP ? PACKS : 1];
-  {
-    int64_t src = r0 + min(r16 % ROWS, cnt - 1);
-    if (a.offsets) src = min(max(a.row_token ? (int64_t)a.row_token[src] : src, (int64_t)0), a.x_rows - 1);
-    const uint16_t* xp = (const uint16_t*)a.X + src * K;
+  Loads buf[D];
+  auto x_k = [&](int j, int t) {
+    return span_k(P * j + r16 / ROWS) + (FOLD == 4 ? 32 * kq + 8 * t : 32 * t + 8 * kq);
+  };
+  auto load_x = [&]() __attribute__((always_inline)) {
+    if (GROUPED) src = min(max(src, 0), (int)a.x_rows - 1);
+    const uint16_t* const xp = (const uint16_t*)a.X + (int64_t)src * K;
 #pragma unroll
     for (int j = 0; j < PACKS; ++j)
 #pragma unroll
-      for (int t = 0; t < FOLD; ++t) {
-        const int k = span_k(P * j + r16 / ROWS) + (FOLD == 4 ? 32 * kq + 8 * t : 32 * t + 8 * kq);
-        x[j][t] = *(const u32x4*)(xp + (k < k_end ? k : 0));
-        if (k >= k_end) x[j][t] = u32x4{0u, 0u, 0u, 0u};
-      }
+      for (int t = 0; t < FOLD; ++t) x[j][t] = *(const u32x4*)(xp + (x_k(j, t) < k_end ? x_k(j, t) : 0));
+  };
+  if (!GROUPED) load_x();
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < PACKS; ++j) {
-      if (KEEP) xs[j] = zero4;
+  for (int d = 0; d < D; ++d)
 #pragma unroll
-      for (int t = 0; t < FOLD; ++t) {
-        x[j][t] = x_operand(x[j][t]);
-        if (KEEP) xs[j] = mfma16<F16X>(x[j][t], ones, xs[j]);
-      }
+    for (int c = 0; c < C; ++c) load_unit(buf[d], tile + (d / H) * stride, d % H, c);
+  __builtin_amdgcn_sched_barrier(0);
+  if (GROUPED) load_x();
+  f32x4 xs[KEEP ? PACKS : 1];
+#pragma unroll
+  for (int j = 0; j < PACKS; ++j) {
+    if (KEEP) xs[j] = zero4;
+#pragma unroll
+    for (int t = 0; t < FOLD; ++t) {
+      x[j][t] = x_k(j, t) < k_end ? x_operand(x[j][t]) : u32x4{0u, 0u, 0u, 0u};
+      if (KEEP) xs[j] = mfma16<F16X>(x[j][t], ones, xs[j]);
     }
   }
 
@@ -491,9 +545,10 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
         const float s = float16_of((uint16_t)(sz & 0xFFFFu), a.s_type), z = (float)(sz >> 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          // the row block's own span: lanes choose by the bits of their group
           float acc = part[0][i];
-          if (P == 2) acc = kq >= 2 ? part[P - 1][i] : acc;
-          if (P == 4) acc = kq == 0 ? acc : kq == 1 ? part[1 % P][i] : kq == 2 ? part[2 % P][i] : part[P - 1][i];
+          if (P == 2) acc = choose(kq_1, part[P - 1][i], acc);
+          if (P == 4) acc = choose(kq_1, choose(kq_0, part[P - 1][i], part[2 % P][i]), choose(kq_0, part[1 % P][i], acc));
           tot[i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[i], acc), tot[i]);
         }
         asm volatile("" : "+v"(tot));         // here, or every pack's sums are held to the end
@@ -505,27 +560,36 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
     // the row blocks' shares meet in the first
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (P >= 2) tot[i] += __shfl_xor(tot[i], 32, 64);
-      if (P == 4) tot[i] += __shfl_xor(tot[i], 16, 64);
+      if (P >= 2) tot[i] = sum_halves(tot[i]);
+      if (P == 4) tot[i] = sum_quarters(tot[i]);
     }
     return tot;
   };
-  // the waves' shares of K meet in LDS (two buffers, one barrier per tile), one thread per output; the
-  // waves take turns at it
+  // The waves' shares of K meet in LDS (two buffers, one barrier per tile), one thread per output, the waves
+  // taking turns at it. A single wave stores what it holds.
+  auto store = [&](int m, int n16, float y, float u) {
+    const int n = 16 * tile + n16;
+    if (SILU) y = silu(y) * u;
+    if (m < cnt && n < No) store_elem(a.Y, a.y_type, (int64_t)(r0 + m) * No + n, y);
+  };
   int turn = 0;
   auto finish = [&](const f32x4* tot) __attribute__((always_inline)) {
+    if (W == 1) {
+      if (4 * kq < ROWS)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store(4 * kq + i, r16, tot[0][i], tot[H - 1][i]);
+      return;
+    }
     f32x4* part = red + (turn & 1) * W * H * 4 * ROWS;
     if (4 * kq < cnt)
 #pragma unroll
       for (int h = 0; h < H; ++h) part[(wave * H + h) * 4 * ROWS + lane] = tot[h];
     __builtin_amdgcn_s_waitcnt(0xC07F);       // the LDS writes; the loads under way stay so
     stage_barrier();
-    const int first = 64 * (turn * (ROWS / 4) % W);
-    int o = (int)threadIdx.x - first;
+    int o = (int)threadIdx.x - 64 * (turn * (ROWS / 4) % W);
     if (o < 0) o += blockDim.x;
-    for (; o < 16 * ROWS; o += blockDim.x) {
-      const int n16 = o & 15, m = o >> 4, n = 16 * tile + n16;
-      if (m >= cnt || n >= No) continue;
+    for (; o < 16 * cnt; o += blockDim.x) {
+      const int n16 = o & 15, m = o >> 4;
       const float* p = (const float*)(part + 16 * (m >> 2) + n16) + (m & 3);
       float y = 0.f, u = 0.f;
 #pragma unroll 4
@@ -533,24 +597,23 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles, i
         y += p[w * H * 16 * ROWS];
         if (SILU) u += p[(w * H + 1) * 16 * ROWS];
       }
-      if (SILU) y = silu(y) * u;
-      store_elem(a.Y, a.y_type, (int64_t)(r0 + m) * No + n, y);
+      store(m, n16, y, u);
     }
     ++turn;
   };
   for (;;) {
     f32x4 tot[2];
     if constexpr (SILU) {
-      tot[0] = work(buf[0], D == 1 ? tile : tile + per_slot, D == 1 ? 1 : 0);
-      tot[1] = work(buf[D - 1], tile + per_slot, D == 1 ? 0 : 1);
+      tot[0] = work(buf[0], D == 1 ? tile : tile + stride, D == 1 ? 1 : 0);
+      tot[1] = work(buf[D - 1], tile + stride, D == 1 ? 0 : 1);
       finish(tot);
-      if ((tile += per_slot) >= tiles) return;
+      if ((tile += stride) >= tiles) return;
     } else {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        tot[0] = work(buf[d], tile + D * per_slot, 0);
+        tot[0] = work(buf[d], tile + D * stride, 0);
         finish(tot);
-        if ((tile += per_slot) >= tiles) return;
+        if ((tile += stride) >= tiles) return;
       }
     }
   }
@@ -583,12 +646,11 @@ hipError_t launch_gemv_t(const Int4GemvArgs& a, hipStream_t s) {
   constexpr int kRows = 16 * MT;
   const int64_t No = a.silu ? a.N / 2 : a.N, per = a.silu ? 16 : 16 * NT;
   const int ngroups = (int)((No + per - 1) / per);
-  // grouped: at most one partly filled slot per expert that has rows
-  const int64_t slots = GROUPED ? std::min<int64_t>(a.E, a.M) + a.M / kRows : (a.M + kRows - 1) / kRows;
-  const int64_t items = slots * ngroups;
+  const int64_t items = GROUPED ? ngroups : (a.M + kRows - 1) / kRows * ngroups;
+  const int64_t grid = GROUPED ? std::max<int64_t>(4 * cu_count(), std::min<int64_t>(a.E, a.M) + a.M / kRows) : items;
   constexpr int kRing = MT == 1 ? 3 : MT == 2 ? 2 : 1;
   hipLaunchKernelGGL((k_int4_gemv<F16X, MT, NT, WAVES, FINE, GROUPED, kRing>),
-                     dim3((unsigned)std::min<int64_t>(items, 1 << 22)), dim3(WAVES * 64), 0, s, a, ngroups, items);
+                     dim3((unsigned)std::min<int64_t>(grid, GROUPED ? grid : 1 << 22)), dim3(WAVES * 64), 0, s, a, ngroups, items);
   return hipGetLastError();
 }
 
@@ -596,44 +658,49 @@ hipError_t launch_gemv_t(const Int4GemvArgs& a, hipStream_t s) {
 #define WG_CU (16 / W > 0 ? 16 / W : 1)
 #endif
 #ifndef GP
-#define GP 4
+#define GP 2
 #endif
 #ifndef D4
-#define D4 2
+#define D4 1
 #endif
 #ifndef D2
 #define D2 1
 #endif
-template <bool F16X, int P, int C, int FOLD, int D, bool SILU>
+template <bool F16X, int P, int C, int FOLD, int D, bool GROUPED, bool SILU>
 hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
   constexpr int ROWS = 16 / P;
   const int nch = (int)((a.K + kChunk - 1) / kChunk), W = (nch + C - 1) / C;
   const int64_t No = SILU ? a.N / 2 : a.N;
   const int tiles = (int)((No + 15) / 16);
-  const int64_t slots = a.offsets ? std::min<int64_t>(a.E, a.M) + a.M / ROWS : 1;
-  const int64_t wgs = (int64_t)cu_count() * WG_CU * (a.offsets ? 2 : 1);
-  const int per_slot = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, wgs / slots));
-  hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, SILU>), dim3((unsigned)(slots * per_slot)), dim3(W * 64),
-                     2 * W * (SILU ? 2 : 1) * 4 * ROWS * 16, s, a, tiles, per_slot);
+  const int64_t wgs = (int64_t)cu_count() * WG_CU;
+  // grouped: at least a workgroup for every slot that there may be (each expert's last may be partial)
+  const int64_t grid = GROUPED ? std::max<int64_t>(2 * wgs, std::min<int64_t>(a.E, a.M) + a.M / ROWS)
+                               : std::min<int64_t>(wgs, tiles);
+  hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, GROUPED, SILU>), dim3((unsigned)grid), dim3(W * 64),
+                     W == 1 ? 0 : 2 * W * (SILU ? 2 : 1) * 4 * ROWS * 16, s, a, tiles);
   return hipGetLastError();
 }
 
-template <bool F16X, int FOLD, bool SILU>
+template <bool F16X, int FOLD, bool GROUPED, bool SILU>
 hipError_t launch_rows_c(const Int4GemvArgs& a, hipStream_t s) {
   const int nch = (int)((a.K + kChunk - 1) / kChunk);
-  if (a.M <= 4 || (a.offsets && GP == 4)) {
-    if (nch <= 64) return launch_rows_t<F16X, 4, 4, FOLD, D4, SILU>(a, s);
-    return launch_rows_t<F16X, 4, 8, FOLD, 1, SILU>(a, s);
+  if (a.M <= 4 || (GROUPED && GP == 4)) {
+    if (nch <= 64) return launch_rows_t<F16X, 4, 4, FOLD, D4, GROUPED, SILU>(a, s);
+    return launch_rows_t<F16X, 4, 8, FOLD, 1, GROUPED, SILU>(a, s);
   }
-  if (a.M <= 8 || (a.offsets && GP == 2)) return launch_rows_t<F16X, 2, 4, FOLD, D2, SILU>(a, s);
-  if (nch <= 32) return launch_rows_t<F16X, 1, 2, FOLD, 2, SILU>(a, s);
-  if (nch <= 48) return launch_rows_t<F16X, 1, 3, FOLD, 2, SILU>(a, s);
-  return launch_rows_t<F16X, 1, 4, FOLD, 1, SILU>(a, s);
+  if (a.M <= 8 || (GROUPED && GP == 2)) return launch_rows_t<F16X, 2, 4, FOLD, D2, GROUPED, SILU>(a, s);
+  if constexpr (!GROUPED || GP == 1) {
+  if (nch <= 32) return launch_rows_t<F16X, 1, 2, FOLD, 2, GROUPED, SILU>(a, s);
+  if (nch <= 48) return launch_rows_t<F16X, 1, 3, FOLD, 2, GROUPED, SILU>(a, s);
+  return launch_rows_t<F16X, 1, 4, FOLD, 1, GROUPED, SILU>(a, s);
+  }
+  return hipSuccess;
 }
 
 template <bool F16X, int FOLD>
 hipError_t launch_rows_s(const Int4GemvArgs& a, hipStream_t s) {
-  return a.silu ? launch_rows_c<F16X, FOLD, true>(a, s) : launch_rows_c<F16X, FOLD, false>(a, s);
+  if (!a.offsets) return launch_rows_c<F16X, FOLD, false, false>(a, s);
+  return a.silu ? launch_rows_c<F16X, FOLD, true, true>(a, s) : launch_rows_c<F16X, FOLD, true, false>(a, s);
 }
 
 template <bool F16X>
