@@ -1,0 +1,262 @@
+// Integer 4-bit product for more rows of Y than k_int4.hip keeps in registers, or a longer K (the arithmetic
+// is in int4.hpp).
+//
+// One workgroup of eight waves computes 16 MT rows of Y for 16 NT weight rows; each wave takes an eighth
+// of K and keeps the whole tile's sums. Weights go straight to registers, one chunk ahead. The activations
+// of a chunk come through the wave's own LDS by direct loads, which need no registers and read each row's
+// 256 bytes together: they are read at the chunk's start and the next chunk's are sent for at once, to
+// arrive while this one is multiplied. No wave waits for another before the end, where the eight tiles of sums meet in the same
+// LDS, one thread per output.
+//
+// Every weight is decoded once and multiplied by MT operands; every operand of activations serves NT
+// tiles, so a workgroup reads 16 MT K activations from the L2 for 16 NT K weights.
+#include <algorithm>
+
+#include "device_once.hpp"
+#include "int4.hpp"
+
+namespace ssn {
+namespace {
+
+constexpr int kWaves = 8;
+
+template <bool F16X, int MT, int NT, int FOLD, bool GROUPED, bool SILU>
+__global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, int ngroups) {
+  constexpr int SPANS = 4 / FOLD, H = SILU ? 2 : 1;
+  constexpr int kLoads = NT * 3;              // loads to registers per chunk
+  // a wave's activations: 256 bytes per row, in 16 pieces, piece p of row r at place p ^ (r % 16), so that
+  // the 16 lanes that read one piece of 16 rows meet no bank twice
+  __shared__ __attribute__((aligned(1024))) char lds[kWaves][16 * MT][256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kq = lane >> 4;
+  const int No = (int)(a.N / H);
+  const int K = (int)a.K, nch = (K + kChunk - 1) / kChunk, g32 = (int)(a.group / 32), groups = (int)a.groups;
+  const int c_lo = nch * wave / kWaves, c_hi = nch * (wave + 1) / kWaves;
+  const uint32_t one = F16X ? 0x3C003C00u : 0x3F803F80u;
+  const u32x4 ones = {one, one, one, one};
+  const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t z_add = a.zeros ? 0u : 8u;
+
+  // Workgroups run over the sets of 16 MT rows (the grid's first axis, so that those that share weights run
+  // side by side) and over groups of weight rows; with experts, a workgroup has one set.
+  int e = 0, r0 = 16 * MT * blockIdx.x, cnt = 0, ng0 = blockIdx.y, ng_step = gridDim.y;
+  if constexpr (GROUPED) {
+    Slot sl;
+    if (!find_slot(a.offsets, a.E, (int)a.M, 16 * MT, ngroups, sl)) return;
+    e = sl.e; r0 = sl.r0; cnt = sl.cnt; ng0 = sl.part; ng_step = sl.parts;
+  }
+  for (int ng = ng0; ng < ngroups; ng += ng_step) {
+    if constexpr (!GROUPED) cnt = min((int)a.M - r0, 16 * MT);
+    // A direct load brings four rows' 256 bytes: lane l piece (l % 16) of row l / 16. Rows past the last come
+    // as zeros or stay what they were; their sums are dropped.
+    const int xrow = lane >> 4;
+    const char* xp[GROUPED ? 4 : 1];          // with experts: a pointer per row, else an offset from the first
+    uint32_t xo[GROUPED ? 1 : 4];
+    const auto xr = buf_rsrc((const uint16_t*)a.X + (GROUPED ? 0 : (int64_t)r0 * K), GROUPED ? 0 : cnt * K * 2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t piece = 16u * (uint32_t)(r16 ^ (4 * q + xrow));
+      if constexpr (GROUPED) {
+        const int m = r0 + min(4 * q + xrow, cnt - 1);
+        const int src = min(max(a.row_token ? a.row_token[m] : m, 0), (int)a.x_rows - 1);
+        xp[q] = (const char*)a.X + (int64_t)src * K * 2 + piece;
+      } else {
+        xo[q] = (uint32_t)(4 * q + xrow) * (uint32_t)K * 2u + piece;
+      }
+    }
+    // first row, and rows, of a tile: those of one expert, gate tiles before up tiles
+    auto tile_row = [&](int t) { return 16 * (SILU ? ng * (NT / H) + t % (NT / H) : ng * NT + t); };
+    struct Loads {
+      u32x4 w[NT];
+      uint32_t s[NT], z[NT];                  // lane group g: the scale of span g (FOLD 4: all the same)
+    };
+    auto load = [&](Loads& o, int c) __attribute__((always_inline)) {
+      const int k = kChunk * c + 32 * kq, ks = FOLD == 4 ? kChunk * c : kChunk * c + 32 * FOLD * kq;
+      const bool in = c < c_hi, in_s = in && kq < SPANS && ks < K;
+      const uint32_t ko = in && k < K ? (uint32_t)(r16 * (K / 2) + k / 2) : kOutside;
+      const uint32_t go = FOLD == 4 ? (in ? (uint32_t)(r16 * groups + ks / 32 / g32) : kOutside / 2)
+                                    : (in_s ? (uint32_t)(r16 * groups + ks / 32 / g32) : kOutside / 2);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int n0 = tile_row(t);
+        // (not max(0, min(..)): the compiler makes v_med3 of it, and a resource in vector registers)
+        const int rows = n0 < No ? min(16, No - n0) : 0;
+        const int64_t row = (int64_t)e * a.N + (SILU && t >= NT / H ? No : 0) + n0;
+        const auto wr = buf_rsrc(a.codes + row * (K / 2), rows * (K / 2));
+        const auto sr = buf_rsrc(a.scales + row * groups, rows * groups * 2);
+        const auto zr = buf_rsrc(a.zeros + row * groups, a.zeros ? rows * groups : 0);
+        o.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, ko, 0, 0));
+        o.s[t] = __builtin_amdgcn_raw_buffer_load_b16(sr, 2 * go, 0, 0);
+        o.z[t] = __builtin_amdgcn_raw_buffer_load_b8(zr, go, 0, 0);
+      }
+    };
+    auto send_x = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4 * MT; ++i) {
+        if constexpr (GROUPED) {
+          // a piece past the end of K: the row's first
+          const uint32_t k = (uint32_t)(c * kChunk) + 8u * (uint32_t)(r16 ^ (4 * i + xrow));
+          lds_dma16(xp[i] + (k < (uint32_t)K ? 2 * c * kChunk : -16 * (r16 ^ (4 * i + xrow))), lds[wave][4 * i]);
+        } else {
+          lds_dma16(xr, xo[i % 4] + (uint32_t)(i / 4 * 16) * (uint32_t)K * 2u + (uint32_t)(2 * c * kChunk), 0u, lds[wave][4 * i]);
+        }
+      }
+    };
+    f32x4 tot[NT][MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) tot[t][mt] = zero4;
+    // chunk c, whose weights are on their way to cur; the next chunk's go to nxt
+    auto chunk = [&](const Loads& cur, Loads& nxt, int c) __attribute__((always_inline)) {
+      wait_vmcnt<kLoads>();                   // this chunk's activations are in LDS, its weights may still come
+      asm volatile("" ::: "memory");
+      u32x4 x[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          x[mt][s] = *(const u32x4*)(lds[wave][16 * mt + r16] + 16 * ((FOLD == 4 ? 4 * kq + s : 4 * s + kq) ^ r16));
+      __builtin_amdgcn_s_waitcnt(0xC07F);     // read, before they are written over
+      asm volatile("" ::: "memory");
+      send_x(min(c + 1, c_hi - 1));           // past the share: its last chunk again, not used
+      __builtin_amdgcn_sched_barrier(0);
+      load(nxt, c + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[mt][s] = x_operand(x[mt][s]);
+      if (kChunk * (c + 1) > K) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int k = kChunk * c + (FOLD == 4 ? 32 * kq : 32 * s);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            if (k >= K) x[mt][s] = u32x4{0u, 0u, 0u, 0u};
+        }
+      }
+      f32x4 sum[SPANS][MT];
+#pragma unroll
+      for (int v = 0; v < SPANS; ++v)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          sum[v][mt] = zero4;
+#pragma unroll
+          for (int i = 0; i < FOLD; ++i) sum[v][mt] = mfma16<F16X>(x[mt][v * FOLD + i], ones, sum[v][mt]);
+        }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x4 w = FOLD == 4 ? cur.w[t] : transpose4(cur.w[t]);
+        const uint32_t sz = cur.s[t] | (cur.z[t] + z_add) << 16;
+        u32x4 szs = {sz, sz, sz, sz};
+        if (FOLD != 4) szs = spread4(sz);
+#pragma unroll
+        for (int v = 0; v < SPANS; ++v) {
+          u32x4 op[FOLD];
+#pragma unroll
+          for (int i = 0; i < FOLD; ++i) op[i] = codes_operand<F16X>(w[v * FOLD + i]);
+          const float s = float16_of((uint16_t)(szs[v] & 0xFFFFu), a.s_type), z = (float)(szs[v] >> 16);
+          f32x4 acc[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) acc[mt] = zero4;
+#pragma unroll
+          for (int i = 0; i < FOLD; ++i)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma16<F16X>(x[mt][v * FOLD + i], op[i], acc[mt]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tot[t][mt][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[v][mt][i], acc[mt][i]), tot[t][mt][i]);
+        }
+      }
+    };
+    if (c_lo < c_hi) {
+      Loads buf[2];
+      send_x(c_lo);
+      __builtin_amdgcn_sched_barrier(0);
+      load(buf[0], c_lo);
+      __builtin_amdgcn_sched_barrier(0);
+      for (int c = c_lo;; c += 2) {
+        chunk(buf[0], buf[1], c);
+        if (c + 1 >= c_hi) break;
+        chunk(buf[1], buf[0], c + 1);
+        if (c + 2 >= c_hi) break;
+      }
+      wait_vmcnt<0>();                        // the last direct loads have written LDS
+      asm volatile("" ::: "memory");
+    }
+    // the eight waves' tiles meet in LDS, each in its wave's own part (NT MT KB of MT 4 KB)
+    static_assert(NT <= 4, "a wave's sums fit its part of LDS");
+    float* const red = (float*)lds;
+    constexpr int kPart = MT * 4 * 256;       // floats per wave
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) *(f32x4*)(red + wave * kPart + (t * MT + mt) * 256 + 4 * lane) = tot[t][mt];
+    __syncthreads();
+    constexpr int kOuts = NT / H * MT * 256;
+    for (int o = threadIdx.x; o < kOuts; o += kWaves * 64) {
+      // output o: weight row o % 16 of its tile, row o / 16 % 16 of its row tile
+      const int n16 = o & 15, m16 = (o >> 4) & 15, j = o >> 8, mt = j % MT, t = j / MT;
+      const int m = 16 * mt + m16, n = tile_row(t) + n16;
+      if (m >= cnt || n >= No) continue;
+      const float* p = red + j * 256 + (16 * (m16 >> 2) + n16) * 4 + (m16 & 3);
+      float y = 0.f, u = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        y += p[w * kPart];
+        if (SILU) u += p[w * kPart + NT / H * MT * 256];
+      }
+      if (SILU) y = silu(y) * u;
+      store_elem(a.Y, a.y_type, (int64_t)(r0 + m) * No + n, y);
+    }
+    __syncthreads();
+  }
+}
+
+template <bool F16X, int MT, int NT, int FOLD, bool GROUPED, bool SILU>
+hipError_t launch_wide(const Int4GemvArgs& a, hipStream_t s) {
+  constexpr int H = SILU ? 2 : 1;
+  const int64_t No = a.N / H;
+  const int ngroups = (int)((No + 16 * NT / H - 1) / (16 * NT / H));
+  dim3 grid((unsigned)((a.M + 16 * MT - 1) / (16 * MT)), (unsigned)std::min(ngroups, 65535));
+  if (GROUPED) grid = dim3((unsigned)std::max<int64_t>(4 * cu_count(), std::min<int64_t>(a.E, a.M) + a.M / (16 * MT)));
+  hipLaunchKernelGGL((k_int4_wide<F16X, MT, NT, FOLD, GROUPED, SILU>), grid, dim3(kWaves * 64), 0, s, a, ngroups);
+  return hipGetLastError();
+}
+
+template <bool F16X, int MT, int FOLD>
+hipError_t launch_wide_n(const Int4GemvArgs& a, hipStream_t s) {
+  const int64_t tiles = (a.N + 15) / 16 * ((a.M + 16 * MT - 1) / (16 * MT)), cus = cu_count();
+  if (tiles >= 3 * cus) return launch_wide<F16X, MT, 4, FOLD, false, false>(a, s);
+  if (tiles >= 3 * cus / 2) return launch_wide<F16X, MT, 2, FOLD, false, false>(a, s);
+  return launch_wide<F16X, MT, 1, FOLD, false, false>(a, s);
+}
+
+template <bool F16X, int FOLD>
+hipError_t launch_wide_m(const Int4GemvArgs& a, hipStream_t s) {
+  if (a.offsets)
+    return a.silu ? launch_wide<F16X, 1, 2, FOLD, true, true>(a, s) : launch_wide<F16X, 1, 2, FOLD, true, false>(a, s);
+  if (a.M <= 16) return launch_wide_n<F16X, 1, FOLD>(a, s);
+  if (a.M <= 32) return launch_wide_n<F16X, 2, FOLD>(a, s);
+  return launch_wide_n<F16X, 4, FOLD>(a, s);
+}
+
+template <bool F16X>
+hipError_t launch_wide_f(const Int4GemvArgs& a, hipStream_t s) {
+  switch (int4_fold(a.group)) {
+    case 4: return launch_wide_m<F16X, 4>(a, s);
+    case 2: return launch_wide_m<F16X, 2>(a, s);
+    default: return launch_wide_m<F16X, 1>(a, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_int4_wide(const Int4GemvArgs& a, hipStream_t s) {
+  return a.x_type == kF16 ? launch_wide_f<true>(a, s) : launch_wide_f<false>(a, s);
+}
+
+}  // namespace ssn

@@ -104,6 +104,7 @@ struct Int4GemvArgs {
   int E, x_type, s_type, y_type, silu;
 };
 hipError_t launch_int4_gemv(const Int4GemvArgs& a, hipStream_t s);
+hipError_t launch_int4_wide(const Int4GemvArgs& a, hipStream_t s);   // its part for many rows or a long K
 
 // tokens to expert order and back: row_of[t k + j] is the row of entry (t, j), none outside [0, R)
 struct PermuteArgs {
