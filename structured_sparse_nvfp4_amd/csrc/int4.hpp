@@ -63,7 +63,16 @@ __device__ __forceinline__ u32x4 codes_operand(uint32_t w) {
                codes_pair<F16X, true>(hi)};
 }
 
-// eight activations (two per word) in that order
+// the same in natural order: two more instructions, for kernels whose activations serve few codes
+template <bool F16X>
+__device__ __forceinline__ u32x4 codes_operand_natural(uint32_t w) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+  return u32x4{codes_pair<F16X, false>(a), codes_pair<F16X, true>(a), codes_pair<F16X, false>(b),
+               codes_pair<F16X, true>(b)};
+}
+
+// eight activations (two per word) in the order 0 2 4 6 1 3 5 7
 __device__ __forceinline__ u32x4 x_operand(u32x4 x) {
   return u32x4{__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[3], x[2], 0x05040100u),
                __builtin_amdgcn_perm(x[1], x[0], 0x07060302u), __builtin_amdgcn_perm(x[3], x[2], 0x07060302u)};

@@ -23,12 +23,14 @@ constexpr int kWaves = 8;
 template <bool F16X, int MT, int NT, int FOLD, bool GROUPED, bool SILU>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, int ngroups) {
   constexpr int SPANS = 4 / FOLD, H = SILU ? 2 : 1;
-  constexpr int kLoads = NT * 3;              // loads to registers per chunk
-  // a wave's activations: 256 bytes per row, in 16 pieces, piece p of row r at place p ^ (r % 16), so that
-  // the 16 lanes that read one piece of 16 rows meet no bank twice
+  // A wave's activations: 256 bytes per row, in 16 pieces, piece p of row r at place p ^ swizzle(r). The LDS
+  // serves a 16-byte read in groups of lanes like 0-3, 12-15, 20-27: rows 0-3 and 12-15 of one piece and
+  // rows 4-11 of the next lane group's. With r itself as the swizzle they meet no bank twice where the lane
+  // groups' pieces follow one another (finer groups of k), with its bit pairs exchanged where they are four apart.
   __shared__ __attribute__((aligned(1024))) char lds[kWaves][16 * MT][256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
+  auto swizzle = [](int r) { return FOLD == 4 ? (r & 3) << 2 | (r >> 2 & 3) : r & 15; };
   const int No = (int)(a.N / H);
   const int K = (int)a.K, nch = (K + kChunk - 1) / kChunk, g32 = (int)(a.group / 32), groups = (int)a.groups;
   const int c_lo = nch * wave / kWaves, c_hi = nch * (wave + 1) / kWaves;
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
     const auto xr = buf_rsrc((const uint16_t*)a.X + (GROUPED ? 0 : (int64_t)r0 * K), GROUPED ? 0 : cnt * K * 2);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t piece = 16u * (uint32_t)(r16 ^ (4 * q + xrow));
+      const uint32_t piece = 16u * (uint32_t)(r16 ^ swizzle(4 * q + xrow));
       if constexpr (GROUPED) {
         const int m = r0 + min(4 * q + xrow, cnt - 1);
         const int src = min(max(a.row_token ? a.row_token[m] : m, 0), (int)a.x_rows - 1);
@@ -68,35 +70,42 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
     auto tile_row = [&](int t) { return 16 * (SILU ? ng * (NT / H) + t % (NT / H) : ng * NT + t); };
     struct Loads {
       u32x4 w[NT];
-      uint32_t s[NT], z[NT];                  // lane group g: the scale of span g (FOLD 4: all the same)
+    };
+    auto tile_base = [&](int t) { return (int64_t)e * a.N + (SILU && t >= NT / H ? No : 0) + tile_row(t); };
+    auto tile_rows = [&](int t) {
+      // (not max(0, min(..)): the compiler makes v_med3 of it, and a resource in vector registers)
+      const int n0 = tile_row(t);
+      return n0 < No ? min(16, No - n0) : 0;
     };
     auto load = [&](Loads& o, int c) __attribute__((always_inline)) {
-      const int k = kChunk * c + 32 * kq, ks = FOLD == 4 ? kChunk * c : kChunk * c + 32 * FOLD * kq;
-      const bool in = c < c_hi, in_s = in && kq < SPANS && ks < K;
-      const uint32_t ko = in && k < K ? (uint32_t)(r16 * (K / 2) + k / 2) : kOutside;
-      const uint32_t go = FOLD == 4 ? (in ? (uint32_t)(r16 * groups + ks / 32 / g32) : kOutside / 2)
-                                    : (in_s ? (uint32_t)(r16 * groups + ks / 32 / g32) : kOutside / 2);
+      const int k = kChunk * c + 32 * kq;
+      const uint32_t ko = c < c_hi && k < K ? (uint32_t)(r16 * (K / 2) + k / 2) : kOutside;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        o.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               buf_rsrc(a.codes + tile_base(t) * (K / 2), tile_rows(t) * (K / 2)), ko, 0, 0));
+    };
+    // Scales and zero points: lane group g loads span g of the four spans from chunk c on, FOLD chunks' worth
+    // (a load of its own for every chunk costs the address unit as much as the codes)
+    uint32_t sc[NT], zp[NT], sz[NT];
+    auto load_sz = [&](int c) __attribute__((always_inline)) {
+      const int k = kChunk * c + 32 * FOLD * kq;
+      const uint32_t go = c < c_hi && k < K ? (uint32_t)(r16 * groups + k / 32 / g32) : kOutside / 2;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int n0 = tile_row(t);
-        // (not max(0, min(..)): the compiler makes v_med3 of it, and a resource in vector registers)
-        const int rows = n0 < No ? min(16, No - n0) : 0;
-        const int64_t row = (int64_t)e * a.N + (SILU && t >= NT / H ? No : 0) + n0;
-        const auto wr = buf_rsrc(a.codes + row * (K / 2), rows * (K / 2));
-        const auto sr = buf_rsrc(a.scales + row * groups, rows * groups * 2);
-        const auto zr = buf_rsrc(a.zeros + row * groups, a.zeros ? rows * groups : 0);
-        o.w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, ko, 0, 0));
-        o.s[t] = __builtin_amdgcn_raw_buffer_load_b16(sr, 2 * go, 0, 0);
-        o.z[t] = __builtin_amdgcn_raw_buffer_load_b8(zr, go, 0, 0);
+        const int rows = tile_rows(t) * groups;
+        sc[t] = __builtin_amdgcn_raw_buffer_load_b16(buf_rsrc(a.scales + tile_base(t) * groups, rows * 2), 2 * go, 0, 0);
+        zp[t] = __builtin_amdgcn_raw_buffer_load_b8(buf_rsrc(a.zeros + tile_base(t) * groups, a.zeros ? rows : 0), go, 0, 0);
       }
     };
-    auto send_x = [&](int c) __attribute__((always_inline)) {
+    // part t of NT of the direct loads of chunk c
+    auto send_x = [&](int c, int t) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 4 * MT; ++i) {
+      for (int i = 4 * MT * t / NT; i < 4 * MT * (t + 1) / NT; ++i) {
         if constexpr (GROUPED) {
           // a piece past the end of K: the row's first
-          const uint32_t k = (uint32_t)(c * kChunk) + 8u * (uint32_t)(r16 ^ (4 * i + xrow));
-          lds_dma16(xp[i] + (k < (uint32_t)K ? 2 * c * kChunk : -16 * (r16 ^ (4 * i + xrow))), lds[wave][4 * i]);
+          const int piece = r16 ^ swizzle(4 * i + xrow);
+          lds_dma16(xp[i] + (kChunk * c + 8 * piece < K ? 2 * c * kChunk : -16 * piece), lds[wave][4 * i]);
         } else {
           lds_dma16(xr, xo[i % 4] + (uint32_t)(i / 4 * 16) * (uint32_t)K * 2u + (uint32_t)(2 * c * kChunk), 0u, lds[wave][4 * i]);
         }
@@ -109,24 +118,23 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
       for (int mt = 0; mt < MT; ++mt) tot[t][mt] = zero4;
     // chunk c, whose weights are on their way to cur; the next chunk's go to nxt
     auto chunk = [&](const Loads& cur, Loads& nxt, int c) __attribute__((always_inline)) {
-      wait_vmcnt<kLoads>();                   // this chunk's activations are in LDS, its weights may still come
+      wait_vmcnt<0>();                        // this chunk's activations are in LDS
       asm volatile("" ::: "memory");
       u32x4 x[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          x[mt][s] = *(const u32x4*)(lds[wave][16 * mt + r16] + 16 * ((FOLD == 4 ? 4 * kq + s : 4 * s + kq) ^ r16));
+          x[mt][s] = *(const u32x4*)(lds[wave][16 * mt + r16] + 16 * ((FOLD == 4 ? 4 * kq + s : 4 * s + kq) ^ swizzle(r16)));
       __builtin_amdgcn_s_waitcnt(0xC07F);     // read, before they are written over
       asm volatile("" ::: "memory");
-      send_x(min(c + 1, c_hi - 1));           // past the share: its last chunk again, not used
-      __builtin_amdgcn_sched_barrier(0);
+      const int phase = (c - c_lo) % FOLD;    // of the chunks that share a load of scales
+      if (phase == 0)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sz[t] = sc[t] | (zp[t] + z_add) << 16;
+      if (phase == FOLD - 1) load_sz(c + 1);
       load(nxt, c + 1);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) x[mt][s] = x_operand(x[mt][s]);
       if (kChunk * (c + 1) > K) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -148,14 +156,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const u32x4 w = FOLD == 4 ? cur.w[t] : transpose4(cur.w[t]);
-        const uint32_t sz = cur.s[t] | (cur.z[t] + z_add) << 16;
-        u32x4 szs = {sz, sz, sz, sz};
-        if (FOLD != 4) szs = spread4(sz);
+        u32x4 szs;                            // of the chunk's spans, in every lane
+        if (FOLD == 1) szs = spread4(sz[t]);
+        else
+#pragma unroll
+          for (int v = 0; v < SPANS; ++v)
+            szs[v] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * (phase * SPANS + v) + r16), (int)sz[t]);
 #pragma unroll
         for (int v = 0; v < SPANS; ++v) {
           u32x4 op[FOLD];
 #pragma unroll
-          for (int i = 0; i < FOLD; ++i) op[i] = codes_operand<F16X>(w[v * FOLD + i]);
+          for (int i = 0; i < FOLD; ++i) op[i] = codes_operand_natural<F16X>(w[v * FOLD + i]);
           const float s = float16_of((uint16_t)(szs[v] & 0xFFFFu), a.s_type), z = (float)(szs[v] >> 16);
           f32x4 acc[MT];
 #pragma unroll
@@ -170,12 +181,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
             for (int i = 0; i < 4; ++i)
               tot[t][mt][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[v][mt][i], acc[mt][i]), tot[t][mt][i]);
         }
+        // the next chunk's activations, a part after each tile: in one burst the waves would stand at the
+        // address unit. Past the share: its last chunk again, not used
+        __builtin_amdgcn_sched_barrier(0);
+        send_x(min(c + 1, c_hi - 1), t);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     if (c_lo < c_hi) {
       Loads buf[2];
-      send_x(c_lo);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) send_x(c_lo, t);
+      load_sz(c_lo);
       load(buf[0], c_lo);
       __builtin_amdgcn_sched_barrier(0);
       for (int c = c_lo;; c += 2) {
