@@ -11,55 +11,138 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// ------------------------------------------------------------------------------ quantise
-// The whole number nearest to w / s (s > 0), halves to the even one.
-__device__ __forceinline__ float nearest_multiple(float w, float s) { return (float)rint((double)w / (double)s); }
-
-// One thread per group.
-__global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restrict__ W, int wt, int64_t N, int64_t K,
-                                                            int64_t group, int64_t groups, uint8_t* __restrict__ codes,
-                                                            uint16_t* __restrict__ scales, int st,
-                                                            uint8_t* __restrict__ zeros) {
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < N * groups; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t n = i / groups, g = i - n * groups;
-    const int64_t k0 = g * group, k1 = min(K, k0 + group);
-    float lo = 0.f, hi = 0.f;
-    for (int64_t k = k0; k < k1; ++k) {
-      const float w = load_elem(W, wt, n * K + k);
-      lo = fminf(lo, w);
-      hi = fmaxf(hi, w);
+// eight consecutive weights of type T as f32, from a pointer aligned to them
+template <int T>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float* w) {
+  if constexpr (T == kF32) {
+    const f32x4 a = ((const f32x4*)p)[i / 4], b = ((const f32x4*)p)[i / 4 + 1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { w[j] = a[j]; w[4 + j] = b[j]; }
+  } else {
+    const u32x4 v = ((const u32x4*)p)[i / 8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[2 * j] = T == kBF16 ? bf16_lo(v[j]) : f16_of((uint16_t)v[j]);
+      w[2 * j + 1] = T == kBF16 ? bf16_hi(v[j]) : f16_of((uint16_t)(v[j] >> 16));
     }
-    const double range = zeros ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
-    const uint16_t sb = round16_sat(range, st);
-    const float s = float16_of(sb, st);
-    float z = 8.f;
-    if (zeros) z = s > 0.f ? fminf(fmaxf(nearest_multiple(-lo, s), 0.f), 15.f) : 0.f;
-    for (int64_t k = k0; k < k1; k += 2) {
-      uint32_t b = 0;
-      for (int j = 0; j < 2; ++j) {
-        const float w = load_elem(W, wt, n * K + k + j);
-        const float q = s > 0.f ? fminf(fmaxf(nearest_multiple(w, s) + z, 0.f), 15.f) : z;
-        b |= (uint32_t)q << (4 * j);
-      }
-      codes[(n * K + k) / 2] = (uint8_t)b;
-    }
-    scales[i] = sb;
-    if (zeros) zeros[i] = (uint8_t)z;
   }
 }
 
-// One thread per pair of codes.
-__global__ __launch_bounds__(kThreads) void k_int4_dequantize(const uint8_t* __restrict__ codes,
+// ------------------------------------------------------------------------------ quantise
+// The whole number nearest to w / s, halves to the even one; inv = 1 / s to a few units. s has at most 11
+// significant bits and q + 1/2 six, so their product is exact and one FMA gives the sign of
+// w - s (q + 1/2) exactly: the quotient's own rounding decides nothing. (Where |w / s| is so large that q + 1/2 is
+// q, the code is clamped anyway.)
+__device__ __forceinline__ float nearest_multiple(float w, float s, float inv) {
+  float q = rintf(w * inv);
+  const float up = __builtin_fmaf(-s, q + 0.5f, w), down = __builtin_fmaf(-s, q - 0.5f, w);
+  const bool odd = (int)q & 1;
+  if (up > 0.f || (up == 0.f && odd)) return q + 1.f;
+  if (down < 0.f || (down == 0.f && odd)) return q - 1.f;
+  return q;
+}
+
+// the larger of each lane's value and those of the L lanes it is among (L a power of two)
+template <int L>
+__device__ __forceinline__ float team_max(float v) {
+  auto of = [&](int moved) { v = fmaxf(v, __int_as_float(moved)); };
+  of(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));                // quad 1 0 3 2
+  of(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));                // quad 2 3 0 1
+  if (L > 4) of(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));    // mirrored in 8
+  if (L > 8) of(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));    // mirrored in 16
+  if (L > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if (L > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
+
+// One team of L lanes per group, eight weights a lane at a time: groups up to 8 L weights are read once and
+// stay in registers, longer ones (L = 64) a second time from the L2. Memory-bound: W read, codes written.
+template <int T, int L>
+__global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restrict__ W, int64_t teams, int K, int group,
+                                                            int groups, uint32_t* __restrict__ codes,
+                                                            uint16_t* __restrict__ scales, int st,
+                                                            uint8_t* __restrict__ zeros) {
+  constexpr int kTeams = kThreads / L;         // per workgroup
+  const int l = threadIdx.x % L;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < teams; t0 += (int64_t)gridDim.x * kTeams) {
+    const int64_t team = t0 + threadIdx.x / L;
+    const bool live = team < teams;
+    // row and group of this team: the workgroup's first by a uniform division, the rest by counting on
+    const int64_t row0 = t0 / groups;
+    const int g0 = (int)(t0 - row0 * groups) + (int)(threadIdx.x / L);
+    const int64_t n = row0 + g0 / groups;
+    const int k0 = g0 % groups * group, len = min(group, K - k0);
+    const int64_t base = n * K + k0;
+    float w[8] = {}, lo = 0.f, hi = 0.f;
+    if (live)
+      for (int k = 8 * l; k < len; k += 8 * L) {
+        load8<T>(W, base + k, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) { lo = fminf(lo, w[j]); hi = fmaxf(hi, w[j]); }
+      }
+    hi = team_max<L>(hi);
+    lo = -team_max<L>(-lo);
+    const double range = zeros ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
+    const uint16_t sb = round16_sat(range, st);
+    const float s0 = float16_of(sb, st);
+    // subnormal scales: both sides times 2^64, exactly, or the reciprocal overflows
+    const float f = s0 < 0x1p-100f ? 0x1p64f : 1.f, s = s0 * f, inv = __builtin_amdgcn_rcpf(s);
+    const bool any = s0 > 0.f;
+    float z = 8.f;
+    if (zeros) z = any ? fminf(fmaxf(nearest_multiple(-lo * f, s, inv), 0.f), 15.f) : 0.f;
+    if (!live) continue;
+    for (int k = 8 * l; k < len; k += 8 * L) {
+      if (len > 8 * L) load8<T>(W, base + k, w);
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = any ? fminf(fmaxf(nearest_multiple(w[j] * f, s, inv) + z, 0.f), 15.f) : z;
+        c |= (uint32_t)q << (4 * j);
+      }
+      codes[(base + k) / 8] = c;
+    }
+    if (l == 0) {
+      scales[team] = sb;
+      if (zeros) zeros[team] = (uint8_t)z;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ dequantise
+// One lane per eight k of a row, over several rows: where its group lies in a row is found once.
+template <int T>
+__global__ __launch_bounds__(kThreads) void k_int4_dequantize(const uint32_t* __restrict__ codes,
                                                               const uint16_t* __restrict__ scales, int st,
-                                                              const uint8_t* __restrict__ zeros, int64_t N, int64_t K,
-                                                              int64_t group, int64_t groups, void* __restrict__ out,
-                                                              int ot) {
-  const int64_t Kh = K / 2;
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < N * Kh; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t n = i / Kh, k = 2 * (i - n * Kh), sg = n * groups + k / group;
-    const float s = float16_of(scales[sg], st), z = zeros ? (float)zeros[sg] : 8.f;
-    store_elem(out, ot, 2 * i, ((float)(codes[i] & 15) - z) * s);
-    store_elem(out, ot, 2 * i + 1, ((float)(codes[i] >> 4) - z) * s);
+                                                              const uint8_t* __restrict__ zeros, int64_t N, int K,
+                                                              int group, int groups, void* __restrict__ out) {
+  const int v = blockIdx.x * kThreads + threadIdx.x, nv = K / 8;
+  if (v >= nv) return;
+  const int g = 8 * v / group;
+#pragma unroll 4
+  for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
+    const uint32_t c = codes[n * nv + v];
+    const float s = float16_of(scales[n * groups + g], st), z = zeros ? (float)zeros[n * groups + g] : 8.f;
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = ((float)(c >> (4 * j) & 15) - z) * s;
+    const int64_t i = n * nv + v;
+    if constexpr (T == kF32) {
+      ((f32x4*)out)[2 * i] = f32x4{w[0], w[1], w[2], w[3]};
+      ((f32x4*)out)[2 * i + 1] = f32x4{w[4], w[5], w[6], w[7]};
+    } else {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = T == kBF16 ? pk_bf16_rne(w[2 * j], w[2 * j + 1])
+                          : (uint32_t)to_f16(w[2 * j]) | (uint32_t)to_f16(w[2 * j + 1]) << 16;
+      ((u32x4*)out)[i] = o;
+    }
   }
 }
 
@@ -295,21 +378,55 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles) {
 
 }  // namespace
 
+namespace {
+
+template <int T, int L>
+hipError_t launch_quantize_l(const void* W, int64_t N, int64_t K, int64_t group, uint8_t* codes, uint16_t* scales,
+                             int s_type, uint8_t* zeros, hipStream_t s) {
+  const int64_t groups = (K + group - 1) / group, teams = N * groups;
+  const int64_t blocks = std::min<int64_t>((teams + kThreads / L - 1) / (kThreads / L), 1 << 22);
+  hipLaunchKernelGGL((k_int4_quantize<T, L>), dim3((unsigned)blocks), dim3(kThreads), 0, s, W, teams, (int)K,
+                     (int)std::min(group, K), (int)groups, (uint32_t*)codes, scales, s_type, zeros);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t launch_quantize_t(const void* W, int64_t N, int64_t K, int64_t group, uint8_t* codes, uint16_t* scales,
+                             int s_type, uint8_t* zeros, hipStream_t s) {
+  const int64_t len = std::min(group, K);
+  if (len <= 32) return launch_quantize_l<T, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
+  if (len <= 64) return launch_quantize_l<T, 8>(W, N, K, group, codes, scales, s_type, zeros, s);
+  if (len <= 128) return launch_quantize_l<T, 16>(W, N, K, group, codes, scales, s_type, zeros, s);
+  if (len <= 256) return launch_quantize_l<T, 32>(W, N, K, group, codes, scales, s_type, zeros, s);
+  return launch_quantize_l<T, 64>(W, N, K, group, codes, scales, s_type, zeros, s);
+}
+
+}  // namespace
+
 hipError_t launch_int4_quantize(const void* W, int w_type, int64_t N, int64_t K, int64_t group, uint8_t* codes,
                                 uint16_t* scales, int s_type, uint8_t* zeros, hipStream_t s) {
-  const int64_t groups = (K + group - 1) / group;
-  const int64_t blocks = std::min<int64_t>((N * groups + kThreads - 1) / kThreads, 1 << 16);
-  hipLaunchKernelGGL(k_int4_quantize, dim3((unsigned)blocks), dim3(kThreads), 0, s, W, w_type, N, K, group, groups,
-                     codes, scales, s_type, zeros);
-  return hipGetLastError();
+  if (w_type == kF32) return launch_quantize_t<kF32>(W, N, K, group, codes, scales, s_type, zeros, s);
+  if (w_type == kF16) return launch_quantize_t<kF16>(W, N, K, group, codes, scales, s_type, zeros, s);
+  return launch_quantize_t<kBF16>(W, N, K, group, codes, scales, s_type, zeros, s);
 }
 
 hipError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, int s_type, const uint8_t* zeros,
                                   int64_t N, int64_t K, int64_t group, void* out, int out_type, hipStream_t s) {
-  const int64_t groups = (K + group - 1) / group;
-  const int64_t blocks = std::min<int64_t>((N * (K / 2) + kThreads - 1) / kThreads, 1 << 16);
-  hipLaunchKernelGGL(k_int4_dequantize, dim3((unsigned)blocks), dim3(kThreads), 0, s, codes, scales, s_type, zeros, N,
-                     K, group, groups, out, out_type);
+  const int groups = (int)((K + group - 1) / group);
+  const int64_t bx = (K / 8 + kThreads - 1) / kThreads;
+  // four rows a lane, and more where the grid would pass its second axis or some 2^20 workgroups
+  const int64_t by = std::min<int64_t>({(N + 3) / 4, 65535, std::max<int64_t>(1, (1 << 20) / bx)});
+  const dim3 grid((unsigned)bx, (unsigned)by);
+  const auto* c = (const uint32_t*)codes;
+  if (out_type == kF32)
+    hipLaunchKernelGGL(k_int4_dequantize<kF32>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+                       (int)std::min(group, K), groups, out);
+  else if (out_type == kF16)
+    hipLaunchKernelGGL(k_int4_dequantize<kF16>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+                       (int)std::min(group, K), groups, out);
+  else
+    hipLaunchKernelGGL(k_int4_dequantize<kBF16>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+                       (int)std::min(group, K), groups, out);
   return hipGetLastError();
 }
 
