@@ -29,17 +29,26 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float* w) {
 }
 
 // ------------------------------------------------------------------------------ quantise
-// The whole number nearest to w / s, halves to the even one; inv = 1 / s to a few units. s has at most 11
-// significant bits and q + 1/2 six, so their product is exact and one FMA gives the sign of
-// w - s (q + 1/2) exactly: the quotient's own rounding decides nothing. (Where |w / s| is so large that q + 1/2 is
-// q, the code is clamped anyway.)
-__device__ __forceinline__ float nearest_multiple(float w, float s, float inv) {
-  float q = rintf(w * inv);
-  const float up = __builtin_fmaf(-s, q + 0.5f, w), down = __builtin_fmaf(-s, q - 0.5f, w);
-  const bool odd = (int)q & 1;
-  if (up > 0.f || (up == 0.f && odd)) return q + 1.f;
-  if (down < 0.f || (down == 0.f && odd)) return q - 1.f;
-  return q;
+// A scale as the quantiser uses it: inv = 1 / s to a few units, half = s / 2, step = twice the distance from
+// half to the next smaller number.
+struct Step {
+  float s, inv, half, step;
+};
+__device__ __forceinline__ Step make_step(float s) {
+  const float half = 0.5f * s;
+  return {s, __builtin_amdgcn_rcpf(s), half, 2.f * (half - __uint_as_float(__float_as_uint(half) - 1))};
+}
+
+// The whole number nearest to w / s, halves to the even one. q = rint(w inv) is it or a neighbour's. The
+// rest w - s q is exact in one FMA (s has at most 11 significant bits and q five, and the rest is a
+// multiple of w's last bit below s), so comparing it with s / 2 decides exactly; an odd q yields at s / 2 itself, that is
+// beyond the next smaller number. (Where |w / s| is far beyond the codes the result is clamped anyway.)
+__device__ __forceinline__ float nearest_multiple(float w, const Step& t) {
+  const float q = __builtin_rintf(w * t.inv);
+  const float rest = __builtin_fmaf(-t.s, q, w);
+  const float odd = __builtin_amdgcn_fractf(0.5f * q);          // 0, or 0.5 for an odd q
+  const float limit = __builtin_fmaf(-odd, t.step, t.half);
+  return __builtin_fabsf(rest) > limit ? q + __builtin_copysignf(1.f, rest) : q;
 }
 
 // the larger of each lane's value and those of the L lanes it is among (L a power of two)
@@ -92,20 +101,23 @@ __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restri
     const uint16_t sb = round16_sat(range, st);
     const float s0 = float16_of(sb, st);
     // subnormal scales: both sides times 2^64, exactly, or the reciprocal overflows
-    const float f = s0 < 0x1p-100f ? 0x1p64f : 1.f, s = s0 * f, inv = __builtin_amdgcn_rcpf(s);
+    const float f = s0 < 0x1p-100f ? 0x1p64f : 1.f;
+    const Step step = make_step(s0 * f);
     const bool any = s0 > 0.f;
     float z = 8.f;
-    if (zeros) z = any ? fminf(fmaxf(nearest_multiple(-lo * f, s, inv), 0.f), 15.f) : 0.f;
+    if (zeros) z = any ? fminf(fmaxf(nearest_multiple(-lo * f, step), 0.f), 15.f) : 0.f;
     if (!live) continue;
     for (int k = 8 * l; k < len; k += 8 * L) {
       if (len > 8 * L) load8<T>(W, base + k, w);
-      uint32_t c = 0;
+      uint32_t even = 0, odd = 0;              // the codes as bytes
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = any ? fminf(fmaxf(nearest_multiple(w[j] * f, s, inv) + z, 0.f), 15.f) : z;
-        c |= (uint32_t)q << (4 * j);
+      for (int j = 0; j < 8; j += 2) {
+        const float a = __builtin_amdgcn_fmed3f(nearest_multiple(w[j] * f, step) + z, 0.f, 15.f);
+        const float b = __builtin_amdgcn_fmed3f(nearest_multiple(w[j + 1] * f, step) + z, 0.f, 15.f);
+        even = __builtin_amdgcn_cvt_pk_u8_f32(a, j / 2, even);
+        odd = __builtin_amdgcn_cvt_pk_u8_f32(b, j / 2, odd);
       }
-      codes[(base + k) / 8] = c;
+      codes[(base + k) / 8] = any ? even | odd << 4 : 0x11111111u * (uint32_t)z;
     }
     if (l == 0) {
       scales[team] = sb;
@@ -115,34 +127,34 @@ __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restri
 }
 
 // ------------------------------------------------------------------------------ dequantise
-// One lane per eight k of a row, over several rows: where its group lies in a row is found once.
+// One lane per 16 bytes of output (four or eight k) of a row, over several rows: where its group lies in a
+// row is found once.
 template <int T>
-__global__ __launch_bounds__(kThreads) void k_int4_dequantize(const uint32_t* __restrict__ codes,
+__global__ __launch_bounds__(kThreads) void k_int4_dequantize(const uint8_t* __restrict__ codes,
                                                               const uint16_t* __restrict__ scales, int st,
                                                               const uint8_t* __restrict__ zeros, int64_t N, int K,
                                                               int group, int groups, void* __restrict__ out) {
-  const int v = blockIdx.x * kThreads + threadIdx.x, nv = K / 8;
+  constexpr int kPer = T == kF32 ? 4 : 8;
+  using Codes = std::conditional_t<T == kF32, uint16_t, uint32_t>;
+  const int v = blockIdx.x * kThreads + threadIdx.x, nv = K / kPer;
   if (v >= nv) return;
-  const int g = 8 * v / group;
+  const int g = kPer * v / group;
 #pragma unroll 4
   for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
-    const uint32_t c = codes[n * nv + v];
-    const float s = float16_of(scales[n * groups + g], st), z = zeros ? (float)zeros[n * groups + g] : 8.f;
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = ((float)(c >> (4 * j) & 15) - z) * s;
     const int64_t i = n * nv + v;
-    if constexpr (T == kF32) {
-      ((f32x4*)out)[2 * i] = f32x4{w[0], w[1], w[2], w[3]};
-      ((f32x4*)out)[2 * i + 1] = f32x4{w[4], w[5], w[6], w[7]};
-    } else {
-      u32x4 o;
+    const uint32_t c = ((const Codes*)codes)[i];
+    const float s = float16_of(scales[n * groups + g], st), z = zeros ? (float)zeros[n * groups + g] : 8.f;
+    float w[kPer];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = T == kBF16 ? pk_bf16_rne(w[2 * j], w[2 * j + 1])
-                          : (uint32_t)to_f16(w[2 * j]) | (uint32_t)to_f16(w[2 * j + 1]) << 16;
-      ((u32x4*)out)[i] = o;
+    for (int j = 0; j < kPer; ++j) w[j] = ((float)(c >> (4 * j) & 15) - z) * s;
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (T == kF32) o[j] = __float_as_uint(w[j]);
+      else if constexpr (T == kBF16) o[j] = pk_bf16_rne(w[2 * j], w[2 * j + 1]);
+      else o[j] = (uint32_t)to_f16(w[2 * j]) | (uint32_t)to_f16(w[2 * j + 1]) << 16;
     }
+    ((u32x4*)out)[i] = o;
   }
 }
 
@@ -413,19 +425,18 @@ hipError_t launch_int4_quantize(const void* W, int w_type, int64_t N, int64_t K,
 hipError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, int s_type, const uint8_t* zeros,
                                   int64_t N, int64_t K, int64_t group, void* out, int out_type, hipStream_t s) {
   const int groups = (int)((K + group - 1) / group);
-  const int64_t bx = (K / 8 + kThreads - 1) / kThreads;
+  const int64_t bx = (K / (out_type == kF32 ? 4 : 8) + kThreads - 1) / kThreads;
   // four rows a lane, and more where the grid would pass its second axis or some 2^20 workgroups
   const int64_t by = std::min<int64_t>({(N + 3) / 4, 65535, std::max<int64_t>(1, (1 << 20) / bx)});
   const dim3 grid((unsigned)bx, (unsigned)by);
-  const auto* c = (const uint32_t*)codes;
   if (out_type == kF32)
-    hipLaunchKernelGGL(k_int4_dequantize<kF32>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+    hipLaunchKernelGGL(k_int4_dequantize<kF32>, grid, dim3(kThreads), 0, s, codes, scales, s_type, zeros, N, (int)K,
                        (int)std::min(group, K), groups, out);
   else if (out_type == kF16)
-    hipLaunchKernelGGL(k_int4_dequantize<kF16>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+    hipLaunchKernelGGL(k_int4_dequantize<kF16>, grid, dim3(kThreads), 0, s, codes, scales, s_type, zeros, N, (int)K,
                        (int)std::min(group, K), groups, out);
   else
-    hipLaunchKernelGGL(k_int4_dequantize<kBF16>, grid, dim3(kThreads), 0, s, c, scales, s_type, zeros, N, (int)K,
+    hipLaunchKernelGGL(k_int4_dequantize<kBF16>, grid, dim3(kThreads), 0, s, codes, scales, s_type, zeros, N, (int)K,
                        (int)std::min(group, K), groups, out);
   return hipGetLastError();
 }
