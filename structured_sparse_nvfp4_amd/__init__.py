@@ -504,32 +504,52 @@ def moe_nvfp4_ffn_noalloc(X, topk_ids, topk_weights, E, up, down, out, bad_ids, 
 # ------------------------------------------------------------------------------------------------
 # integer 4-bit weights with group scales
 
-_DTYPES = {torch.float32: SSN_F32, torch.bfloat16: SSN_BF16, torch.float16: SSN_F16}
+_DTYPES = {torch.float32: SSN_F32, torch.bfloat16: SSN_BF16, torch.float16: SSN_F16, torch.uint8: None}
 _HALVES = (torch.bfloat16, torch.float16)
 _ANY = (torch.float32, torch.bfloat16, torch.float16)
+_BYTES = (torch.uint8,)
 
 
-def _dtype(t, name, allowed):
-    dt = t if isinstance(t, torch.dtype) else getattr(t, "dtype", None)
-    if dt not in allowed:
-        raise TypeError(f"{name} must be one of {', '.join(str(a)[6:] for a in allowed)}, got {dt}")
-    return _DTYPES[dt]
-
-
-def _dims(t, n, name):
+def _first(t, n, name, allowed):
+    """(shape, device, dtype code) of a call's leading tensor, which settles its device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+    dt = _code(t.dtype, name, allowed)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape, t.device, dt
+
+
+def _code(dtype, name, allowed):
+    if dtype not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(a)[6:] for a in allowed)}, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _on(dev, t, dtype, name, shape):
+    """Address of a contiguous tensor of this type and shape on `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be a device tensor on {dev}, it is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _run_on(dev, fname, cargs, prepare, keep, result):
-    """_run with `dev` current for the launch, after a check that every tensor is on it. A prepared call
+    """_run with `dev` current for the launch and its current stream as the last argument. A prepared call
     launches on the device that is current when it is called."""
-    for t in (*keep, *(result if isinstance(result, tuple) else (result,))):
-        if isinstance(t, torch.Tensor) and t.device != dev:
-            raise ValueError(f"{fname}: tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"{fname} takes device tensors, got tensors on {dev}")
+    # the raw handle: torch.cuda.current_stream() builds an object, which takes 2 us of a call's 7
+    cargs = (*cargs, torch._C._cuda_getCurrentRawStream(dev.index))
     if prepare or dev.index == torch.cuda.current_device():
         return _run(fname, cargs, prepare, keep, result)
     with torch.cuda.device(dev):
@@ -547,58 +567,49 @@ def int4_quantize(W, group=128, symmetric=False, scale_dtype=torch.bfloat16, cod
     """4-bit codes of W [N, K] (f32, bf16 or f16) with a scale, and unless symmetric a zero point, per `group`
     consecutive k. Returns (codes u8 [N, K/2], scales of scale_dtype [N, ceil(K/group)], zeros u8 of that shape
     or None)."""
-    N, K = _dims(W, 2, "W")
-    wdt = _dtype(_need(W, W.dtype, "W"), "W", _ANY)
+    (N, K), dev, wdt = _first(W, 2, "W", _ANY)
     groups = _int4_group(K, group)
-    dev = W.device
     if symmetric and zeros is not None:
         raise ValueError("symmetric quantisation has no zeros")
     codes = codes if codes is not None else torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
     scales = scales if scales is not None else torch.empty((N, groups), dtype=scale_dtype, device=dev)
     if not symmetric and zeros is None:
         zeros = torch.empty((N, groups), dtype=torch.uint8, device=dev)
-    sdt = _dtype(scales, "scales", _HALVES)
-    _need(codes, torch.uint8, "codes", (N, K // 2)); _need(scales, scales.dtype, "scales", (N, groups))
-    if zeros is not None:
-        _need(zeros, torch.uint8, "zeros", (N, groups))
-    cargs = (_ptr(W), wdt, N, K, group, sdt, _ptr(codes), _ptr(scales), _ptr(zeros), _stream(dev))
+    sdt = _code(scales.dtype, "scales", _HALVES)
+    cargs = (W.data_ptr(), wdt, N, K, group, sdt, _on(dev, codes, torch.uint8, "codes", (N, K // 2)),
+             _on(dev, scales, scales.dtype, "scales", (N, groups)),
+             None if zeros is None else _on(dev, zeros, torch.uint8, "zeros", (N, groups)))
     return _run_on(dev, "int4_quantize", cargs, prepare, (W,), (codes, scales, zeros))
 
 
 def int4_dequantize(codes, scales, zeros=None, group=128, out_dtype=torch.float32, out=None, prepare=False):
     """W_hat [N, K] = scales * (codes - zeros) (zeros None: 8), f32, bf16 or f16."""
-    N, Kh = _dims(codes, 2, "codes")
+    (N, Kh), dev, _ = _first(codes, 2, "codes", _BYTES)
     K = 2 * Kh
     groups = _int4_group(K, group)
-    sdt = _dtype(scales, "scales", _HALVES)
-    _need(codes, torch.uint8, "codes"); _need(scales, scales.dtype, "scales", (N, groups))
-    if zeros is not None:
-        _need(zeros, torch.uint8, "zeros", (N, groups))
-    out = out if out is not None else torch.empty((N, K), dtype=out_dtype, device=codes.device)
-    odt = _dtype(out, "out", _ANY)
-    _need(out, out.dtype, "out", (N, K))
-    cargs = (_ptr(codes), _ptr(scales), sdt, _ptr(zeros), N, K, group, _ptr(out), odt, _stream(codes.device))
-    return _run_on(codes.device, "int4_dequantize", cargs, prepare, (codes, scales, zeros), out)
+    sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
+    out = out if out is not None else torch.empty((N, K), dtype=out_dtype, device=dev)
+    odt = _code(out.dtype, "out", _ANY)
+    cargs = (codes.data_ptr(), _on(dev, scales, scales.dtype, "scales", (N, groups)), sdt,
+             None if zeros is None else _on(dev, zeros, torch.uint8, "zeros", (N, groups)), N, K, group,
+             _on(dev, out, out.dtype, "out", (N, K)), odt)
+    return _run_on(dev, "int4_dequantize", cargs, prepare, (codes, scales, zeros), out)
 
 
 def gemv_int4(X, codes, scales, zeros=None, group=128, y_dtype=torch.float32, algo=ALGO_AUTO, Y=None, prepare=False):
     """Y = X . W_hat^T for a few rows of X (bf16 or f16 [M, K]) and integer 4-bit weights: codes u8 [N, K/2],
     scales bf16 or f16 and zeros u8 (or None: 8) [N, ceil(K/group)]. Returns (Y, algorithm that ran)."""
-    M, K = _dims(X, 2, "X")
-    N, _ = _dims(codes, 2, "codes")
+    (M, K), dev, xdt = _first(X, 2, "X", _HALVES)
     groups = _int4_group(K, group)
-    xdt, sdt = _dtype(X, "X", _HALVES), _dtype(scales, "scales", _HALVES)
-    _need(X, X.dtype, "X"); _need(codes, torch.uint8, "codes", (N, K // 2))
-    _need(scales, scales.dtype, "scales", (N, groups))
-    if zeros is not None:
-        _need(zeros, torch.uint8, "zeros", (N, groups))
-    dev = X.device
+    (N, _), _, _ = _first(codes, 2, "codes", _BYTES)
+    sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
     Y = Y if Y is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
-    ydt = _dtype(Y, "Y", _ANY)
-    _need(Y, Y.dtype, "Y", (M, N))
+    ydt = _code(Y.dtype, "Y", _ANY)
     used = ctypes.c_int(-1)
-    cargs = (_ptr(X), xdt, M, N, K, _ptr(codes), _ptr(scales), sdt, _ptr(zeros), group, _ptr(Y), ydt, algo,
-             ctypes.byref(used), _stream(dev))
+    cargs = (X.data_ptr(), xdt, M, N, K, _on(dev, codes, torch.uint8, "codes", (N, K // 2)),
+             _on(dev, scales, scales.dtype, "scales", (N, groups)), sdt,
+             None if zeros is None else _on(dev, zeros, torch.uint8, "zeros", (N, groups)), group,
+             _on(dev, Y, Y.dtype, "Y", (M, N)), ydt, algo, ctypes.byref(used))
     out = _run_on(dev, "gemv_int4", cargs, prepare, (X, codes, scales, zeros, used), Y)
     return (out[0], (Y, used)) if prepare else (Y, used.value)
 
@@ -609,24 +620,20 @@ def moe_grouped_gemv_int4(X, row_token, expert_offsets, R, codes, scales, zeros=
     [x_rows, K]; row_token int32 [R] or None (identity); expert_offsets int32 [E+1]; codes u8 [E, N, K/2], scales
     bf16 or f16 and zeros u8 (or None: 8) [E, N, ceil(K/group)]. Returns (Y [R, N], or [R, N/2] for
     EPI_SILU_GATE, algorithm that ran); rows of no expert keep what Y held."""
-    x_rows, K = _dims(X, 2, "X")
-    E, N, _ = _dims(codes, 3, "codes")
+    (x_rows, K), dev, xdt = _first(X, 2, "X", _HALVES)
     groups = _int4_group(K, group)
-    xdt, sdt = _dtype(X, "X", _HALVES), _dtype(scales, "scales", _HALVES)
-    _need(X, X.dtype, "X"); _need(expert_offsets, torch.int32, "expert_offsets", (E + 1,))
-    if row_token is not None:
-        _need(row_token, torch.int32, "row_token", (R,))
-    _need(codes, torch.uint8, "codes", (E, N, K // 2)); _need(scales, scales.dtype, "scales", (E, N, groups))
-    if zeros is not None:
-        _need(zeros, torch.uint8, "zeros", (E, N, groups))
-    dev = X.device
+    (E, N, _), _, _ = _first(codes, 3, "codes", _BYTES)
+    sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
     ncols = N // 2 if epilogue == EPI_SILU_GATE else N
     Y = Y if Y is not None else torch.empty((R, ncols), dtype=y_dtype, device=dev)
-    ydt = _dtype(Y, "Y", _ANY)
-    _need(Y, Y.dtype, "Y", (R, ncols))
+    ydt = _code(Y.dtype, "Y", _ANY)
     used = ctypes.c_int(-1)
-    cargs = (_ptr(X), xdt, x_rows, _ptr(row_token), _ptr(expert_offsets), E, R, N, K, _ptr(codes), _ptr(scales), sdt,
-             _ptr(zeros), group, epilogue, _ptr(Y), ydt, algo, ctypes.byref(used), _stream(dev))
+    cargs = (X.data_ptr(), xdt, x_rows, None if row_token is None else _on(dev, row_token, torch.int32, "row_token", (R,)),
+             _on(dev, expert_offsets, torch.int32, "expert_offsets", (E + 1,)), E, R, N, K,
+             _on(dev, codes, torch.uint8, "codes", (E, N, K // 2)),
+             _on(dev, scales, scales.dtype, "scales", (E, N, groups)), sdt,
+             None if zeros is None else _on(dev, zeros, torch.uint8, "zeros", (E, N, groups)), group, epilogue,
+             _on(dev, Y, Y.dtype, "Y", (R, ncols)), ydt, algo, ctypes.byref(used))
     out = _run_on(dev, "moe_grouped_gemv_int4", cargs, prepare,
                   (X, row_token, expert_offsets, codes, scales, zeros, used), Y)
     return (out[0], (Y, used)) if prepare else (Y, used.value)
@@ -636,69 +643,64 @@ def moe_grouped_gemv_int4(X, row_token, expert_offsets, R, codes, scales, zeros=
 # tokens to expert order and back, and the gradients
 
 
-def _entries(row_of, T, topk_weights):
-    """k of a routing of T tokens, from its row_of [T*k] and weights [T, k]."""
-    F, = _dims(_need(row_of, torch.int32, "row_of"), 1, "row_of")
+def _entries(dev, row_of, T, topk_weights):
+    """(k, address of row_of [T*k], address of the weights [T, k] or None) of a routing of T tokens."""
+    if not isinstance(row_of, torch.Tensor) or row_of.dim() != 1:
+        raise ValueError("row_of must be a tensor of one dimension")
+    F = row_of.shape[0]
     if topk_weights is not None:
-        k = _dims(topk_weights, 2, "topk_weights")[1]
-        _need(topk_weights, torch.float32, "topk_weights", (T, k))
+        if not isinstance(topk_weights, torch.Tensor) or topk_weights.dim() != 2:
+            raise ValueError("topk_weights must be a tensor of two dimensions")
+        k = topk_weights.shape[1]
+        w = _on(dev, topk_weights, torch.float32, "topk_weights", (T, k))
     else:
-        k = F // T if T > 0 else 1
-    if F != T * k:
-        raise ValueError(f"row_of has {F} entries, not {T} tokens times {k}")
-    return k
+        k, w = F // T if T > 0 else 1, None
+    return k, _on(dev, row_of, torch.int32, "row_of", (T * k,)), w
 
 
 def moe_permute(X, row_of, topk_weights=None, R=None, Xp=None, prepare=False):
     """Tokens to expert order: Xp[row_of[t*k+j]] = topk_weights[t, j] * X[t] (no weights: a copy). X f32, bf16 or
     f16 [T, D]; row_of int32 [T*k] as moe_route gives it (entries outside [0, R) have no row). Returns Xp [R, D]
     of X's type, R = T*k unless given; rows that no entry owns keep what Xp held."""
-    T, D = _dims(X, 2, "X")
-    k = _entries(row_of, T, topk_weights)
-    dt = _dtype(_need(X, X.dtype, "X"), "X", _ANY)
+    (T, D), dev, dt = _first(X, 2, "X", _ANY)
+    k, ro, w = _entries(dev, row_of, T, topk_weights)
     R = R if R is not None else (T * k if Xp is None else Xp.shape[0])
-    Xp = Xp if Xp is not None else torch.empty((R, D), dtype=X.dtype, device=X.device)
-    _need(Xp, X.dtype, "Xp", (R, D))
-    cargs = (_ptr(X), dt, T, k, D, _ptr(row_of), _ptr(topk_weights), R, _ptr(Xp), _stream(X.device))
-    return _run_on(X.device, "moe_permute", cargs, prepare, (X, row_of, topk_weights), Xp)
+    Xp = Xp if Xp is not None else torch.empty((R, D), dtype=X.dtype, device=dev)
+    cargs = (X.data_ptr(), dt, T, k, D, ro, w, R, _on(dev, Xp, X.dtype, "Xp", (R, D)))
+    return _run_on(dev, "moe_permute", cargs, prepare, (X, row_of, topk_weights), Xp)
+
+
+def _dweights(dev, dweights, other, name, dtype, shape, T, k):
+    """(address of `other` or None, the weights' gradient or None, its address or None)."""
+    if other is None:
+        if dweights is not None:
+            raise ValueError(f"dweights needs {name}")
+        return None, None, None
+    dweights = dweights if dweights is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    return _on(dev, other, dtype, name, shape), dweights, _on(dev, dweights, torch.float32, "dweights", (T, k))
 
 
 def moe_permute_backward(dXp, row_of, T, topk_weights=None, X=None, dX=None, dweights=None, prepare=False):
     """Gradient of moe_permute for T tokens from dXp [R, D]: (dX [T, D] of dXp's type, dweights f32 [T, k]).
     The weights' gradient needs the forward's X; without X it is None."""
-    R, D = _dims(dXp, 2, "dXp")
-    k = _entries(row_of, T, topk_weights)
-    dt = _dtype(_need(dXp, dXp.dtype, "dXp"), "dXp", _ANY)
-    dev = dXp.device
+    (R, D), dev, dt = _first(dXp, 2, "dXp", _ANY)
+    k, ro, w = _entries(dev, row_of, T, topk_weights)
     dX = dX if dX is not None else torch.empty((T, D), dtype=dXp.dtype, device=dev)
-    _need(dX, dXp.dtype, "dX", (T, D))
-    dweights = _dweights(dweights, X, "X", dXp.dtype, (T, D), T, k, dev)
-    cargs = (_ptr(dXp), dt, R, _ptr(row_of), _ptr(topk_weights), T, k, D, _ptr(X), _ptr(dX), _ptr(dweights),
-             _stream(dev))
+    x, dweights, dw = _dweights(dev, dweights, X, "X", dXp.dtype, (T, D), T, k)
+    cargs = (dXp.data_ptr(), dt, R, ro, w, T, k, D, x, _on(dev, dX, dXp.dtype, "dX", (T, D)), dw)
     return _run_on(dev, "moe_permute_backward", cargs, prepare, (dXp, row_of, topk_weights, X), (dX, dweights))
-
-
-def _dweights(dweights, other, name, dtype, shape, T, k, dev):
-    if other is None:
-        if dweights is not None:
-            raise ValueError(f"dweights needs {name}")
-        return None
-    _need(other, dtype, name, shape)
-    dweights = dweights if dweights is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
-    return _need(dweights, torch.float32, "dweights", (T, k))
 
 
 def moe_unpermute(Yp, row_of, T, topk_weights=None, out_dtype=None, out=None, prepare=False):
     """Expert rows back to T tokens: out[t] = sum_j topk_weights[t, j] * Yp[row_of[t*k+j]] (no weights: the plain
     sum), summed in f32. Yp f32, bf16 or f16 [R, D]; out [T, D] of Yp's type unless out_dtype is float32."""
-    R, D = _dims(Yp, 2, "Yp")
-    k = _entries(row_of, T, topk_weights)
-    ydt = _dtype(_need(Yp, Yp.dtype, "Yp"), "Yp", _ANY)
+    (R, D), dev, ydt = _first(Yp, 2, "Yp", _ANY)
+    k, ro, w = _entries(dev, row_of, T, topk_weights)
     if out is None:
-        out = torch.empty((T, D), dtype=out_dtype if out_dtype is not None else Yp.dtype, device=Yp.device)
-    odt = _dtype(_need(out, out.dtype, "out", (T, D)), "out", (torch.float32, Yp.dtype))
-    cargs = (_ptr(Yp), ydt, R, _ptr(row_of), _ptr(topk_weights), T, k, D, _ptr(out), odt, _stream(Yp.device))
-    return _run_on(Yp.device, "moe_unpermute", cargs, prepare, (Yp, row_of, topk_weights), out)
+        out = torch.empty((T, D), dtype=out_dtype if out_dtype is not None else Yp.dtype, device=dev)
+    odt = _code(out.dtype, "out", (torch.float32, Yp.dtype))
+    cargs = (Yp.data_ptr(), ydt, R, ro, w, T, k, D, _on(dev, out, out.dtype, "out", (T, D)), odt)
+    return _run_on(dev, "moe_unpermute", cargs, prepare, (Yp, row_of, topk_weights), out)
 
 
 def moe_unpermute_backward(dout, row_of, R, topk_weights=None, Yp=None, y_dtype=None, dYp=None, dweights=None,
@@ -706,18 +708,15 @@ def moe_unpermute_backward(dout, row_of, R, topk_weights=None, Yp=None, y_dtype=
     """Gradient of moe_unpermute (and of moe_combine) from dout [T, D]: (dYp [R, D], dweights f32 [T, k]). dYp has
     y_dtype (dout's type unless given), or Yp's type; the weights' gradient needs the forward's Yp; without Yp it
     is None. Rows that no entry owns keep what dYp held."""
-    T, D = _dims(dout, 2, "dout")
-    k = _entries(row_of, T, topk_weights)
-    dev = dout.device
+    (T, D), dev, odt = _first(dout, 2, "dout", _ANY)
+    k, ro, w = _entries(dev, row_of, T, topk_weights)
     if y_dtype is None:
         y_dtype = Yp.dtype if Yp is not None else dYp.dtype if dYp is not None else dout.dtype
-    ydt = _dtype(y_dtype, "dYp", _ANY)
-    odt = _dtype(_need(dout, dout.dtype, "dout"), "dout", (torch.float32, y_dtype))
+    ydt = _code(y_dtype, "dYp", _ANY)
+    _code(dout.dtype, "dout", (torch.float32, y_dtype))
     dYp = dYp if dYp is not None else torch.empty((R, D), dtype=y_dtype, device=dev)
-    _need(dYp, y_dtype, "dYp", (R, D))
-    dweights = _dweights(dweights, Yp, "Yp", y_dtype, (R, D), T, k, dev)
-    cargs = (_ptr(dout), odt, T, k, D, _ptr(row_of), _ptr(topk_weights), R, _ptr(Yp), _ptr(dYp), ydt, _ptr(dweights),
-             _stream(dev))
+    y, dweights, dw = _dweights(dev, dweights, Yp, "Yp", y_dtype, (R, D), T, k)
+    cargs = (dout.data_ptr(), odt, T, k, D, ro, w, R, y, _on(dev, dYp, y_dtype, "dYp", (R, D)), ydt, dw)
     return _run_on(dev, "moe_unpermute_backward", cargs, prepare, (dout, row_of, topk_weights, Yp), (dYp, dweights))
 
 
