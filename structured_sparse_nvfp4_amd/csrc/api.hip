@@ -492,13 +492,13 @@ int check_scales(const char* fn, const uint16_t* scales) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
-// the products address 16 weight rows with 32-bit byte offsets
-constexpr int64_t kMaxInt4K = (int64_t)1 << 20;
+// the products address 16 weight rows with 32-bit byte offsets, and sets of rows by the grid
+constexpr int64_t kMaxInt4K = (int64_t)1 << 20, kMaxInt4Rows = (int64_t)1 << 24;
 
 int gemv_int4_common(const char* fn, ssn::Int4GemvArgs a, void* stream) {
   int st;
   if ((st = check_nk(fn, a.N, a.K))) return st;
-  if (a.M < 0 || a.M > kMaxRows || a.x_rows < 0 || a.x_rows > kMaxRows)
+  if (a.M < 0 || a.M > kMaxInt4Rows || a.x_rows < 0 || a.x_rows > kMaxRows)
     return fail(SSN_E_SHAPE, "%s: bad row counts (%lld of Y, %lld of X)", fn, (long long)a.M, (long long)a.x_rows);
   if ((st = check_group(fn, a.group))) return st;
   if ((st = check_type(fn, a.x_type, "x_dtype", false)) || (st = check_type(fn, a.s_type, "s_dtype", false)) ||

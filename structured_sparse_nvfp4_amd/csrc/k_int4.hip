@@ -443,26 +443,19 @@ hipError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, 
 
 namespace {
 
-#ifndef WG_CU
-#define WG_CU (16 / W > 0 ? 16 / W : 1)
-#endif
-#ifndef GP
-#define GP 2
-#endif
-#ifndef D4
-#define D4 1
-#endif
-#ifndef D2
-#define D2 1
-#endif
-template <bool F16X, int P, int C, int FOLD, int D, bool GROUPED, bool SILU>
+template <bool F16X, int P, int C, int FOLD, bool GROUPED, bool SILU>
 hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
   constexpr int ROWS = 16 / P;
+  // Units in flight per wave. With the activations of 16 rows in registers a compute unit holds 16 waves, which need
+  // two units each to keep the memory busy; with fewer rows a second unit in flight was slower (N = 13824,
+  // K = 5120, M = 1: 11.0 against 12.5 us), and with four chunks of 16 rows there is no room for one.
+  constexpr int D = P == 1 && C < 4 ? 2 : 1;
   const int nch = (int)((a.K + kChunk - 1) / kChunk), W = (nch + C - 1) / C;
-  const int64_t No = SILU ? a.N / 2 : a.N;
-  const int tiles = (int)((No + 15) / 16);
-  const int64_t wgs = (int64_t)cu_count() * WG_CU;
-  // grouped: at least a workgroup for every slot that there may be (each expert's last may be partial)
+  const int tiles = (int)(((SILU ? a.N / 2 : a.N) + 15) / 16);
+  // As many workgroups as give a compute unit some 16 waves: more (20 or 24 waves) start more often from cold
+  // activations than they hide (N = 13824, K = 5120, M = 8: 13.1 against 17.0 us).
+  const int64_t wgs = (int64_t)cu_count() * std::max(1, 16 / W);
+  // grouped: a workgroup at least for every slot that there may be (each expert's last may be partial)
   const int64_t grid = GROUPED ? std::max<int64_t>(2 * wgs, std::min<int64_t>(a.E, a.M) + a.M / ROWS)
                                : std::min<int64_t>(wgs, tiles);
   hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, GROUPED, SILU>), dim3((unsigned)grid), dim3(W * 64),
@@ -470,20 +463,25 @@ hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Chunks per wave (C) so that at most 16 waves cover K; rows per workgroup (16 / P) by how many there are.
+// With experts the rows of each are few but unknown here, and sets of eight serve best over routings: against
+// sets of four and sixteen, 32 tokens to 10 of 512 experts took 58, 57 and 58 us (gate and up, K = 2048),
+// to 10 of 20 experts 20.7, 28 and 21 us, one token 7.3, 7.3 and 9.0 us.
 template <bool F16X, int FOLD, bool GROUPED, bool SILU>
 hipError_t launch_rows_c(const Int4GemvArgs& a, hipStream_t s) {
   const int nch = (int)((a.K + kChunk - 1) / kChunk);
-  if (a.M <= 4 || (GROUPED && GP == 4)) {
-    if (nch <= 64) return launch_rows_t<F16X, 4, 4, FOLD, D4, GROUPED, SILU>(a, s);
-    return launch_rows_t<F16X, 4, 8, FOLD, 1, GROUPED, SILU>(a, s);
+  if (a.M <= 4) {
+    if (nch <= 64) return launch_rows_t<F16X, 4, 4, FOLD, GROUPED, SILU>(a, s);
+    return launch_rows_t<F16X, 4, 8, FOLD, GROUPED, SILU>(a, s);
   }
-  if (a.M <= 8 || (GROUPED && GP == 2)) return launch_rows_t<F16X, 2, 4, FOLD, D2, GROUPED, SILU>(a, s);
-  if constexpr (!GROUPED || GP == 1) {
-  if (nch <= 32) return launch_rows_t<F16X, 1, 2, FOLD, 2, GROUPED, SILU>(a, s);
-  if (nch <= 48) return launch_rows_t<F16X, 1, 3, FOLD, 2, GROUPED, SILU>(a, s);
-  return launch_rows_t<F16X, 1, 4, FOLD, 1, GROUPED, SILU>(a, s);
+  if constexpr (GROUPED) {
+    return launch_rows_t<F16X, 2, 4, FOLD, true, SILU>(a, s);
+  } else {
+    if (a.M <= 8) return launch_rows_t<F16X, 2, 4, FOLD, false, false>(a, s);
+    if (nch <= 32) return launch_rows_t<F16X, 1, 2, FOLD, false, false>(a, s);
+    if (nch <= 48) return launch_rows_t<F16X, 1, 3, FOLD, false, false>(a, s);
+    return launch_rows_t<F16X, 1, 4, FOLD, false, false>(a, s);
   }
-  return hipSuccess;
 }
 
 template <bool F16X, int FOLD>
@@ -506,8 +504,12 @@ hipError_t launch_rows(const Int4GemvArgs& a, hipStream_t s) {
 hipError_t launch_int4_gemv(const Int4GemvArgs& args, hipStream_t s) {
   Int4GemvArgs a = args;
   if (a.group >= a.K) a.group = (a.K + kChunk - 1) / kChunk * kChunk;   // one group: any length past K's end
-  const bool fits = a.K <= 64 * kChunk || (a.M <= 4 && a.K <= 128 * kChunk);
-  if (!fits || (!a.offsets && a.M > 16)) return launch_int4_wide(a, s);
+  // what the registers of 16 waves hold: 64 chunks of K, or 128 where four rows share an operand
+  const bool fits = a.K <= (a.M <= 4 ? 128 : 64) * kChunk;
+  // 9 to 16 rows take long to bring into registers, which pays from four tiles of weight rows per compute unit
+  // on (K = 5120, M = 16: N = 13824 18.1 against 16.9 us with the other kernel, N = 24576 22.9 against 30.0 us)
+  const bool pays = a.offsets || a.M <= 8 || (a.M <= 16 && a.N >= 4 * 16 * (int64_t)cu_count());
+  if (!fits || !pays) return launch_int4_wide(a, s);
   return a.x_type == kF16 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
 }
 

@@ -21,7 +21,7 @@ namespace {
 constexpr int kWaves = 8;
 
 template <bool F16X, int MT, int NT, int FOLD, bool GROUPED, bool SILU>
-__global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, int ngroups) {
+__global__ __launch_bounds__(kWaves * 64, !GROUPED && MT * NT <= 2 ? 4 : 2) void k_int4_wide(Int4GemvArgs a, int ngroups) {
   constexpr int SPANS = 4 / FOLD, H = SILU ? 2 : 1;
   // A wave's activations: 256 bytes per row, in 16 pieces, piece p of row r at place p ^ swizzle(r). The LDS
   // serves a 16-byte read in groups of lanes like 0-3, 12-15, 20-27: rows 0-3 and 12-15 of one piece and
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
     };
     // Scales and zero points: lane group g loads span g of the four spans from chunk c on, FOLD chunks' worth
     // (a load of its own for every chunk costs the address unit as much as the codes)
-    uint32_t sc[NT], zp[NT], sz[NT];
+    uint32_t sc[NT], zp[NT], sz[NT] = {};
     auto load_sz = [&](int c) __attribute__((always_inline)) {
       const int k = kChunk * c + 32 * FOLD * kq;
       const uint32_t go = c < c_hi && k < K ? (uint32_t)(r16 * groups + k / 32 / g32) : kOutside / 2;
@@ -129,9 +129,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int4_wide(Int4GemvArgs a, in
       __builtin_amdgcn_s_waitcnt(0xC07F);     // read, before they are written over
       asm volatile("" ::: "memory");
       const int phase = (c - c_lo) % FOLD;    // of the chunks that share a load of scales
-      if (phase == 0)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sz[t] = sc[t] | (zp[t] + z_add) << 16;
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t fresh = sc[t] | (zp[t] + z_add) << 16;
+        sz[t] = phase == 0 ? fresh : sz[t];
+      }
       if (phase == FOLD - 1) load_sz(c + 1);
       load(nxt, c + 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -246,10 +248,16 @@ hipError_t launch_wide(const Int4GemvArgs& a, hipStream_t s) {
 
 template <bool F16X, int MT, int FOLD>
 hipError_t launch_wide_n(const Int4GemvArgs& a, hipStream_t s) {
+  // Tiles of 64 weight rows read the activations least often, smaller ones fill the chip with few weight rows.
   const int64_t tiles = (a.N + 15) / 16 * ((a.M + 16 * MT - 1) / (16 * MT)), cus = cu_count();
+  // the fewest: two sets of 32 rows of Y side by side on a compute unit rather than one of 64 (N = 4097, K = 5152,
+  // M = 50: 21.0 against 23.2 us)
+  if constexpr (MT == 4)
+    if (tiles < 3 * cus / 2) return launch_wide_n<F16X, 2, FOLD>(a, s);
   if (tiles >= 3 * cus) return launch_wide<F16X, MT, 4, FOLD, false, false>(a, s);
   if (tiles >= 3 * cus / 2) return launch_wide<F16X, MT, 2, FOLD, false, false>(a, s);
-  return launch_wide<F16X, MT, 1, FOLD, false, false>(a, s);
+  if constexpr (MT < 4) return launch_wide<F16X, MT, 1, FOLD, false, false>(a, s);
+  return hipErrorInvalidValue;   // not reached: few tiles of four row tiles went to two
 }
 
 template <bool F16X, int FOLD>

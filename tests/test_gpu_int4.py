@@ -196,6 +196,69 @@ def test_gemv_beyond_4_gib_of_codes():
     check_product(got[:, rows], want, int4.product_error(B, K, 1024), "f32")
 
 
+def sampled_case(M, N, K, group, asym, x_type="bf16", s_type="bf16", y_type="f32"):
+    """A product too large for the oracle, checked on weight rows spread over all of it, the last among them."""
+    g = torch.Generator(device="cuda").manual_seed(N + K + M)
+    groups = -(-K // group)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand((N, groups), generator=g, device="cuda") * 0.01).to(TYPES[s_type])
+    zeros = torch.randint(0, 16, (N, groups), generator=g, device="cuda", dtype=torch.uint8) if asym else None
+    x, X = make_x(np.random.default_rng(M), (M, K), x_type)
+    Y = torch.full((M, N), float("nan"), dtype=TYPES[y_type], device="cuda")
+    ssn.gemv_int4(X, codes, scales, zeros, group=group, Y=Y)
+    assert bool(torch.isfinite(Y).all())
+    rows = torch.unique(torch.cat((torch.arange(0, N, max(1, N // 40)), torch.arange(max(0, N - 20), N)))).cuda()
+    q, s = int4.unpack(codes[rows].cpu().numpy()), np64(scales[rows])
+    z = zeros[rows].cpu().numpy().astype(np.int64) if asym else np.full(s.shape, 8)
+    want, B = int4.product(x, q, s, z, group)
+    check_product(Y[:, rows], want, int4.product_error(B, K, group), y_type)
+
+
+# 9 to 16 rows over many weight rows (activations in registers, one operand per row set); more waves and chunks
+@pytest.mark.parametrize("M", [9, 16])
+@pytest.mark.parametrize("K,group", [(96, 32), (1024, 128), (4096, 64), (4224, 128), (5152, 64), (6272, 32), (8192, 128),
+                                     (8160, 96), (7200, 7200)])
+def test_gemv_many_weight_rows(M, K, group):
+    sampled_case(M, 16500, K, group, True, *(("f16", "bf16", "f16") if K == 4224 else ()))
+
+
+# tiles of 16, 32 and 64 weight rows times one, two and four row tiles
+@pytest.mark.parametrize("M", [12, 20, 64, 130])
+@pytest.mark.parametrize("N", [100, 6200, 12300])
+@pytest.mark.parametrize("K,group", [(160, 64), (1056, 96), (2048, 128), (2080, 128)])
+def test_gemv_tile_shapes(M, N, K, group):
+    sampled_case(M, N, K, group, K != 1056, "f16" if N == 6200 else "bf16")
+
+
+@pytest.mark.parametrize("M", [1, 4, 5, 16])
+@pytest.mark.parametrize("K,group", [(8224, 32), (12320, 128), (16352, 64), (16384, 16384), (16416, 96), (40000, 128)])
+def test_gemv_long_rows(M, K, group):
+    sampled_case(M, 70, K, group, True)
+
+
+def test_gemv_at_the_longest_row():
+    sampled_case(2, 3, 1 << 20, 128, True)
+
+
+def test_two_products_at_once():
+    """Two streams, other inputs: nothing is shared between calls."""
+    rng = np.random.default_rng(12)
+    sets = []
+    for i in range(2):
+        _, dev = make_weights(rng, (2048,), 1024, 128, True, "bf16")
+        sets.append((make_x(rng, (6 + 12 * i, 1024), "bf16")[1], dev, torch.cuda.Stream()))
+    want = [ssn.gemv_int4(X, *dev)[0] for X, dev, _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (X, dev, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                got[i].append(ssn.gemv_int4(X, *dev)[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
 # ------------------------------------------------------------------------------ grouped product
 def grouped_case(counts, R, x_rows, N, K, group, asym, silu, x_type="bf16", s_type="bf16", y_type="f32", gather=True):
     """counts: rows of each expert; R >= their sum (rows behind them belong to no expert)."""
@@ -240,6 +303,19 @@ def test_grouped_columns(N, silu):
 @pytest.mark.parametrize("silu", [False, True])
 def test_grouped_lengths(K, group, silu):
     grouped_case([1, 2, 0, 18], 21, 21, 64, K, group, True, silu, "bf16", "f16", "bf16", gather=False)
+
+
+@pytest.mark.parametrize("K,group", [(8224, 32), (12320, 96), (16416, 128), (8320, 8320)])
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_long_rows(K, group, silu, gather):
+    grouped_case([3, 0, 18], 22, 22, 34, K, group, True, silu, "bf16", "f16", "bf16", gather=gather)
+    grouped_case([1, 2], 3, 3, 34, K, group, False, silu, "f16", "f16", "f32", gather=gather)
+
+
+def test_grouped_unequal_experts():
+    """One expert with most rows beside many with one: sets of rows are dealt to workgroups on the device."""
+    grouped_case([1] * 30 + [700] + [0] * 20 + [1] * 13, 743, 40, 64, 128, 64, True, True)
 
 
 def test_grouped_many_experts():
@@ -310,6 +386,16 @@ def test_prepared_calls_streams_and_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+def test_misaligned_tensors_are_refused():
+    X = torch.zeros((3, 32), dtype=torch.bfloat16, device="cuda").view(-1)[8:72]     # 16 bytes on: aligned
+    c, s = torch.zeros((4, 16), dtype=torch.uint8, device="cuda"), torch.zeros((4, 1), dtype=torch.bfloat16, device="cuda")
+    ssn.gemv_int4(X.view(2, 32), c, s, group=32)
+    with pytest.raises(ssn.SsnError, match="X.*aligned"):
+        ssn.gemv_int4(torch.zeros(65, dtype=torch.bfloat16, device="cuda")[1:].view(2, 32), c, s, group=32)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssn.gemv_int4(torch.zeros((32, 2), dtype=torch.bfloat16, device="cuda").t(), c, s, group=32)
 
 
 def test_tensors_on_two_devices_are_refused():

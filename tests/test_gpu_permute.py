@@ -150,6 +150,36 @@ def test_non_finite_values_reach_only_their_rows():
     assert torch.equal(got[0][keep], clean[0][keep])
 
 
+def test_weights_of_entries_without_a_row_are_not_read():
+    dro = torch.tensor([1, -1, 0, 7], dtype=torch.int32, device="cuda")          # two entries without a row
+    w = torch.tensor([[0.5, float("nan")], [2.0, float("inf")]], device="cuda")
+    Y = torch.ones((2, 10), device="cuda")
+    assert torch.equal(ssn.moe_unpermute(Y, dro, 2, w), torch.tensor([[0.5], [2.0]], device="cuda").expand(2, 10))
+    dX, dw = ssn.moe_permute_backward(Y, dro, 2, w, X=Y)
+    assert torch.equal(dw, torch.tensor([[10.0, 0.0], [10.0, 0.0]], device="cuda")) and bool(torch.isfinite(dX).all())
+    assert torch.equal(ssn.moe_permute(Y, dro, w, R=2)[:, 0], torch.tensor([2.0, 0.5], device="cuda"))
+
+
+def test_two_calls_at_once():
+    rng = np.random.default_rng(10)
+    T, k, D = 300, 6, 520
+    sets = [(torch.from_numpy(routing(rng, T, k, T * k, 0)).cuda(), torch.rand((T, k), device="cuda"),
+             tensor(rng, (T, D), "bf16")[1], tensor(rng, (T * k, D), "bf16")[1], torch.cuda.Stream()) for _ in range(2)]
+
+    def both(ro, w, X, Y):
+        return (*ssn.moe_permute_backward(Y, ro, T, w, X=X), *ssn.moe_unpermute_backward(X, ro, T * k, w, Yp=Y))
+    want = [both(*s[:4]) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(sets):
+            with torch.cuda.stream(s[4]):
+                got[i].append(both(*s[:4]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
 def test_unweighted_permutation_is_a_copy_bit_for_bit():
     bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).cuda()     # every 16-bit pattern, NaNs among them
     for t in (torch.bfloat16, torch.float16):

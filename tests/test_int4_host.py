@@ -48,6 +48,9 @@ CASES = [
     ("gemv_int4", GEMV, dict(X=N0), ssn.SSN_E_NULL), ("gemv_int4", GEMV, dict(Y=N0), ssn.SSN_E_NULL),
     ("gemv_int4", GEMV, dict(scales=N0), ssn.SSN_E_NULL), ("gemv_int4", GEMV, dict(X=at(0x1002)), ssn.SSN_E_ALIGN),
     ("gemv_int4", GEMV, dict(N=1 << 30, K=1 << 30), ssn.SSN_E_SHAPE),
+    ("gemv_int4", GEMV, dict(K=(1 << 20) + 32), ssn.SSN_E_SHAPE), ("gemv_int4", GEMV, dict(M=(1 << 24) + 1), ssn.SSN_E_SHAPE),
+    ("moe_grouped_gemv_int4", GROUPED, dict(R=(1 << 24) + 1), ssn.SSN_E_SHAPE),
+    ("moe_grouped_gemv_int4", GROUPED, dict(K=(1 << 20) + 32), ssn.SSN_E_SHAPE),
     ("moe_grouped_gemv_int4", GROUPED, dict(E=0), ssn.SSN_E_RANGE),
     ("moe_grouped_gemv_int4", GROUPED, dict(E=4096), ssn.SSN_E_RANGE),
     ("moe_grouped_gemv_int4", GROUPED, dict(epi=2), ssn.SSN_E_RANGE),
