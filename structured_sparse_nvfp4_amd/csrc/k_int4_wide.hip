@@ -98,10 +98,11 @@ __global__ __launch_bounds__(kWaves * 64, !GROUPED && MT * NT <= 2 ? 4 : 2) void
         zp[t] = __builtin_amdgcn_raw_buffer_load_b8(buf_rsrc(a.zeros + tile_base(t) * groups, a.zeros ? rows : 0), go, 0, 0);
       }
     };
-    // part t of NT of the direct loads of chunk c
-    auto send_x = [&](int c, int t) __attribute__((always_inline)) {
+    // part j of the kParts of the direct loads of chunk c
+    constexpr int kParts = SPANS * NT;
+    auto send_x = [&](int c, int j) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 4 * MT * t / NT; i < 4 * MT * (t + 1) / NT; ++i) {
+      for (int i = 4 * MT * j / kParts; i < 4 * MT * (j + 1) / kParts; ++i) {
         if constexpr (GROUPED) {
           // a piece past the end of K: the row's first
           const int piece = r16 ^ swizzle(4 * i + xrow);
@@ -146,30 +147,34 @@ __global__ __launch_bounds__(kWaves * 64, !GROUPED && MT * NT <= 2 ? 4 : 2) void
             if (k >= K) x[mt][s] = u32x4{0u, 0u, 0u, 0u};
         }
       }
-      f32x4 sum[SPANS][MT];
-#pragma unroll
-      for (int v = 0; v < SPANS; ++v)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          sum[v][mt] = zero4;
-#pragma unroll
-          for (int i = 0; i < FOLD; ++i) sum[v][mt] = mfma16<F16X>(x[mt][v * FOLD + i], ones, sum[v][mt]);
-        }
+      u32x4 w[NT], szs[NT];                   // codes, and scales and zero points of the chunk's spans, in every lane
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const u32x4 w = FOLD == 4 ? cur.w[t] : transpose4(cur.w[t]);
-        u32x4 szs;                            // of the chunk's spans, in every lane
-        if (FOLD == 1) szs = spread4(sz[t]);
+        w[t] = FOLD == 4 ? cur.w[t] : transpose4(cur.w[t]);
+        if (FOLD == 1) szs[t] = spread4(sz[t]);
         else
 #pragma unroll
           for (int v = 0; v < SPANS; ++v)
-            szs[v] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * (phase * SPANS + v) + r16), (int)sz[t]);
+            szs[t][v] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * (phase * SPANS + v) + r16), (int)sz[t]);
+      }
+      // Span by span, so that only one span's sums of x are held (M = 64, N = 131072, K = 5120 182 us; with all
+      // of them held 190). Activations sent straight to registers come in pieces of 64 bytes and were slower than
+      // through LDS: 21.6 against 18.6 us at M = 20, N = 13824, K = 5120, 24.0 against 20.0 at M = 50, N = 4097.
 #pragma unroll
-        for (int v = 0; v < SPANS; ++v) {
+      for (int v = 0; v < SPANS; ++v) {
+        f32x4 sum[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          sum[mt] = zero4;
+#pragma unroll
+          for (int i = 0; i < FOLD; ++i) sum[mt] = mfma16<F16X>(x[mt][v * FOLD + i], ones, sum[mt]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
           u32x4 op[FOLD];
 #pragma unroll
-          for (int i = 0; i < FOLD; ++i) op[i] = codes_operand_natural<F16X>(w[v * FOLD + i]);
-          const float s = float16_of((uint16_t)(szs[v] & 0xFFFFu), a.s_type), z = (float)(szs[v] >> 16);
+          for (int i = 0; i < FOLD; ++i) op[i] = codes_operand_natural<F16X>(w[t][v * FOLD + i]);
+          const float s = float16_of((uint16_t)(szs[t][v] & 0xFFFFu), a.s_type), z = (float)(szs[t][v] >> 16);
           f32x4 acc[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) acc[mt] = zero4;
@@ -181,19 +186,18 @@ __global__ __launch_bounds__(kWaves * 64, !GROUPED && MT * NT <= 2 ? 4 : 2) void
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tot[t][mt][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[v][mt][i], acc[mt][i]), tot[t][mt][i]);
+              tot[t][mt][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[mt][i], acc[mt][i]), tot[t][mt][i]);
+          // the next chunk's activations, a part at a time; past the share its last chunk again, not used
+          __builtin_amdgcn_sched_barrier(0);
+          send_x(min(c + 1, c_hi - 1), v * NT + t);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        // the next chunk's activations, a part after each tile: in one burst the waves would stand at the
-        // address unit. Past the share: its last chunk again, not used
-        __builtin_amdgcn_sched_barrier(0);
-        send_x(min(c + 1, c_hi - 1), t);
-        __builtin_amdgcn_sched_barrier(0);
       }
     };
     if (c_lo < c_hi) {
       Loads buf[2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) send_x(c_lo, t);
+      for (int j = 0; j < kParts; ++j) send_x(c_lo, j);
       load_sz(c_lo);
       load(buf[0], c_lo);
       __builtin_amdgcn_sched_barrier(0);
