@@ -250,27 +250,46 @@ hipError_t launch_wide(const Int4GemvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool F16X, int MT, int FOLD>
-hipError_t launch_wide_n(const Int4GemvArgs& a, hipStream_t s) {
-  // Tiles of 64 weight rows read the activations least often, smaller ones fill the chip with few weight rows.
-  const int64_t tiles = (a.N + 15) / 16 * ((a.M + 16 * MT - 1) / (16 * MT)), cus = cu_count();
-  // the fewest: two sets of 32 rows of Y side by side on a compute unit rather than one of 64 (N = 4097, K = 5152,
-  // M = 50: 21.0 against 23.2 us)
-  if constexpr (MT == 4)
-    if (tiles < 3 * cus / 2) return launch_wide_n<F16X, 2, FOLD>(a, s);
-  if (tiles >= 3 * cus) return launch_wide<F16X, MT, 4, FOLD, false, false>(a, s);
-  if (tiles >= 3 * cus / 2) return launch_wide<F16X, MT, 2, FOLD, false, false>(a, s);
-  if constexpr (MT < 4) return launch_wide<F16X, MT, 1, FOLD, false, false>(a, s);
-  return hipErrorInvalidValue;   // not reached: few tiles of four row tiles went to two
-}
+// The tile of a product: a compute unit holds one workgroup's sums at a time, so the time is the number of
+// rounds of cu_count() workgroups times a workgroup's own, which grows with its tile. Measured per round at
+// K = 5120, in tenths of a us (more K lengthens all of them alike):
+//   NT            1    2    3    4
+//   16 rows      65   97  125  149
+//   32 rows      80  115  144  172
+//   64 rows           167  198  230
+// The larger tiles cost less per output, the smaller ones leave less of a last round empty: M = 50, N = 5120 takes
+// 14.4 us in one round of 2 x 3 tiles, 16.1 in one of 4 x 2, 19.4 in two of 2 x 2, 22.2 in a third of one of 4 x 4.
+struct Tile {
+  int mt, nt, cost;
+};
+constexpr Tile kTiles[] = {{4, 4, 230}, {4, 3, 198}, {4, 2, 167}, {2, 4, 172}, {2, 3, 144}, {2, 2, 115},
+                           {2, 1, 80},  {1, 4, 149}, {1, 3, 125}, {1, 2, 97},  {1, 1, 65}};
 
 template <bool F16X, int FOLD>
 hipError_t launch_wide_m(const Int4GemvArgs& a, hipStream_t s) {
   if (a.offsets)
     return a.silu ? launch_wide<F16X, 1, 2, FOLD, true, true>(a, s) : launch_wide<F16X, 1, 2, FOLD, true, false>(a, s);
-  if (a.M <= 16) return launch_wide_n<F16X, 1, FOLD>(a, s);
-  if (a.M <= 32) return launch_wide_n<F16X, 2, FOLD>(a, s);
-  return launch_wide_n<F16X, 4, FOLD>(a, s);
+  const int64_t cus = cu_count();
+  const Tile* best = nullptr;
+  int64_t least = 0;
+  for (const Tile& t : kTiles) {
+    const int64_t wgs = (a.M + 16 * t.mt - 1) / (16 * t.mt) * ((a.N + 16 * t.nt - 1) / (16 * t.nt));
+    const int64_t cost = (wgs + cus - 1) / cus * t.cost;
+    if (!best || cost < least) best = &t, least = cost;
+  }
+  switch (4 * best->mt + best->nt) {
+    case 20: return launch_wide<F16X, 4, 4, FOLD, false, false>(a, s);
+    case 19: return launch_wide<F16X, 4, 3, FOLD, false, false>(a, s);
+    case 18: return launch_wide<F16X, 4, 2, FOLD, false, false>(a, s);
+    case 12: return launch_wide<F16X, 2, 4, FOLD, false, false>(a, s);
+    case 11: return launch_wide<F16X, 2, 3, FOLD, false, false>(a, s);
+    case 10: return launch_wide<F16X, 2, 2, FOLD, false, false>(a, s);
+    case 9: return launch_wide<F16X, 2, 1, FOLD, false, false>(a, s);
+    case 8: return launch_wide<F16X, 1, 4, FOLD, false, false>(a, s);
+    case 7: return launch_wide<F16X, 1, 3, FOLD, false, false>(a, s);
+    case 6: return launch_wide<F16X, 1, 2, FOLD, false, false>(a, s);
+    default: return launch_wide<F16X, 1, 1, FOLD, false, false>(a, s);
+  }
 }
 
 template <bool F16X>

@@ -230,6 +230,14 @@ def test_gemv_tile_shapes(M, N, K, group):
     sampled_case(M, N, K, group, K != 1056, "f16" if N == 6200 else "bf16")
 
 
+@pytest.mark.parametrize("M,N", [(13, 1000), (13, 6150), (13, 10230), (13, 12345),      # one row tile, 1 to 4 column tiles
+                                 (29, 4090), (29, 8190), (29, 10230), (29, 12345),     # two
+                                 (61, 8190), (61, 10230), (61, 13801), (130, 12290)])  # four, 2 to 4 column tiles
+@pytest.mark.parametrize("K,group,x_type", [(1184, 32, "f16"), (1184, 64, "bf16"), (1056, 128, "bf16")])
+def test_gemv_row_and_column_tiles(M, N, K, group, x_type):
+    sampled_case(M, N, K, group, True, x_type)
+
+
 @pytest.mark.parametrize("M", [1, 4, 5, 16])
 @pytest.mark.parametrize("K,group", [(8224, 32), (12320, 128), (16352, 64), (16384, 16384), (16416, 96), (40000, 128)])
 def test_gemv_long_rows(M, K, group):
