@@ -400,7 +400,8 @@ int int4_dequantize(const uint8_t* codes, const void* scales, int s_dtype, const
  * weight is rounded. X [M, K] bf16 or f16 (x_dtype); Y [M, N] f32, bf16 or f16 (y_dtype, rounded to
  * nearest even). Any M up to 2^24 and K up to 2^20 are computed; larger M than some 64 are a matrix
  * product, which the tiles of gemm_nvfp4_dense are made for and this call is not. A non-finite X[m, k]
- * makes row m of Y non-finite.
+ * makes row m of Y non-finite, and so may activations whose sum times 255 over a group passes the range of
+ * f32, whatever the scale (no f16, and bf16 beyond some 2^100).
  * algo: AUTO or MFMA, reported in *algo_used (host, nullable).
  * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE (group), HIP.
  * ------------------------------------------------------------------------------------------- */
@@ -413,8 +414,7 @@ int gemv_int4(const void* X, int x_dtype, int64_t M, int64_t N, int64_t K, const
  *   Y[r, :] = X[src(r), :] . W_hat_e^T  for r in [offsets[e], offsets[e+1]),
  * src(r) = row_token[r], or r where row_token is NULL; weights [E, N, ...] per expert. For routings with
  * few rows per expert: an expert's weights stream once per 8 of its rows (R up to 2^24, K up to
- * 2^20). Epilogue (SSN_EPI_NONE,
- * SSN_EPI_SILU_GATE), x_rows, R and the clamping of offsets into [0, R] and of source rows into
+ * 2^20). Epilogue (SSN_EPI_NONE, SSN_EPI_SILU_GATE), x_rows, R and the clamping of offsets into [0, R] and of source rows into
  * [0, x_rows) are those of moe_grouped_gemm_nvfp4; N need only be even for SILU_GATE, and the gate is
  * formed from the f32 sums. Offsets must ascend, as moe_route writes them. Rows of Y that belong to no
  * expert (r >= offsets[E]) are left as they were. algo: AUTO or STREAM, reported in *algo_used (host,

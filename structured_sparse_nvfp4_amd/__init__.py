@@ -559,6 +559,8 @@ def _run_on(dev, fname, cargs, prepare, keep, result):
 def _int4_group(K, group):
     if isinstance(group, bool) or not isinstance(group, int) or group < 32 or group % 32:
         raise ValueError(f"group must be a positive multiple of 32, got {group}")
+    if group >= 1 << 62:                       # the call takes 64 bits
+        raise ValueError(f"group={group} is too large (K gives one group per row)")
     return -(-K // group)
 
 

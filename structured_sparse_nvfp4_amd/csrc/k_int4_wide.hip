@@ -5,8 +5,8 @@
 // of K and keeps the whole tile's sums. Weights go straight to registers, one chunk ahead. The activations
 // of a chunk come through the wave's own LDS by direct loads, which need no registers and read each row's
 // 256 bytes together: they are read at the chunk's start and the next chunk's are sent for at once, to
-// arrive while this one is multiplied. No wave waits for another before the end, where the eight tiles of sums meet in the same
-// LDS, one thread per output.
+// arrive while this one is multiplied. No wave waits for another before the end, where the eight tiles of
+// sums meet in the same LDS, one thread per output.
 //
 // Every weight is decoded once and multiplied by MT operands; every operand of activations serves NT
 // tiles, so a workgroup reads 16 MT K activations from the L2 for 16 NT K weights.

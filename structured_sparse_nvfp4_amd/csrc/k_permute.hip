@@ -98,7 +98,7 @@ __device__ __forceinline__ float wave_sum_last(float v) {
 // Both movements. AT, BT: types of the token and the row side; WT: waves per token; DOT: dw too.
 template <bool GATHER, int AT, int BT, int WT, bool DOT>
 __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
-    // Rows under way together. Against 8 and 16 for 16-bit rows (4096 tokens x 10, D = 2048, bf16): permute
+  // Rows under way together. Against 8 and 16 for 16-bit rows (4096 tokens x 10, D = 2048, bf16): permute
   // 37.6, 38.2, 39.7 us, unpermute 41.5, 44.7, 43.9 us; for f32 rows 4 was 2% slower than 8.
   constexpr int kBatch = BT == kF32 ? 8 : 4;
   constexpr int kTokens = kThreads / (64 * WT);                        // per workgroup

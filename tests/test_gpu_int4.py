@@ -170,6 +170,16 @@ def test_gemv_non_finite_rows_stay_in_their_row(M, bad):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("M", [1, 12, 40])
+def test_gemv_keeps_subnormal_halves(M):
+    """Activations below f16's smallest normal number, 2^-14, count as they are."""
+    rng = np.random.default_rng(M)
+    (q, s, z), dev = make_weights(rng, (40,), 512, 128, True, "f16")
+    X = torch.from_numpy(rng.integers(-1000, 1001, (M, 512)) * 2.0 ** -24).half()
+    want, B = int4.product(np64(X), q, s, z, 128)
+    check_product(ssn.gemv_int4(X.cuda(), *dev)[0], want, int4.product_error(B, 512, 128), "f32")
+
+
 def test_gemv_unaligned_scales_and_zeros():
     """Scales and zero points of one part of a larger array: 2-byte and 1-byte aligned."""
     rng = np.random.default_rng(8)

@@ -146,3 +146,6 @@ def test_binding_refusals():
         ssn.moe_permute(x, torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError, match="dimensions"):
         ssn.moe_unpermute(x[0], torch.zeros(4, dtype=torch.int32), 2)
+    for group in (1 << 62, (1 << 64) + 32):               # beyond the 64 bits of the call
+        with pytest.raises(ValueError, match="too large"):
+            ssn.gemv_int4(x, c, s[:, :1].contiguous(), group=group)
