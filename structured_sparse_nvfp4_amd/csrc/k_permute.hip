@@ -11,9 +11,12 @@
 //
 // Memory-bound: the token side moves once and the row side once. So the work is cut along the tokens, where
 // a token's row is read once for all its slots, and not along the rows, which would read it k times through
-// eight L2s. WT waves share a token (as many as its row has 512 elements, at most four), a lane moves
-// eight elements at a time, and the slots' rows are fetched kBatch together. Rows need not be aligned: the
-// memory system takes 16-byte accesses at any element.
+// eight L2s. WT waves share a token (as many as its row has 512 elements, at most four), a lane moves eight
+// elements at a time (four where f32 rows are only written), and the slots' rows are fetched kBatch together.
+// Lane j of a wave loads slot j's row number and weight, once per token: loaded by the slot's turn, each batch
+// waited for them (8 tokens x 10, D = 2048: permute 4.0 against 3.2 us, 4096 tokens unpermute 41.5 against
+// 38.1). Rows need not be aligned: the memory system takes 16-byte accesses at any element. 4096 tokens x 10,
+// D = 2048, bf16: permute 37.6 us, 4.9 TB/s, where a large copy reaches 5.0.
 #include <algorithm>
 
 #include "common.hpp"
@@ -23,23 +26,23 @@
 namespace ssn {
 namespace {
 
-constexpr int kThreads = 256, kVec = 8;
+constexpr int kThreads = 256;
 
-// eight elements, packed as they lie in memory
-template <int T>
+// V elements, packed as they lie in memory
+template <int T, int V>
 struct Vec {
-  u32x4 w[T == kF32 ? 2 : 1];
+  u32x4 w[T == kF32 ? V / 4 : 1];
 };
 
-// the first n of them (all eight if n >= 8) at element i of p, which is aligned to one element
-template <int T>
-__device__ __forceinline__ Vec<T> load_vec(const void* p, int64_t i, int n) {
-  Vec<T> v = {};
-  if (n >= kVec) {
+// the first n of them (all V if n >= V) at element i of p, which is aligned to one element
+template <int T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const void* p, int64_t i, int n) {
+  Vec<T, V> v = {};
+  if (n >= V) {
     __builtin_memcpy(&v, (const char*)p + i * (T == kF32 ? 4 : 2), sizeof v);
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec - 1; ++j)
+    for (int j = 0; j < V - 1; ++j)
       if (j < n) {
         if constexpr (T == kF32) v.w[j / 4][j % 4] = ((const uint32_t*)p)[i + j];
         else v.w[0][j / 2] |= (uint32_t)((const uint16_t*)p)[i + j] << (16 * (j & 1));
@@ -48,13 +51,13 @@ __device__ __forceinline__ Vec<T> load_vec(const void* p, int64_t i, int n) {
   return v;
 }
 
-template <int T>
-__device__ __forceinline__ void store_vec(void* p, int64_t i, int n, const Vec<T>& v) {
-  if (n >= kVec) {
+template <int T, int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t i, int n, const Vec<T, V>& v) {
+  if (n >= V) {
     __builtin_memcpy((char*)p + i * (T == kF32 ? 4 : 2), &v, sizeof v);
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec - 1; ++j)
+    for (int j = 0; j < V - 1; ++j)
       if (j < n) {
         if constexpr (T == kF32) ((uint32_t*)p)[i + j] = v.w[j / 4][j % 4];
         else ((uint16_t*)p)[i + j] = (uint16_t)(v.w[0][j / 2] >> (16 * (j & 1)));
@@ -62,8 +65,8 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, int n, const Vec<T
   }
 }
 
-template <int T>
-__device__ __forceinline__ float to_f32(const Vec<T>& v, int j) {
+template <int T, int V>
+__device__ __forceinline__ float to_f32(const Vec<T, V>& v, int j) {
   if constexpr (T == kF32) return __uint_as_float(v.w[j / 4][j % 4]);
   const uint32_t w = v.w[0][j / 2];
   if constexpr (T == kBF16) return j & 1 ? bf16_hi(w) : bf16_lo(w);
@@ -71,8 +74,8 @@ __device__ __forceinline__ float to_f32(const Vec<T>& v, int j) {
 }
 
 // two values into elements j and j + 1 (j even)
-template <int T>
-__device__ __forceinline__ void from_f32(Vec<T>& v, int j, float lo, float hi) {
+template <int T, int V>
+__device__ __forceinline__ void from_f32(Vec<T, V>& v, int j, float lo, float hi) {
   if constexpr (T == kF32) {
     v.w[j / 4][j % 4] = __float_as_uint(lo);
     v.w[j / 4][j % 4 + 1] = __float_as_uint(hi);
@@ -98,9 +101,13 @@ __device__ __forceinline__ float wave_sum_last(float v) {
 // Both movements. AT, BT: types of the token and the row side; WT: waves per token; DOT: dw too.
 template <bool GATHER, int AT, int BT, int WT, bool DOT>
 __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
-  // Rows under way together. Against 8 and 16 for 16-bit rows (4096 tokens x 10, D = 2048, bf16): permute
-  // 37.6, 38.2, 39.7 us, unpermute 41.5, 44.7, 43.9 us; for f32 rows 4 was 2% slower than 8.
+  // Rows under way together. 4, 8 and 16 of 16 bits (4096 tokens x 10, D = 2048, bf16): unpermute 38.1, 38.4,
+  // 38.8 us, with dw 76.4, 80.8, 88.7 (permute 38 each); 4 of f32 (2048 x 8, D = 4096) 122.7 against 120.1 us.
   constexpr int kBatch = BT == kF32 ? 8 : 4;
+  // Elements a lane moves at a time. Eight of f32 are two accesses that leave every other 16 bytes to each other:
+  // stores alone run better as whole lines (that f32 permute 63.4 against 72.4 us), loads better in eights
+  // (unpermute 62.1 against 63.1 us, its gradient with dw 120.1 against 126.1).
+  constexpr int kVec = AT == kF32 && BT == kF32 && !GATHER && !DOT ? 4 : 8;
   constexpr int kTokens = kThreads / (64 * WT);                        // per workgroup
   constexpr int kMaxSlots = 64;
   __shared__ float dots[DOT ? kThreads / 64 : 1][DOT ? kMaxSlots : 1];
@@ -111,30 +118,36 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
     const bool live = t < a.T;                  // uniform in a wave; all waves meet at the barriers
     if (DOT)
       for (int j = lane; j < k; j += 64) dots[wave][j] = 0.f;
+    // lane j has slot j's row, -1 for none, and weight
+    int own_row = -1;
+    float own_w = 1.f;
+    if (live && lane < k) {
+      own_row = a.row_of[t * k + lane];
+      if (own_row >= a.R) own_row = -1;
+      if (a.w) own_w = a.w[t * k + lane];
+    }
     if (live)
       for (int d = kVec * (64 * part + lane); d - kVec * lane < D; d += kVec * 64 * WT) {
-        // The row's last eight elements, where eight no longer follow: the lane before has the first `twice`
-        // of them too, and computes the same. Rows under eight elements go element by element.
+        // The row's last kVec elements, where so many no longer follow: the lane before has the first `twice`
+        // of them too, and computes the same. Rows under kVec elements go element by element.
         const bool in = d < D;
         const int at = max(0, min(d, D - kVec)), n = min(D, kVec), twice = d - at;
-        Vec<AT> av = {};
-        if ((!GATHER || DOT) && in) av = load_vec<AT>(a.A, t * D + at, n);
+        Vec<AT, kVec> av = {};
+        if ((!GATHER || DOT) && in) av = load_vec<AT, kVec>(a.A, t * D + at, n);
         float sum[kVec] = {};
         for (int j0 = 0; j0 < k; j0 += kBatch) {
           int row[kBatch];
           float w[kBatch];
-          Vec<BT> bv[kBatch];
+          Vec<BT, kVec> bv[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            const int64_t f = t * k + min(j0 + i, k - 1);
-            row[i] = __builtin_amdgcn_readfirstlane(a.row_of[f]);
-            if (j0 + i >= k || row[i] >= a.R) row[i] = -1;
-            w[i] = a.w ? a.w[f] : 1.f;
+            row[i] = j0 + i < k ? __builtin_amdgcn_readlane(own_row, (j0 + i) & 63) : -1;
+            w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(own_w), (j0 + i) & 63));
           }
           if (GATHER || DOT)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
-              if (row[i] >= 0 && in) bv[i] = load_vec<BT>(a.B, (int64_t)row[i] * D + at, n);
+              if (row[i] >= 0 && in) bv[i] = load_vec<BT, kVec>(a.B, (int64_t)row[i] * D + at, n);
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             if (row[i] < 0) continue;           // no row: nothing moves, dw stays 0
@@ -144,14 +157,14 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
 #pragma unroll
                 for (int q = 0; q < kVec; ++q) sum[q] = __builtin_fmaf(w[i], to_f32(bv[i], q), sum[q]);
               } else {
-                Vec<BT> out;
+                Vec<BT, kVec> out;
                 if (AT == BT && !a.w) {         // a copy: every bit as it is
                   __builtin_memcpy(&out, &av, sizeof out);
                 } else {
 #pragma unroll
                   for (int q = 0; q < kVec; q += 2) from_f32(out, q, w[i] * to_f32(av, q), w[i] * to_f32(av, q + 1));
                 }
-                store_vec<BT>(a.B_out, (int64_t)row[i] * D + at, n, out);
+                store_vec<BT, kVec>(a.B_out, (int64_t)row[i] * D + at, n, out);
               }
               if (DOT)
 #pragma unroll
@@ -165,10 +178,10 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
           }
         }
         if (GATHER && in) {
-          Vec<AT> out;
+          Vec<AT, kVec> out;
 #pragma unroll
           for (int q = 0; q < kVec; q += 2) from_f32(out, q, sum[q], sum[q + 1]);
-          store_vec<AT>(a.A_out, t * D + at, n, out);
+          store_vec<AT, kVec>(a.A_out, t * D + at, n, out);
         }
       }
     if constexpr (DOT) {
