@@ -16,7 +16,7 @@
 // Lane j of a wave loads slot j's row number and weight, once per token: loaded by the slot's turn, each batch
 // waited for them (8 tokens x 10, D = 2048: permute 4.0 against 3.2 us, 4096 tokens unpermute 41.5 against
 // 38.1). Rows need not be aligned: the memory system takes 16-byte accesses at any element. 4096 tokens x 10,
-// D = 2048, bf16: permute 37.6 us, 4.9 TB/s, where a large copy reaches 5.0.
+// D = 2048, bf16: permute 38 us, 4.8 TB/s, where a large copy reaches 5.0.
 #include <algorithm>
 
 #include "common.hpp"
@@ -86,16 +86,21 @@ __device__ __forceinline__ void from_f32(Vec<T, V>& v, int j, float lo, float hi
   }
 }
 
-// the sum of the wave's lanes, in lane 63
-__device__ __forceinline__ float wave_sum_last(float v) {
-  auto add = [&](int moved) { v += __int_as_float(moved); };
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xF, 0xF, false));
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xF, 0xF, false));
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xF, 0xF, false));
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));   // row_bcast 15, 31
-  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
-  return v;
+// The sums of four values over the wave's lanes, one in the last lane of each 16: of v[0], v[2], v[1], v[3]
+// (halves of the wave and then of each half change places, so that one addition serves two values).
+__device__ __forceinline__ float wave_sums(const float* v) {
+  auto swapped = [](bool half, float x, float y) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    const auto r = half ? __builtin_amdgcn_permlane32_swap(a, b, false, false) : __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  float s = swapped(false, swapped(true, v[0], v[1]), swapped(true, v[2], v[3]));
+  auto add = [&](int moved) { s += __int_as_float(moved); };
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x112, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x114, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(s), 0x118, 0xF, 0xF, false));
+  return s;
 }
 
 // Both movements. AT, BT: types of the token and the row side; WT: waves per token; DOT: dw too.
@@ -148,10 +153,11 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
               if (row[i] >= 0 && in) bv[i] = load_vec<BT, kVec>(a.B, (int64_t)row[i] * D + at, n);
+          float dot[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
+            dot[i] = 0.f;
             if (row[i] < 0) continue;           // no row: nothing moves, dw stays 0
-            float dot = 0.f;
             if (in) {
               if constexpr (GATHER) {
 #pragma unroll
@@ -169,13 +175,16 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
               if (DOT)
 #pragma unroll
                 for (int q = 0; q < kVec; ++q)
-                  if (q >= twice) dot = __builtin_fmaf(to_f32(av, q), to_f32(bv[i], q), dot);
-            }
-            if (DOT) {
-              dot = wave_sum_last(dot);
-              if (lane == 63) dots[wave][j0 + i] += dot;
+                  if (q >= twice) dot[i] = __builtin_fmaf(to_f32(av, q), to_f32(bv[i], q), dot[i]);
             }
           }
+          if (DOT)
+#pragma unroll
+            for (int i = 0; i < kBatch; i += 4) {
+              const float s = wave_sums(dot + i);
+              const int j = j0 + i + (lane >> 5 | (lane >> 4 & 1) << 1);
+              if (lane % 16 == 15 && j < k) dots[wave][j] += s;
+            }
         }
         if (GATHER && in) {
           Vec<AT, kVec> out;
