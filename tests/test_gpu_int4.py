@@ -66,6 +66,24 @@ def test_quantize_is_exact(N, K, group, symmetric, s_type, w_type):
     assert np.array_equal(codes.cpu().numpy(), int4.pack(q))
 
 
+@pytest.mark.parametrize("symmetric", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 96, 128, 256, 512, 1024, 2048, 4096])
+def test_quantize_close_to_halves(group, symmetric):
+    """Weights at, and a few bits to either side of, the middle between two codes."""
+    rng = np.random.default_rng(group)
+    K = 2 * group + 32                                    # two groups and a short one
+    W = (rng.integers(-15, 16, (40, K)) + 0.5) * rng.choice([1.0, 0.7], (40, 1))
+    W *= 1 + rng.choice([-1.0, 0.0, 1.0], W.shape) * 2.0 ** -rng.integers(10, 25, W.shape)
+    lo, hi = (-7.0, 7.0) if symmetric else (-7.0, 8.0)    # ranges whose scale is 1, or 0.7 rounded
+    W = np.clip(W, lo, hi)
+    W[:, ::32], W[:, 1::32] = lo, hi
+    W = torch.from_numpy(np.float32(W))
+    q, s, z = int4.quantize(np64(W), group, symmetric, "bf16")
+    codes, scales, zeros = ssn.int4_quantize(W.cuda(), group=group, symmetric=symmetric)
+    assert np.array_equal(np64(scales), s) and (symmetric or np.array_equal(zeros.cpu().numpy(), z))
+    assert np.array_equal(codes.cpu().numpy(), int4.pack(q))
+
+
 @pytest.mark.parametrize("out_type", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("N,K,group,asym,s_type", [(1, 32, 32, True, "bf16"), (17, 2080, 64, True, "f16"),
                                                    (5, 5152, 96, False, "bf16"), (3, 256, 512, True, "f16")])
