@@ -51,10 +51,18 @@ __device__ __forceinline__ Vec<T, V> load_vec(const void* p, int64_t i, int n) {
   return v;
 }
 
-template <int T, int V>
+// STREAM: past the caches
+template <int T, int V, bool STREAM>
 __device__ __forceinline__ void store_vec(void* p, int64_t i, int n, const Vec<T, V>& v) {
   if (n >= V) {
-    __builtin_memcpy((char*)p + i * (T == kF32 ? 4 : 2), &v, sizeof v);
+    if constexpr (STREAM) {
+      typedef u32x4 __attribute__((aligned(2))) loose;
+#pragma unroll
+      for (int j = 0; j < (int)(sizeof v / 16); ++j)
+        __builtin_nontemporal_store(v.w[j], (loose*)((char*)p + i * (T == kF32 ? 4 : 2)) + j);
+    } else {
+      __builtin_memcpy((char*)p + i * (T == kF32 ? 4 : 2), &v, sizeof v);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < V - 1; ++j)
@@ -103,8 +111,9 @@ __device__ __forceinline__ float wave_sums(const float* v) {
   return s;
 }
 
-// Both movements. AT, BT: types of the token and the row side; WT: waves per token; DOT: dw too.
-template <bool GATHER, int AT, int BT, int WT, bool DOT>
+// Both movements. AT, BT: types of the token and the row side; WT: waves per token; DOT: dw too; STREAM: rows
+// are written past the caches.
+template <bool GATHER, int AT, int BT, int WT, bool DOT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
   // Rows under way together. 4, 8 and 16 of 16 bits (4096 tokens x 10, D = 2048, bf16): unpermute 38.1, 38.4,
   // 38.8 us, with dw 76.4, 80.8, 88.7 (permute 38 each); 4 of f32 (2048 x 8, D = 4096) 122.7 against 120.1 us.
@@ -170,7 +179,7 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
 #pragma unroll
                   for (int q = 0; q < kVec; q += 2) from_f32(out, q, w[i] * to_f32(av, q), w[i] * to_f32(av, q + 1));
                 }
-                store_vec<BT, kVec>(a.B_out, (int64_t)row[i] * D + at, n, out);
+                store_vec<BT, kVec, STREAM>(a.B_out, (int64_t)row[i] * D + at, n, out);
               }
               if (DOT)
 #pragma unroll
@@ -190,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
           Vec<AT, kVec> out;
 #pragma unroll
           for (int q = 0; q < kVec; q += 2) from_f32(out, q, sum[q], sum[q + 1]);
-          store_vec<AT, kVec>(a.A_out, t * D + at, n, out);
+          store_vec<AT, kVec, false>(a.A_out, t * D + at, n, out);
         }
       }
     if constexpr (DOT) {
@@ -207,20 +216,31 @@ __global__ __launch_bounds__(kThreads) void k_permute(PermuteArgs a) {
   }
 }
 
-template <bool GATHER, int AT, int BT, bool DOT>
+template <bool GATHER, int AT, int BT, bool DOT, bool STREAM>
 hipError_t launch_wt(const PermuteArgs& a, hipStream_t s) {
   const int wt = a.D <= 512 ? 1 : a.D <= 1024 ? 2 : 4;
   const int64_t tokens = kThreads / 64 / wt, blocks = (a.T + tokens - 1) / tokens;
   const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 22));
-  if (wt == 1) hipLaunchKernelGGL((k_permute<GATHER, AT, BT, 1, DOT>), grid, dim3(kThreads), 0, s, a);
-  else if (wt == 2) hipLaunchKernelGGL((k_permute<GATHER, AT, BT, 2, DOT>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_permute<GATHER, AT, BT, 4, DOT>), grid, dim3(kThreads), 0, s, a);
+  const auto kernel = wt == 1 ? k_permute<GATHER, AT, BT, 1, DOT, STREAM>
+                              : wt == 2 ? k_permute<GATHER, AT, BT, 2, DOT, STREAM> : k_permute<GATHER, AT, BT, 4, DOT, STREAM>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
+}
+
+// Rows that the 256 MB cache does not hold are written past it: 2048 x 8, D = 4096, f32 (268 MB) 53.5 against
+// 63.5 us, 4096 x 10, D = 2048, f32 (336 MB) with the unpermute that reads them 143 against 174 us. Fewer are
+// better found there: bf16 (168 MB) with the unpermute 73.5 against 65.0 us. With dw as many are read, and that
+// f32 gradient took 128.7 against 119.7 us.
+template <bool GATHER, int AT, int BT, bool DOT>
+hipError_t launch_stream(const PermuteArgs& a, hipStream_t s) {
+  if constexpr (!GATHER && !DOT)
+    if (std::min(a.R, a.T * a.k) * a.D >= ((int64_t)256 << 20) / (BT == kF32 ? 4 : 2)) return launch_wt<GATHER, AT, BT, DOT, true>(a, s);
+  return launch_wt<GATHER, AT, BT, DOT, false>(a, s);
 }
 
 template <bool GATHER, int AT, int BT>
 hipError_t launch_dot(const PermuteArgs& a, hipStream_t s) {
-  return a.dw ? launch_wt<GATHER, AT, BT, true>(a, s) : launch_wt<GATHER, AT, BT, false>(a, s);
+  return a.dw ? launch_stream<GATHER, AT, BT, true>(a, s) : launch_stream<GATHER, AT, BT, false>(a, s);
 }
 
 template <bool GATHER>

@@ -94,6 +94,20 @@ def test_dequantize(N, K, group, asym, s_type, out_type):
     assert torch.equal(ssn.int4_dequantize(*dev, group=group, out_dtype=TYPES[out_type]).cpu(), W.to(TYPES[out_type]))
 
 
+@pytest.mark.parametrize("out_type,N", [("f32", 6600), ("bf16", 13100), ("f16", 13100)])
+def test_dequantize_beyond_the_cache(out_type, N):
+    """Output of 128 MB and more, which is written past the caches: whole against f32 arithmetic on the GPU."""
+    K, group = 5152, 96
+    g = torch.Generator(device="cuda").manual_seed(N)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.rand((N, -(-K // group)), generator=g, device="cuda").bfloat16()
+    zeros = torch.randint(0, 256, scales.shape, generator=g, device="cuda", dtype=torch.uint8)
+    got = ssn.int4_dequantize(codes, scales, zeros, group=group, out_dtype=TYPES[out_type])
+    q = torch.stack((codes & 15, codes >> 4), 2).view(N, K).float()
+    spread = lambda v: v.float().repeat_interleave(group, 1)[:, :K]
+    assert torch.equal(got, ((q - spread(zeros)) * spread(scales)).to(TYPES[out_type]))    # at most 17 bits: exact
+
+
 def test_quantize_into_given_tensors_and_back():
     rng = np.random.default_rng(5)
     W = torch.from_numpy(np.float32(rng.standard_normal((33, 320)))).cuda()

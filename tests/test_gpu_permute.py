@@ -216,6 +216,35 @@ def test_rows_beyond_2_gib():
     assert torch.equal(out[2], Xp[1024].float())
 
 
+@pytest.mark.parametrize("T,k,D,t,dout_t", [(2100, 16, 2001, "f32", "f32"), (7000, 16, 601, "f32", "f32"),
+                                            (14000, 16, 301, "f32", "f32"), (4200, 16, 2001, "bf16", "bf16"),
+                                            (4200, 16, 2001, "f16", "f32"), (28000, 16, 303, "bf16", "f32")])
+def test_rows_beyond_the_cache(T, k, D, t, dout_t):
+    """Rows of 268 MB and more, which are written past the caches."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    X = torch.randn((T, D), generator=g, device="cuda").to(TYPES[t])
+    row_of = torch.randperm(T * k, generator=g, device="cuda").int()
+    row_of[5] = -1
+    owned = row_of.long().clamp(min=0)
+    keep = row_of >= 0
+    w = torch.rand((T, k), generator=g, device="cuda") + 0.1
+    Xp = torch.zeros((T * k, D), dtype=TYPES[t], device="cuda")
+    ssn.moe_permute(X, row_of, Xp=Xp)
+    assert torch.equal(Xp[owned[keep]], X.repeat_interleave(k, 0)[keep])
+    dout = torch.randn((T, D), generator=g, device="cuda").to(TYPES[dout_t])
+    dYp, dw = ssn.moe_unpermute_backward(dout, row_of, T * k, w, Yp=Xp)
+    # one product, rounded to the type: to f32 first (half a step 2^-24) or, with halves, in one instruction without
+    half, least = {"f32": (2.0 ** -24, 2.0 ** -150), "bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}[t]
+    for j in range(k):
+        mine = keep.view(T, k)[:, j]
+        want = (w[:, j:j + 1].double() * dout.double())[mine]
+        off = (dYp[owned.view(T, k)[:, j]][mine].double() - want).abs()
+        assert bool((off <= (half * (1 + 2.0 ** -24) + 2.0 ** -24) * want.abs() + least).all())
+    a, b = dout.double(), X.double()
+    err = (D + 16) * 2.0 ** -24 * (a * b).abs().sum(1, keepdim=True)
+    assert bool(((dw - (a * b).sum(1, keepdim=True)).abs() <= err)[keep.view(T, k)].all()) and dw[0, 5] == 0
+
+
 def test_graph_replays():
     rng = np.random.default_rng(9)
     T, k, D = 40, 5, 136
