@@ -505,8 +505,11 @@ hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
   // As many workgroups as give a compute unit some 16 waves: more (20 or 24 waves) start more often from cold
   // activations than they hide (N = 13824, K = 5120, M = 8: 13.1 against 17.0 us).
   const int64_t wgs = (int64_t)cu_count() * std::max(1, 16 / W);
-  // grouped: a workgroup at least for every slot that there may be (each expert's last may be partial)
-  const int64_t grid = GROUPED ? std::max<int64_t>(2 * wgs, std::min<int64_t>(a.E, a.M) + a.M / ROWS)
+  // grouped: a workgroup at least for every slot that there may be (each expert's last may be partial), and
+  // otherwise fewer than the chip holds, as each first finds its slot, token and activations: three quarters of `wgs`
+  // against half and twice as many, 32 tokens to 10 of 512 experts 33.1, 35.9 and 37.3 us (K = 512), 57, 53 and 57
+  // (gate and up, K = 2048), 8 tokens 22, 21 and 26, 32 tokens to 10 of 20 experts 15.4, 15.9 and 20.4 us.
+  const int64_t grid = GROUPED ? std::max<int64_t>(3 * wgs / 4, std::min<int64_t>(a.E, a.M) + a.M / ROWS)
                                : std::min<int64_t>(wgs, tiles);
   hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, GROUPED, SILU>), dim3((unsigned)grid), dim3(W * 64),
                      W == 1 ? 0 : 2 * W * (SILU ? 2 : 1) * 4 * ROWS * 16, s, a, tiles);
@@ -515,8 +518,8 @@ hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
 
 // Chunks per wave (C) so that at most 16 waves cover K; rows per workgroup (16 / P) by how many there are.
 // With experts the rows of each are few but unknown here, and sets of eight serve best over routings: against
-// sets of four and sixteen, 32 tokens to 10 of 512 experts took 58, 57 and 58 us (gate and up, K = 2048),
-// to 10 of 20 experts 20.7, 28 and 21 us, one token 7.3, 7.3 and 9.0 us.
+// sets of four and sixteen, 32 tokens to 10 of 512 experts took 58, 57 and 60 us (gate and up, K = 2048),
+// to 10 of 20 experts 15.4, 20.8 and 17.4 us, one token 7.1, 6.8 and 8.5 us.
 template <bool F16X, int FOLD, bool GROUPED, bool SILU>
 hipError_t launch_rows_c(const Int4GemvArgs& a, hipStream_t s) {
   const int nch = (int)((a.K + kChunk - 1) / kChunk);
