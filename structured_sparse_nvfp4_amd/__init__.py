@@ -522,6 +522,16 @@ def _first(t, n, name, allowed):
     return t.shape, t.device, dt
 
 
+def _size(t, n, name):
+    """Shape of a tensor of n dimensions that _on checks later."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {len(shape)}")
+    return shape
+
+
 def _code(dtype, name, allowed):
     if dtype not in allowed:
         raise TypeError(f"{name} must be one of {', '.join(str(a)[6:] for a in allowed)}, got {dtype}")
@@ -530,6 +540,8 @@ def _code(dtype, name, allowed):
 
 def _on(dev, t, dtype, name, shape):
     """Address of a contiguous tensor of this type and shape on `dev`."""
+    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
@@ -538,9 +550,7 @@ def _on(dev, t, dtype, name, shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _run_on(dev, fname, cargs, prepare, keep, result):
@@ -548,12 +558,20 @@ def _run_on(dev, fname, cargs, prepare, keep, result):
     launches on the device that is current when it is called."""
     if dev.type != "cuda":
         raise ValueError(f"{fname} takes device tensors, got tensors on {dev}")
-    # the raw handle: torch.cuda.current_stream() builds an object, which takes 2 us of a call's 7
+    # A small call's time is the host's: the raw handle and device number take 0.1 us, where
+    # torch.cuda.current_stream() and current_device() take 2.2.
     cargs = (*cargs, torch._C._cuda_getCurrentRawStream(dev.index))
-    if prepare or dev.index == torch.cuda.current_device():
-        return _run(fname, cargs, prepare, keep, result)
-    with torch.cuda.device(dev):
-        return _run(fname, cargs, prepare, keep, result)
+    if prepare:
+        return _run(fname, cargs, True, keep, result)
+    call = getattr(_lib or lib(), fname)
+    if dev.index == torch._C._cuda_getDevice():
+        status = call(*cargs)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*cargs)
+    if status:
+        _check(status)
+    return result
 
 
 def _int4_group(K, group):
@@ -573,10 +591,10 @@ def int4_quantize(W, group=128, symmetric=False, scale_dtype=torch.bfloat16, cod
     groups = _int4_group(K, group)
     if symmetric and zeros is not None:
         raise ValueError("symmetric quantisation has no zeros")
-    codes = codes if codes is not None else torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
-    scales = scales if scales is not None else torch.empty((N, groups), dtype=scale_dtype, device=dev)
+    codes = codes if codes is not None else W.new_empty((N, K // 2), dtype=torch.uint8)
+    scales = scales if scales is not None else W.new_empty((N, groups), dtype=scale_dtype)
     if not symmetric and zeros is None:
-        zeros = torch.empty((N, groups), dtype=torch.uint8, device=dev)
+        zeros = W.new_empty((N, groups), dtype=torch.uint8)
     sdt = _code(scales.dtype, "scales", _HALVES)
     cargs = (W.data_ptr(), wdt, N, K, group, sdt, _on(dev, codes, torch.uint8, "codes", (N, K // 2)),
              _on(dev, scales, scales.dtype, "scales", (N, groups)),
@@ -590,7 +608,7 @@ def int4_dequantize(codes, scales, zeros=None, group=128, out_dtype=torch.float3
     K = 2 * Kh
     groups = _int4_group(K, group)
     sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
-    out = out if out is not None else torch.empty((N, K), dtype=out_dtype, device=dev)
+    out = out if out is not None else codes.new_empty((N, K), dtype=out_dtype)
     odt = _code(out.dtype, "out", _ANY)
     cargs = (codes.data_ptr(), _on(dev, scales, scales.dtype, "scales", (N, groups)), sdt,
              None if zeros is None else _on(dev, zeros, torch.uint8, "zeros", (N, groups)), N, K, group,
@@ -603,9 +621,9 @@ def gemv_int4(X, codes, scales, zeros=None, group=128, y_dtype=torch.float32, al
     scales bf16 or f16 and zeros u8 (or None: 8) [N, ceil(K/group)]. Returns (Y, algorithm that ran)."""
     (M, K), dev, xdt = _first(X, 2, "X", _HALVES)
     groups = _int4_group(K, group)
-    (N, _), _, _ = _first(codes, 2, "codes", _BYTES)
+    N, _ = _size(codes, 2, "codes")
     sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
-    Y = Y if Y is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+    Y = Y if Y is not None else X.new_empty((M, N), dtype=y_dtype)
     ydt = _code(Y.dtype, "Y", _ANY)
     used = ctypes.c_int(-1)
     cargs = (X.data_ptr(), xdt, M, N, K, _on(dev, codes, torch.uint8, "codes", (N, K // 2)),
@@ -624,10 +642,10 @@ def moe_grouped_gemv_int4(X, row_token, expert_offsets, R, codes, scales, zeros=
     EPI_SILU_GATE, algorithm that ran); rows of no expert keep what Y held."""
     (x_rows, K), dev, xdt = _first(X, 2, "X", _HALVES)
     groups = _int4_group(K, group)
-    (E, N, _), _, _ = _first(codes, 3, "codes", _BYTES)
+    E, N, _ = _size(codes, 3, "codes")
     sdt = _code(getattr(scales, "dtype", None), "scales", _HALVES)
     ncols = N // 2 if epilogue == EPI_SILU_GATE else N
-    Y = Y if Y is not None else torch.empty((R, ncols), dtype=y_dtype, device=dev)
+    Y = Y if Y is not None else X.new_empty((R, ncols), dtype=y_dtype)
     ydt = _code(Y.dtype, "Y", _ANY)
     used = ctypes.c_int(-1)
     cargs = (X.data_ptr(), xdt, x_rows, None if row_token is None else _on(dev, row_token, torch.int32, "row_token", (R,)),
@@ -667,7 +685,7 @@ def moe_permute(X, row_of, topk_weights=None, R=None, Xp=None, prepare=False):
     (T, D), dev, dt = _first(X, 2, "X", _ANY)
     k, ro, w = _entries(dev, row_of, T, topk_weights)
     R = R if R is not None else (T * k if Xp is None else Xp.shape[0])
-    Xp = Xp if Xp is not None else torch.empty((R, D), dtype=X.dtype, device=dev)
+    Xp = Xp if Xp is not None else X.new_empty((R, D))
     cargs = (X.data_ptr(), dt, T, k, D, ro, w, R, _on(dev, Xp, X.dtype, "Xp", (R, D)))
     return _run_on(dev, "moe_permute", cargs, prepare, (X, row_of, topk_weights), Xp)
 
@@ -687,7 +705,7 @@ def moe_permute_backward(dXp, row_of, T, topk_weights=None, X=None, dX=None, dwe
     The weights' gradient needs the forward's X; without X it is None."""
     (R, D), dev, dt = _first(dXp, 2, "dXp", _ANY)
     k, ro, w = _entries(dev, row_of, T, topk_weights)
-    dX = dX if dX is not None else torch.empty((T, D), dtype=dXp.dtype, device=dev)
+    dX = dX if dX is not None else dXp.new_empty((T, D))
     x, dweights, dw = _dweights(dev, dweights, X, "X", dXp.dtype, (T, D), T, k)
     cargs = (dXp.data_ptr(), dt, R, ro, w, T, k, D, x, _on(dev, dX, dXp.dtype, "dX", (T, D)), dw)
     return _run_on(dev, "moe_permute_backward", cargs, prepare, (dXp, row_of, topk_weights, X), (dX, dweights))
@@ -699,7 +717,7 @@ def moe_unpermute(Yp, row_of, T, topk_weights=None, out_dtype=None, out=None, pr
     (R, D), dev, ydt = _first(Yp, 2, "Yp", _ANY)
     k, ro, w = _entries(dev, row_of, T, topk_weights)
     if out is None:
-        out = torch.empty((T, D), dtype=out_dtype if out_dtype is not None else Yp.dtype, device=dev)
+        out = Yp.new_empty((T, D), dtype=out_dtype)
     odt = _code(out.dtype, "out", (torch.float32, Yp.dtype))
     cargs = (Yp.data_ptr(), ydt, R, ro, w, T, k, D, _on(dev, out, out.dtype, "out", (T, D)), odt)
     return _run_on(dev, "moe_unpermute", cargs, prepare, (Yp, row_of, topk_weights), out)
@@ -716,7 +734,7 @@ def moe_unpermute_backward(dout, row_of, R, topk_weights=None, Yp=None, y_dtype=
         y_dtype = Yp.dtype if Yp is not None else dYp.dtype if dYp is not None else dout.dtype
     ydt = _code(y_dtype, "dYp", _ANY)
     _code(dout.dtype, "dout", (torch.float32, y_dtype))
-    dYp = dYp if dYp is not None else torch.empty((R, D), dtype=y_dtype, device=dev)
+    dYp = dYp if dYp is not None else dout.new_empty((R, D), dtype=y_dtype)
     y, dweights, dw = _dweights(dev, dweights, Yp, "Yp", y_dtype, (R, D), T, k)
     cargs = (dout.data_ptr(), odt, T, k, D, ro, w, R, y, _on(dev, dYp, y_dtype, "dYp", (R, D)), ydt, dw)
     return _run_on(dev, "moe_unpermute_backward", cargs, prepare, (dout, row_of, topk_weights, Yp), (dYp, dweights))
