@@ -75,6 +75,8 @@ __device__ __forceinline__ float team_max(float v) {
 // written. Two vectors of eight a lane rather than one halve what a lane spends on its group (the range's
 // way across lanes, the scale, the places), 13824 x 5120, group 128: f32 58 against 63 us (5.5 TB/s), bf16 47
 // against 58; group 32, bf16: 49 against 57.
+// Groups beyond 2048 have a workgroup, which holds 8192 weights: one group of 5120 to a row 60 us, with a wave and
+// a second reading 79; 16 rows of 8192 4.2 against 8.7.
 template <int T, int L, int U>
 __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restrict__ W, int64_t teams, int K, int group,
                                                             int groups, uint32_t* __restrict__ codes,
@@ -109,8 +111,21 @@ __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restri
         extend(v);
       }
     }
-    hi = team_max<L>(hi);
-    lo = -team_max<L>(-lo);
+    if constexpr (L <= 64) {
+      hi = team_max<L>(hi);
+      lo = -team_max<L>(-lo);
+    } else {                                   // the workgroup's waves meet in LDS
+      __shared__ float most[2][kThreads / 64];
+      const float h = team_max<64>(hi), m = team_max<64>(-lo);
+      __syncthreads();                         // the group before has been read
+      if (threadIdx.x % 64 == 0) most[0][threadIdx.x / 64] = h, most[1][threadIdx.x / 64] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kThreads / 64; ++i) {
+        hi = fmaxf(hi, most[0][i]);
+        lo = fminf(lo, -most[1][i]);
+      }
+    }
     const double range = zeros ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
     const uint16_t sb = round16_sat(range, st);
     const float s0 = float16_of(sb, st);
@@ -445,7 +460,7 @@ hipError_t launch_quantize_l(const void* W, int64_t N, int64_t K, int64_t group,
   return hipGetLastError();
 }
 
-// lanes per group so that a lane has two vectors of eight of it
+// lanes per group so that a lane has two vectors of eight of it, or four of a long one
 template <int T>
 hipError_t launch_quantize_t(const void* W, int64_t N, int64_t K, int64_t group, uint8_t* codes, uint16_t* scales,
                              int s_type, uint8_t* zeros, hipStream_t s) {
@@ -455,7 +470,8 @@ hipError_t launch_quantize_t(const void* W, int64_t N, int64_t K, int64_t group,
   if (len <= 128) return launch_quantize_l<T, 8, 2>(W, N, K, group, codes, scales, s_type, zeros, s);
   if (len <= 256) return launch_quantize_l<T, 16, 2>(W, N, K, group, codes, scales, s_type, zeros, s);
   if (len <= 512) return launch_quantize_l<T, 32, 2>(W, N, K, group, codes, scales, s_type, zeros, s);
-  return launch_quantize_l<T, 64, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
+  if (len <= 2048) return launch_quantize_l<T, 64, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
+  return launch_quantize_l<T, 256, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
 }
 
 }  // namespace

@@ -67,7 +67,7 @@ def test_quantize_is_exact(N, K, group, symmetric, s_type, w_type):
 
 
 @pytest.mark.parametrize("symmetric", [False, True])
-@pytest.mark.parametrize("group", [32, 64, 96, 128, 256, 512, 1024, 2048, 4096])
+@pytest.mark.parametrize("group", [32, 64, 96, 128, 256, 512, 1024, 2048, 2080, 4096, 8192, 12320])
 def test_quantize_close_to_halves(group, symmetric):
     """Weights at, and a few bits to either side of, the middle between two codes."""
     rng = np.random.default_rng(group)
