@@ -653,10 +653,12 @@ int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, in
   if ((st = check_permute(fn, T, k, D, R)) || (st = check_side_types(fn, yp_dtype, out_dtype, "out_dtype"))) return st;
   if (T == 0) return ok();
   REQUIRE_ELEM_PTR(row_of); REQUIRE_OPT_ELEM_PTR(topk_weights); REQUIRE_OPT_ELEM_PTR(dweights);
-  if (D > 0 && R > 0) {
-    REQUIRE_PTR(dout); REQUIRE_PTR(dYp);
-    if (dweights) REQUIRE_PTR(Yp);
-  } else if (!dweights) return ok();   // no row: only the weights' gradients, all 0, are left to write
+  if ((D == 0 || R == 0) && !dweights) return ok();   // no row: only the weights' gradients, all 0, are left to write
+  if (D > 0) {
+    REQUIRE_PTR(dout);                                // read for dweights also where no entry has a row
+    if (R > 0) REQUIRE_PTR(dYp);
+    if (R > 0 && dweights) REQUIRE_PTR(Yp);
+  }
   ssn::PermuteArgs a{T, D, R, k, out_dtype, yp_dtype, row_of, topk_weights, dout, Yp, nullptr, dYp, dweights};
   return hip_status(ssn::launch_moe_scatter(a, as_stream(stream)), fn);
 }

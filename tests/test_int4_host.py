@@ -117,6 +117,15 @@ def test_permutation_empty_problems_launch_nothing():
     assert _call("moe_unpermute_backward", UNPERMUTE_B, R=0, dw=N0)[0] == ssn.SSN_OK
 
 
+@pytest.mark.parametrize("name,args", [("moe_permute_backward", ("X", "dX")), ("moe_unpermute", ("out",)),
+                                       ("moe_unpermute_backward", ("dout",))])
+def test_token_side_is_checked_without_rows(name, args):
+    """R = 0: the token side still has T rows, and what launches checks it first."""
+    for arg in args:
+        assert _call(name, dict(ALL)[name], R=0, **{arg: N0})[0] == ssn.SSN_E_NULL, arg
+        assert _call(name, dict(ALL)[name], R=0, **{arg: at(0x1008)})[0] == ssn.SSN_E_ALIGN, arg
+
+
 def test_half_type_is_still_refused_by_the_other_calls():
     L = ssn.lib()
     assert L.gemm_nvfp4_dense(P, 2, 4, 64, P, P, P, P, ssn.SSN_F16, 0, N0, N0) == ssn.SSN_E_DTYPE
