@@ -453,7 +453,7 @@ namespace {
 template <int T, int L, int U>
 hipError_t launch_quantize_l(const void* W, int64_t N, int64_t K, int64_t group, uint8_t* codes, uint16_t* scales,
                              int s_type, uint8_t* zeros, hipStream_t s) {
-  const int64_t groups = (K + group - 1) / group, teams = N * groups;
+  const int64_t groups = (K - 1) / group + 1, teams = N * groups;
   const int64_t blocks = std::min<int64_t>((teams + kThreads / L - 1) / (kThreads / L), 1 << 22);
   hipLaunchKernelGGL((k_int4_quantize<T, L, U>), dim3((unsigned)blocks), dim3(kThreads), 0, s, W, teams, (int)K,
                      (int)std::min(group, K), (int)groups, (uint32_t*)codes, scales, s_type, zeros);
@@ -488,7 +488,7 @@ namespace {
 template <int T>
 hipError_t launch_dequantize_t(const uint8_t* codes, const uint16_t* scales, int s_type, const uint8_t* zeros, int64_t N,
                                int64_t K, int64_t group, void* out, hipStream_t s) {
-  const int groups = (int)((K + group - 1) / group);
+  const int groups = (int)((K - 1) / group + 1);
   const int64_t bx = (K / (T == kF32 ? 4 : 8) + kThreads - 1) / kThreads;
   // four rows a lane, and more where the grid would pass its second axis or some 2^20 workgroups
   const int64_t by = std::min<int64_t>({(N + 3) / 4, 65535, std::max<int64_t>(1, (1 << 20) / bx)});

@@ -56,3 +56,24 @@ def test_abi_checks_under_host_sanitizers():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, (r.stdout[-3000:] + r.stderr[-3000:])
     assert " passed" in r.stdout and "skipped" not in r.stdout
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC) or _runtime() is None, reason="hipcc or the ASan runtime is missing")
+def test_largest_group_of_the_int4_calls_under_host_sanitizers():
+    """One group per row whatever `group` beyond K, up to the argument's last multiple of 32: no overflow on the
+    way to the launch, which then finds no device (none is visible here)."""
+    _build()
+    env = dict(os.environ, LD_PRELOAD=_runtime(), ASAN_OPTIONS="detect_leaks=0:halt_on_error=1:abort_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1", HIP_VISIBLE_DEVICES="-1", ROCR_VISIBLE_DEVICES="-1")
+    code = ("import structured_sparse_nvfp4_amd as s\n"
+            f"s.LIB_PATH = {LIB!r}\n"
+            "L, P = s.lib(), 0x1000\n"
+            "for K in (32, 64, 5120):\n"
+            "    for group in (K, 1 << 40, (1 << 62), (1 << 63) - 32):\n"
+            "        st = (L.int4_quantize(P, 0, 4, K, group, 1, P, P, P, None),\n"
+            "              L.int4_dequantize(P, P, 1, P, 4, K, group, P, 0, None),\n"
+            "              L.gemv_int4(P, 1, 2, 4, K, P, P, 1, P, group, P, 0, 0, None, None))\n"
+            "        assert st == (s.SSN_E_HIP,) * 3, (K, group, st)\n"
+            "print('reached the launch')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "reached the launch" in r.stdout, (r.stdout[-3000:] + r.stderr[-3000:])

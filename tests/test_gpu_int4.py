@@ -122,6 +122,23 @@ def test_quantize_into_given_tensors_and_back():
     assert bool(((back - W).abs() <= 1.01 * step).all())
 
 
+def test_any_group_beyond_the_row_is_one_group():
+    """Through the C entry: up to the last multiple of 32 of its 64 bits, as a group of K."""
+    rng = np.random.default_rng(7)
+    for K in (32, 64, 5120):
+        W = torch.from_numpy(np.float32(rng.standard_normal((9, K)))).cuda()
+        codes, scales, zeros = ssn.int4_quantize(W, group=K)
+        back = ssn.int4_dequantize(codes, scales, zeros, group=K)
+        for group in (K + 32, 1 << 40, (1 << 63) - 32):
+            got = [torch.zeros_like(t) for t in (codes, scales, zeros, back)]
+            at = [t.data_ptr() for t in got]
+            stream = torch.cuda.current_stream().cuda_stream
+            assert ssn.lib().int4_quantize(W.data_ptr(), ssn.SSN_F32, 9, K, group, ssn.SSN_BF16, *at[:3], stream) == 0
+            assert ssn.lib().int4_dequantize(at[0], at[1], ssn.SSN_BF16, at[2], 9, K, group, at[3], ssn.SSN_F32,
+                                             stream) == 0
+            assert all(torch.equal(a, b) for a, b in zip(got, (codes, scales, zeros, back)))
+
+
 # ------------------------------------------------------------------------------ product
 def check_product(got, Y, err, y_type):
     tol = err + int4.rounding(np.abs(Y) + err, y_type)
