@@ -37,7 +37,6 @@ constexpr int kChunk = 128;                  // k per step of a wave's loop
 constexpr uint32_t kOutside = 0x80000000u;   // a byte offset past the end of every buffer resource
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 // A resource of `bytes` bytes: loads at offsets past its end give zero and make no traffic.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* base, int bytes) {

@@ -1,5 +1,5 @@
 // Element types of the calls that take f32, bf16 and f16 alike (the codes of include/ssnvfp4.h:
-// SSN_F32, SSN_BF16, SSN_F16): loads to f32 and stores rounded to nearest even.
+// SSN_F32, SSN_BF16, SSN_F16): conversions to f32 and back, rounded to nearest even.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -22,10 +22,6 @@ __device__ __forceinline__ uint16_t round16_sat(double v, int t) {
   return to_bf16(fminf((float)v, __uint_as_float(0x7F7F0000u)));
 }
 
-__device__ __forceinline__ float load_elem(const void* p, int t, int64_t i) {
-  if (t == kF32) return ((const float*)p)[i];
-  return float16_of(((const uint16_t*)p)[i], t);
-}
 __device__ __forceinline__ void store_elem(void* p, int t, int64_t i, float v) {
   if (t == kF32) ((float*)p)[i] = v;
   else ((uint16_t*)p)[i] = t == kF16 ? to_f16(v) : to_bf16(v);
