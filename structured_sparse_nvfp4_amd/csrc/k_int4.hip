@@ -243,6 +243,7 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles) {
   constexpr int H = SILU ? 2 : 1;             // units per tile of 16 outputs: gate and up
   constexpr int SPANS = 4 * C / FOLD, PACKS = SPANS / P, ROWS = 16 / P;
   static_assert(SPANS % P == 0, "whole packs");
+  static_assert(!SILU || D == 1, "gate and up take turns in one set of registers");
   using Loads = UnitLoads<C, FOLD>;
   // whether the sums of x stay in registers too, or are formed again for every unit (one more matrix
   // instruction per step: the matrix cores have the time, the registers are full)
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles) {
 #pragma unroll
   for (int d = 0; d < D; ++d)
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_unit(buf[d], tile + (d / H) * stride, d % H, c);
+    for (int c = 0; c < C; ++c) load_unit(buf[d], tile + d * stride, 0, c);
   __builtin_amdgcn_sched_barrier(0);
   if (GROUPED) load_x();
   f32x4 xs[KEEP ? PACKS : 1];
@@ -431,8 +432,8 @@ __global__ __launch_bounds__(1024) void k_int4_rows(Int4GemvArgs a, int tiles) {
   for (;;) {
     f32x4 tot[2];
     if constexpr (SILU) {
-      tot[0] = work(buf[0], D == 1 ? tile : tile + stride, D == 1 ? 1 : 0);
-      tot[1] = work(buf[D - 1], tile + stride, D == 1 ? 0 : 1);
+      tot[0] = work(buf[0], tile, 1);
+      tot[1] = work(buf[0], tile + stride, 0);
       finish(tot);
       if ((tile += stride) >= tiles) return;
     } else {
