@@ -70,18 +70,20 @@ __device__ __forceinline__ float team_max(float v) {
   return v;
 }
 
-// One team of L lanes per group, whose first 8 U L weights stay in registers between the search for the range and
-// the codes; the rest of a longer group is read a second time, from the L2. Memory-bound: W read, codes
-// written. Two vectors of eight a lane rather than one halve what a lane spends on its group (the range's
-// way across lanes, the scale, the places), 13824 x 5120, group 128: f32 58 against 63 us (5.5 TB/s), bf16 47
-// against 58; group 32, bf16: 49 against 57.
+// One team of L lanes per group. Its 8 U L weights stay in registers between the search for the range and the
+// codes, which is the whole group for the teams of a wave or less; a workgroup (L = 256) reads what goes beyond a
+// second time, from the L2. Memory-bound: W read, codes written. Two vectors of eight a lane rather than one halve
+// what a lane spends on its group (the range's way across lanes, the scale, the places), 13824 x 5120, group 128:
+// f32 58 against 63 us (5.5 TB/s), bf16 47 against 58; group 32, bf16: 49 against 57.
 // Groups beyond 2048 have a workgroup, which holds 8192 weights: one group of 5120 to a row 60 us, with a wave and
 // a second reading 79; 16 rows of 8192 4.2 against 8.7.
+// Six waves per SIMD at least: left alone the compiler unpacks all of a bf16 wave's 2048 weights at once (104
+// registers, four waves), groups of 1024 65 us against 54.
 template <int T, int L, int U>
-__global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restrict__ W, int64_t teams, int K, int group,
-                                                            int groups, uint32_t* __restrict__ codes,
-                                                            uint16_t* __restrict__ scales, int st,
-                                                            uint8_t* __restrict__ zeros) {
+__global__ __launch_bounds__(kThreads, 6) void k_int4_quantize(const void* __restrict__ W, int64_t teams, int K,
+                                                               int group, int groups, uint32_t* __restrict__ codes,
+                                                               uint16_t* __restrict__ scales, int st,
+                                                               uint8_t* __restrict__ zeros) {
   constexpr int kTeams = kThreads / L;         // per workgroup
   const int l = threadIdx.x % L;
   for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < teams; t0 += (int64_t)gridDim.x * kTeams) {
@@ -105,11 +107,12 @@ __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restri
         if (8 * (l + L * u) < len) load8<T>(W, base + 8 * (l + L * u), w[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) extend(w[u]);
-      for (int k = 8 * (l + L * U); k < len; k += 8 * L) {
-        float v[8];
-        load8<T>(W, base + k, v);
-        extend(v);
-      }
+      if constexpr (L > 64)
+        for (int k = 8 * (l + L * U); k < len; k += 8 * L) {
+          float v[8];
+          load8<T>(W, base + k, v);
+          extend(v);
+        }
     }
     if constexpr (L <= 64) {
       hi = team_max<L>(hi);
@@ -166,11 +169,12 @@ __global__ __launch_bounds__(kThreads) void k_int4_quantize(const void* __restri
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (8 * (l + L * u) < len) encode(w[u], 8 * (l + L * u));
-    for (int k = 8 * (l + L * U); k < len; k += 8 * L) {
-      float v[8];
-      load8<T>(W, base + k, v);
-      encode(v, k);
-    }
+    if constexpr (L > 64)
+      for (int k = 8 * (l + L * U); k < len; k += 8 * L) {
+        float v[8];
+        load8<T>(W, base + k, v);
+        encode(v, k);
+      }
     if (l == 0) {
       scales[team] = sb;
       if (zeros) zeros[team] = (uint8_t)z;
@@ -461,7 +465,7 @@ hipError_t launch_quantize_l(const void* W, int64_t N, int64_t K, int64_t group,
   return hipGetLastError();
 }
 
-// lanes per group so that a lane has two vectors of eight of it, or four of a long one
+// lanes per group so that a lane has two vectors of eight of it, or four of a long one: all of a group of up to 2048
 template <int T>
 hipError_t launch_quantize_t(const void* W, int64_t N, int64_t K, int64_t group, uint8_t* codes, uint16_t* scales,
                              int s_type, uint8_t* zeros, hipStream_t s) {
@@ -472,7 +476,7 @@ hipError_t launch_quantize_t(const void* W, int64_t N, int64_t K, int64_t group,
   if (len <= 256) return launch_quantize_l<T, 16, 2>(W, N, K, group, codes, scales, s_type, zeros, s);
   if (len <= 512) return launch_quantize_l<T, 32, 2>(W, N, K, group, codes, scales, s_type, zeros, s);
   if (len <= 2048) return launch_quantize_l<T, 64, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
-  return launch_quantize_l<T, 256, 4>(W, N, K, group, codes, scales, s_type, zeros, s);
+  return launch_quantize_l<T, 256, 4>(W, N, K, group, codes, scales, s_type, zeros, s);   // the one that reads again
 }
 
 }  // namespace
