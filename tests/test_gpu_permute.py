@@ -245,6 +245,47 @@ def test_rows_beyond_the_cache(T, k, D, t, dout_t):
     assert bool(((dw - (a * b).sum(1, keepdim=True)).abs() <= err)[keep.view(T, k)].all()) and dw[0, 5] == 0
 
 
+# T k D elements of 268 MB and more; a wave, two or four to a token, rows of fewer elements than a lane moves, whole
+# vectors and a last one that overlaps
+@pytest.mark.parametrize("T,k,D,t,dout_t", [
+    (14000, 16, 301, "f32", "f32"), (7000, 16, 601, "f32", "f32"), (2100, 16, 2001, "f32", "f32"), (210000, 64, 5, "f32", "f32"),
+    (28000, 16, 303, "bf16", "bf16"), (14000, 16, 601, "bf16", "bf16"), (4100, 16, 2048, "bf16", "bf16"),
+    (28000, 16, 303, "f16", "f16"), (14000, 16, 601, "f16", "f16"), (4200, 16, 2001, "f16", "f16"),
+    (28000, 16, 303, "bf16", "f32"), (14000, 16, 601, "bf16", "f32"), (4200, 16, 2001, "bf16", "f32"),
+    (28000, 16, 303, "f16", "f32"), (14000, 16, 601, "f16", "f32"), (4100, 16, 2048, "f16", "f32")])
+def test_weighted_rows_beyond_the_cache(T, k, D, t, dout_t):
+    """The weighted movements that write such rows past the caches: moe_unpermute_backward without dweights, equal
+    bit for bit to the call with dweights, which writes through them, and moe_permute with weights."""
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    row_of = torch.randperm(T * k, generator=g, device="cuda").int()
+    lost = int(row_of[5])
+    row_of[5] = -1
+    keep = row_of.view(T, k) >= 0
+    w = torch.rand((T, k), generator=g, device="cuda") + 0.1
+    # one product, rounded to the type: to f32 first (half a step 2^-24) or, with halves, in one instruction without
+    half, least = {"f32": (2.0 ** -24, 2.0 ** -150), "bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}[t]
+
+    def scattered(rows, A):
+        assert bool((rows[lost] == -777).all())
+        for j in range(k):
+            want = (w[:, j:j + 1].double() * A.double())[keep[:, j]]
+            off = (rows[row_of.view(T, k)[:, j][keep[:, j]].long()].double() - want).abs()
+            assert bool((off <= (half * (1 + 2.0 ** -24) + 2.0 ** -24) * want.abs() + least).all())
+
+    dout = torch.randn((T, D), generator=g, device="cuda").to(TYPES[dout_t])
+    dYp = torch.full((T * k, D), -777.0, dtype=TYPES[t], device="cuda")
+    assert ssn.moe_unpermute_backward(dout, row_of, T * k, w, y_dtype=TYPES[t], dYp=dYp)[1] is None
+    scattered(dYp, dout)
+    with_dw = torch.full((T * k, D), -777.0, dtype=TYPES[t], device="cuda")
+    ssn.moe_unpermute_backward(dout, row_of, T * k, w, Yp=dYp, dYp=with_dw)
+    assert torch.equal(with_dw, dYp)
+    del with_dw
+    if t == dout_t:
+        dYp.fill_(-777.0)
+        ssn.moe_permute(dout, row_of, w, R=T * k, Xp=dYp)
+        scattered(dYp, dout)
+
+
 def test_graph_replays():
     rng = np.random.default_rng(9)
     T, k, D = 40, 5, 136
