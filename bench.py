@@ -2,7 +2,8 @@
 
     python bench.py [--gpus 1] [--steps K] [--warmup W] [--workloads decode,square,head,moe,w4a4,refs]
 
-Prints ONE JSON line. The headline (``value``, ``ms_per_step``, ``roofline``) is the prefill
+Prints ONE JSON line, short enough for a log that keeps the last few KB; the record of every workload
+goes to stderr, as one more line. The headline (``value``, ``ms_per_step``, ``roofline``) is the prefill
 product, the largest of the workloads: X bf16 [8192, 5120] ~ N(0, 1) times dense NVFP4 weights
 W [27648, 5120] (~ N(0, 0.02) with 1% of the entries x20 before quantisation), f32 accumulation,
 bf16 output, on the matrix cores (gemm_nvfp4_dense, 256 x 256 tiles). One step is one such
@@ -19,7 +20,7 @@ temperature while it runs. Per kernel the bench reports the average over back-to
 (HIP events around the batch) and the median and minimum of at least 20 individually timed
 launches.
 
-``workloads`` adds: ``decode`` (the GEMVs at N = 13824, K = 5120, M = 1, 4, 8 on a ring of 16
+The record (``workloads``, on stderr) adds: ``decode`` (the GEMVs at N = 13824, K = 5120, M = 1, 4, 8 on a ring of 16
 weight copies, and the weight-preparation calls on three rotating copies of W, each against
 8 TB/s and the measured copy bandwidth), ``square`` (4096^3, f32 out), ``head`` (N = 131072,
 K = 5120, M = 1, 8, 9), ``moe`` (512 experts, top-10 of Zipf(1.1), D = 2048, I = 512: 4096
@@ -1224,6 +1225,12 @@ def summarize(kind, out, dirs, cmd_note):
 
 
 # ------------------------------------------------------------------------------------------
+def report(out, work):
+    """The headline's line on stdout, the workloads' record (some 18 KB) on stderr before it."""
+    print("[bench] " + json.dumps({"workloads": work}), file=sys.stderr, flush=True)
+    print(json.dumps(out), flush=True)
+
+
 def main():
     args = parse()
     if args.summarize:
@@ -1287,11 +1294,10 @@ def main():
             work["w4a4"]["square"] = run_w4a4(torch, ssn, synth, 4096, 4096, 4096, False,
                                               work["square"]["dense_mfma"]["us"])
         print("[bench] w4a4 done", file=sys.stderr, flush=True)
-    out["workloads"] = work
     if not args.no_cpu_baseline:
         out["cpu_baseline"] = cpu_baseline_prefill(x_pre)
         print("[bench] cpu baseline done", file=sys.stderr, flush=True)
-    print(json.dumps(out), flush=True)
+    report(out, work)
 
 
 if __name__ == "__main__":

@@ -121,3 +121,12 @@ def test_counter_summary_averages_each_counter_per_kernel_and_grid(tmp_path):
     assert f"| `{a}` | 256 | 2 | 20.0 | 4.0 |" in text       # mean of the two dispatches per counter
     assert f"| `{a}` | 512 | 1 | 7.0 |  |" in text            # a counter not read for that grid stays empty
     assert f"| `{b}` | 64 | 1 | 1.0 |  |" in text
+
+
+def test_the_headline_is_one_short_line_and_the_record_goes_to_stderr(capsys):
+    out = {"metric": bench.METRIC, "value": 1.5, "steps": 20}
+    work = {"prefill": {str(i): {"us": 1.25, "trials": 20} for i in range(2000)}}
+    bench.report(out, work)
+    got = capsys.readouterr()
+    assert got.out.count("\n") == 1 and json.loads(got.out) == out
+    assert json.loads(got.err.removeprefix("[bench] ")) == {"workloads": work}
