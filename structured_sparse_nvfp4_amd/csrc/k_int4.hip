@@ -72,9 +72,11 @@ __device__ __forceinline__ float team_max(float v) {
 
 // One team of L lanes per group. Its 8 U L weights stay in registers between the search for the range and the
 // codes, which is the whole group for the teams of a wave or less; a workgroup (L = 256) reads what goes beyond a
-// second time, from the L2. Memory-bound: W read, codes written. Two vectors of eight a lane rather than one halve
-// what a lane spends on its group (the range's way across lanes, the scale, the places), 13824 x 5120, group 128:
-// f32 58 against 63 us (5.5 TB/s), bf16 47 against 58; group 32, bf16: 49 against 57.
+// second time, from the L2. f32 is bound by memory (W read, codes written), 16-bit weights by the vector units, which
+// issue all the time: 20 instructions a weight for f32, 29 for bf16, whose lanes take the exact decision (below) as
+// well more often than not. Two vectors of eight a lane rather than one halve what a lane spends on its group
+// (the range's way across lanes, the scale, the places), 13824 x 5120, group 128: f32 58 against 63 us (5.5 TB/s), bf16
+// 47 against 58; group 32, bf16: 49 against 57.
 // Groups beyond 2048 have a workgroup, which holds 8192 weights: one group of 5120 to a row 60 us, with a wave and
 // a second reading 79; 16 rows of 8192 4.2 against 8.7.
 // Six waves per SIMD at least: left alone the compiler unpacks all of a bf16 wave's 2048 weights at once (104
@@ -141,8 +143,9 @@ __global__ __launch_bounds__(kThreads, 6) void k_int4_quantize(const void* __res
     if (!live) continue;
     auto encode = [&](const float* v, int k) __attribute__((always_inline)) {
       // The codes as bytes, from w inv + z. With s normal that is off by less than 2^-17 from w / s + z wherever
-      // it is not clamped, so only what lies within 2^-16 of a half needs the exact decision, seldom enough
-      // for the whole wave to take it.
+      // it is not clamped, so only what lies within 2^-16 of a half needs the exact decision. The whole wave takes
+      // it where one lane must: for normally distributed weights in groups of 128 1.5 percent of the time if they
+      // are f32, 59 if they and the scales are bf16 (f16 11), as quotients of so few bits fall on halves more often.
       uint32_t even = 0, odd = 0;
       float far = 0.f;                         // the farthest from its whole number
 #pragma unroll
@@ -532,9 +535,11 @@ hipError_t launch_rows_t(const Int4GemvArgs& a, hipStream_t s) {
   // activations than they hide (N = 13824, K = 5120, M = 8: 13.1 against 17.0 us).
   const int64_t wgs = (int64_t)cu_count() * std::max(1, 16 / W);
   // grouped: a workgroup at least for every slot that there may be (each expert's last may be partial), and
-  // otherwise fewer than the chip holds, as each first finds its slot, token and activations: three quarters of `wgs`
-  // against half and twice as many, 32 tokens to 10 of 512 experts 33.1, 35.9 and 37.3 us (K = 512), 57, 53 and 57
-  // (gate and up, K = 2048), 8 tokens 22, 21 and 26, 32 tokens to 10 of 20 experts 15.4, 15.9 and 20.4 us.
+  // otherwise fewer than the chip holds, as each first finds its slot, token and activations. Three quarters of
+  // `wgs` against half, all and twice as many: 32 tokens to 10 of 512 experts, down (K = 512) 33.9, 35.1, 33.4 and 36
+  // us, gate and up (K = 2048) 57, 53, 56 and 55; 8 tokens, gate and up 21, 21, 22 and 25, down 11.8, 12.1, 13.8 and
+  // 16.8; 32 tokens to 10 of 20 experts, gate and up 15.5, 14.4, 16.9 and 19.6. None is best for all: half loses 2 to 4
+  // percent on down projections and gains 7 on the other two, all loses 4 to 17 percent with few or crowded rows.
   const int64_t grid = GROUPED ? std::max<int64_t>(3 * wgs / 4, std::min<int64_t>(a.E, a.M) + a.M / ROWS)
                                : std::min<int64_t>(wgs, tiles);
   hipLaunchKernelGGL((k_int4_rows<F16X, P, C, FOLD, D, GROUPED, SILU>), dim3((unsigned)grid), dim3(W * 64),
@@ -585,8 +590,11 @@ hipError_t launch_int4_gemv(const Int4GemvArgs& args, hipStream_t s) {
   if (a.group >= a.K) a.group = (a.K + kChunk - 1) / kChunk * kChunk;   // one group: any length past K's end
   // what the registers of 16 waves hold: 64 chunks of K, or 128 where four rows share an operand
   const bool fits = a.K <= (a.M <= 4 ? 128 : 64) * kChunk;
-  // 9 to 16 rows take long to bring into registers, which pays from four tiles of weight rows per compute unit
-  // on (K = 5120, M = 16: N = 13824 18.1 against 16.9 us with the other kernel, N = 24576 22.9 against 30.0 us)
+  // 9 to 16 rows take long to bring into registers, which pays from some four tiles of weight rows per compute
+  // unit on. This kernel against the other, us: K = 5120, M = 16, N = 13824 18.2 and 16.6, 16384 18.4 and 17.1, 20480
+  // 20.4 and 23.3, 32768 27.1 and 31.6; M = 9, N = 13824 15.5 and 16.1, 32768 24.5 and 31.2. K = 2048, M = 16,
+  // N = 20480 11.3 and 11.2, 24576 12.6 and 11.5, 32768 14.4 and 16.2. K = 8192, M = 16, N = 16384 25.8 and 24.2,
+  // 20480 29.7 and 32.8.
   const bool pays = a.offsets || a.M <= 8 || (a.M <= 16 && a.N >= 4 * 16 * (int64_t)cu_count());
   if (!fits || !pays) return launch_int4_wide(a, s);
   return a.x_type == kF16 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);

@@ -11,8 +11,10 @@
 // Every weight is decoded once and multiplied by MT operands; every operand of activations serves NT
 // tiles, so a workgroup reads 16 MT K activations from the L2 for 16 NT K weights. No one part bounds it:
 // a wave goes through loads, LDS, decode and matrix instructions in turn, and two waves per SIMD hide little of
-// that (M = 50, N = 4097, K = 5152, group 64 16.8 us; without any loads 12.7, without the decode 16.4). M = 64, group
-// 128: N = 13824, K = 5120 25 us, N = 131072 183 us (2.1 TB/s, 470 TFLOP/s); M = 16: N = 13824 16.6 us.
+// that (M = 50, N = 4097, K = 5152, group 64 16.8 us; without any loads 12.7, without the decode 16.4; M = 64, N =
+// 131072, group 128: vector units busy 0.41 of the time, matrix cores 0.26, a wave waits 0.33 of its own for memory or
+// LDS and 0.38 for its turn). M = 64, group 128: N = 13824, K = 5120 25 us, N = 131072 183 us (2.1 TB/s, 470
+// TFLOP/s); M = 16: N = 13824 16.6 us. The 4 x 4 tile spills 36 bytes a lane for groups of 32 and 16 for 64.
 #include <algorithm>
 
 #include "device_once.hpp"
@@ -253,15 +255,19 @@ hipError_t launch_wide(const Int4GemvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tile of a product: a compute unit holds one workgroup's sums at a time, so the time is the number of
-// rounds of cu_count() workgroups times a workgroup's own, which grows with its tile. Measured per round at
-// K = 5120, in tenths of a us (more K lengthens all of them alike):
+// The tile of a product: the time is taken to be the number of rounds of cu_count() workgroups times a
+// round's own, which grows with the tile. Measured at K = 5120, in tenths of a us per round:
 //   NT            1    2    3    4
 //   16 rows      65   97  125  149
 //   32 rows      80  115  144  172
 //   64 rows           167  198  230
 // The larger tiles cost less per output, the smaller ones leave less of a last round empty: M = 50, N = 5120 takes
 // 14.4 us in one round of 2 x 3 tiles, 16.1 in one of 4 x 2, 19.4 in two of 2 x 2, 22.2 in a third of one of 4 x 4.
+// Two things it leaves out. A compute unit holds two workgroups of the tiles 1 x 2, 1 x 3 and 2 x 1 (of 2 x 2
+// too for groups of a multiple of 128) and three of 1 x 1, so that their second round is often the shorter one (1 x 1
+// 6.5 us and 3.5 more, 2 x 1 8.3 and 5.3, 1 x 3 13.0 and 9.3); one of each other tile. And K changes the
+// proportions where it is short: one round of 4 x 4, 2 x 2 and 1 x 1 takes 10.6, 5.8 and 4.6 us at K = 1024, 27.5,
+// 10.7 and 6.5 at 5120, 67, 33 and 17.5 at 16384.
 struct Tile {
   int mt, nt, cost;
 };
