@@ -372,7 +372,8 @@ int gemm_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const
  *   zeros   u8 [N, groups], any value of a byte; or NULL: every zero point is 8 (symmetric)
  *   W_hat[n, k] = scales[n, g] * (q[n, k] - zeros[n, g])
  * Scales are 2-byte aligned and zeros any, so that one row's or one expert's part of a larger array can
- * be passed; the other tensors are 16-byte aligned. K % 32 == 0.
+ * be passed; the other tensors are 16-byte aligned. K % 32 == 0. Limits: N up to 2^31 - 1024, K up to 2^30 (the
+ * products: 2^20, and 2^40 bytes of codes).
  * ============================================================================================= */
 
 /* ---------------------------------------------------------------------------------------------
@@ -395,13 +396,15 @@ int int4_dequantize(const uint8_t* codes, const void* scales, int s_dtype, const
                     int64_t group, void* out, int out_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
- * gemv_int4 — Y = X . W_hat^T for one token or a few: the weights stream from memory once per 64
- * rows of X. Inside a group the sum runs over x (q - z) in f32, and the scale multiplies it once, so no
- * weight is rounded. X [M, K] bf16 or f16 (x_dtype); Y [M, N] f32, bf16 or f16 (y_dtype, rounded to
- * nearest even). Any M up to 2^24 and K up to 2^20 are computed; larger M than some 64 are a matrix
- * product, which the tiles of gemm_nvfp4_dense are made for and this call is not. A non-finite X[m, k]
- * makes row m of Y non-finite, and so may activations whose sum times 255 over a group passes the range of
- * f32, whatever the scale (no f16, and bf16 beyond some 2^100).
+ * gemv_int4 — Y = X . W_hat^T for one token or a few: the weights are read once for up to 16 rows of X;
+ * more rows are taken in sets of 16, 32 or 64, side by side, that each read them (from the caches where they
+ * are found there). Inside a group the sum runs over x (q - z) in f32, and the scale multiplies it once, so
+ * no weight is rounded. X [M, K] bf16 or f16 (x_dtype); Y [M, N] f32, bf16 or f16 (y_dtype, rounded to
+ * nearest even). Any M up to 2^24 is computed, but each set decodes the weights again, and there are no
+ * tiles for these weights like those of gemm_nvfp4_dense: from some 350 rows on int4_dequantize and a library
+ * product of its result take less time, from some 150 on where that result is kept (13824 x 5120). A
+ * non-finite X[m, k] makes row m of Y non-finite, and so may activations whose sum times 255 over a group
+ * passes the range of f32, whatever the scale (no f16, and bf16 beyond some 2^100).
  * algo: AUTO or MFMA, reported in *algo_used (host, nullable).
  * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE (group), HIP.
  * ------------------------------------------------------------------------------------------- */
@@ -413,12 +416,13 @@ int gemv_int4(const void* X, int x_dtype, int64_t M, int64_t N, int64_t K, const
  * moe_grouped_gemv_int4 — the same product for every expert's rows, in one launch:
  *   Y[r, :] = X[src(r), :] . W_hat_e^T  for r in [offsets[e], offsets[e+1]),
  * src(r) = row_token[r], or r where row_token is NULL; weights [E, N, ...] per expert. For routings with
- * few rows per expert: an expert's weights stream once per 8 of its rows (R up to 2^24, K up to
- * 2^20). Epilogue (SSN_EPI_NONE, SSN_EPI_SILU_GATE), x_rows, R and the clamping of offsets into [0, R] and of source rows into
- * [0, x_rows) are those of moe_grouped_gemm_nvfp4; N need only be even for SILU_GATE, and the gate is
- * formed from the f32 sums. Offsets must ascend, as moe_route writes them. Rows of Y that belong to no
- * expert (r >= offsets[E]) are left as they were. algo: AUTO or STREAM, reported in *algo_used (host,
- * nullable). Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE, HIP.
+ * few rows per expert: an expert's weights are read and decoded once per 8 of its rows (4 where R <= 4 and
+ * K <= 16384; 16 for other K beyond 8192). R up to 2^24. Epilogue (SSN_EPI_NONE, SSN_EPI_SILU_GATE),
+ * x_rows, R and the clamping of offsets into [0, R] and of source rows into [0, x_rows) are those of
+ * moe_grouped_gemm_nvfp4; N need only be even for SILU_GATE, and the gate is formed from the f32 sums.
+ * Offsets must ascend, as moe_route writes them. Rows of Y that belong to no expert (r >= offsets[E]) are
+ * left as they were. algo: AUTO or STREAM, reported in *algo_used (host, nullable).
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE, HIP.
  * ------------------------------------------------------------------------------------------- */
 int moe_grouped_gemv_int4(const void* X, int x_dtype, int64_t x_rows, const int32_t* row_token,
                           const int32_t* expert_offsets, int E, int64_t R, int64_t N, int64_t K, const uint8_t* codes,
@@ -432,8 +436,9 @@ int moe_grouped_gemv_int4(const void* X, int x_dtype, int64_t x_rows, const int3
  * value outside [0, R) means that the entry has no row (an invalid id, or a dropped one): nothing is
  * written for it, it adds nothing, and its weight's gradient is 0. No two entries may own one row.
  * topk_weights f32 [T, k]; NULL: every weight is 1. Sums are f32 in slot order. Rows and tokens are
- * f32, bf16 or f16, each result rounded once; any D. Limits: 1 <= k <= 64, T*k < 2^31. Outputs must
- * not overlap inputs.
+ * f32, bf16 or f16, each result rounded once. Limits: 1 <= k <= 64, T*k < 2^31 - 1024, R <= 2^31 - 1024,
+ * D <= 2^30. Outputs must not overlap inputs. The gradients are calls like any other: nothing records the
+ * forward ones, and the products above have no gradient here.
  * ============================================================================================= */
 
 /* ---------------------------------------------------------------------------------------------

@@ -4,6 +4,10 @@ Argument marshalling only: every step runs in the library's HIP kernels. PyTorch
 device memory and the current stream. The functions have the names of the C entry points
 declared in ``include/ssnvfp4.h``; outputs are allocated here with torch when not given.
 If the shared library is missing, every call raises (there is no fallback).
+
+No call records itself for torch's automatic differentiation: results never require a gradient, whatever the
+inputs do. ``moe_permute`` and ``moe_unpermute`` have theirs as calls (``moe_permute_backward``,
+``moe_unpermute_backward``), to be made by hand or from a ``torch.autograd.Function`` of the caller's.
 """
 from __future__ import annotations
 
@@ -681,7 +685,8 @@ def _entries(dev, row_of, T, topk_weights):
 def moe_permute(X, row_of, topk_weights=None, R=None, Xp=None, prepare=False):
     """Tokens to expert order: Xp[row_of[t*k+j]] = topk_weights[t, j] * X[t] (no weights: a copy). X f32, bf16 or
     f16 [T, D]; row_of int32 [T*k] as moe_route gives it (entries outside [0, R) have no row). Returns Xp [R, D]
-    of X's type, R = T*k unless given; rows that no entry owns keep what Xp held."""
+    of X's type, R = T*k unless given; rows that no entry owns keep what Xp held. Its gradient is
+    moe_permute_backward, which nothing calls by itself."""
     (T, D), dev, dt = _first(X, 2, "X", _ANY)
     k, ro, w = _entries(dev, row_of, T, topk_weights)
     R = R if R is not None else (T * k if Xp is None else Xp.shape[0])
@@ -713,7 +718,8 @@ def moe_permute_backward(dXp, row_of, T, topk_weights=None, X=None, dX=None, dwe
 
 def moe_unpermute(Yp, row_of, T, topk_weights=None, out_dtype=None, out=None, prepare=False):
     """Expert rows back to T tokens: out[t] = sum_j topk_weights[t, j] * Yp[row_of[t*k+j]] (no weights: the plain
-    sum), summed in f32. Yp f32, bf16 or f16 [R, D]; out [T, D] of Yp's type unless out_dtype is float32."""
+    sum), summed in f32. Yp f32, bf16 or f16 [R, D]; out [T, D] of Yp's type unless out_dtype is float32. Its
+    gradient is moe_unpermute_backward, which nothing calls by itself."""
     (R, D), dev, ydt = _first(Yp, 2, "Yp", _ANY)
     k, ro, w = _entries(dev, row_of, T, topk_weights)
     if out is None:
