@@ -66,8 +66,8 @@ typedef enum {
   SSN_E_RANGE = 7   /* an argument is outside its documented range (e.g. top-k, expert count) */
 } ssn_status;
 
-/* SSN_F16 (IEEE half) is taken by the integer 4-bit calls and by moe_permute / moe_unpermute and their
- * gradients; the other calls refuse it (DTYPE). */
+/* SSN_F16 (IEEE half) is taken by the integer 4-bit calls, by moe_permute / moe_unpermute and their
+ * gradients, and by the calls of the 4-bit cache; the other calls refuse it (DTYPE). */
 enum { SSN_F32 = 0, SSN_BF16 = 1, SSN_F16 = 2 };
 
 /* GEMM algorithms. Each call writes the one it ran to *algo_used (host int, nullable).
@@ -475,6 +475,81 @@ int moe_unpermute(const void* Yp, int yp_dtype, int64_t R, const int32_t* row_of
 int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, int64_t D, const int32_t* row_of,
                            const float* topk_weights, int64_t R, const void* Yp, void* dYp, int yp_dtype,
                            float* dweights, void* stream);
+
+/* =============================================================================================
+ * A cache of keys and values in NVFP4, and attention over it: what a decode step reads beside its weights.
+ *
+ * The cache is pages of page_size tokens (a multiple of 16 in [16, 2^20]); inside a page a head's tokens are one
+ * run. Hkv key heads in [1, 4096], width D a multiple of 32 in [32, 256], pages in [1, 2^31 - 1024]:
+ *   k_codes   u8 [pages, Hkv, page_size, D/2]    two E2M1 nibbles a byte, the even d in the low one
+ *   k_scales  u8 [pages, Hkv, page_size, D/16]   E4M3, one per 16 values along D
+ *   v_codes   u8 [pages, Hkv, page_size, D/2]
+ *   v_scales  u8 [pages, Hkv, D/16, page_size]   the values' scales with the tokens innermost
+ *   k_tensor_scale, v_tensor_scale  f32 [Hkv]    s_h, the tensor scale of each head (finite)
+ * A cached value is E2M1(code) * E4M3(scale) * s_h. The token at place o of page p has slot p * page_size + o. Slots
+ * that nothing was written to may hold anything: no call reads what it is not asked for, nor lets it into a result.
+ * These calls have no gradients.
+ * ============================================================================================= */
+
+/* ---------------------------------------------------------------------------------------------
+ * kv_nvfp4_append — keys and values quantised as they are written: token t of K and V (f32, bf16 or f16, dtype)
+ * goes to slots[t], by the rule of nvfp4_quantize with tensor_scale_in = s_h for the D values of each head (bit for
+ * bit; a magnitude beyond 6 * 448 * s_h saturates; a head whose s_h is 0 or less holds zeros). K and V are
+ * [T, Hkv, D] with the D values of a head contiguous and rows of any 16-byte aligned strides (in elements), as the
+ * parts of one projection are. A token with a negative slot is not written, one beyond the cache is not written and
+ * counted in bad_slots (device int64 [1], nullable, set by the call). No two tokens may own one slot. T <= 2^26.
+ * K and V must be finite (a NaN is written as 0, an infinity as the largest value).
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (Hkv), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int kv_nvfp4_append(const void* K, const void* V, int dtype, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
+                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots, uint8_t* k_codes,
+                    uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, const float* k_tensor_scale,
+                    const float* v_tensor_scale, int64_t pages, int page_size, int Hkv, int D, int64_t* bad_slots,
+                    void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * kv_nvfp4_read — keys and values [T, Hkv, D] (contiguous, f32, bf16 or f16, out_dtype) of any slots, the same one
+ * more than once if asked: the f32 product above, rounded to out_dtype as nvfp4_dequantize does. Tokens whose slot
+ * is negative or beyond the cache are zeros. T <= 2^26. Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (Hkv), HIP.
+ * ------------------------------------------------------------------------------------------- */
+int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const uint8_t* k_scales,
+                  const uint8_t* v_codes, const uint8_t* v_scales, const float* k_tensor_scale,
+                  const float* v_tensor_scale, int64_t pages, int page_size, int Hkv, int D, void* K, void* V,
+                  int out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * attn_kv_nvfp4 — attention of B sequences' newest tokens over the cache: with query i of sequence b at position
+ * p = seq_lens[b] - n_b + i (its own key and those before it are in the cache already),
+ *   out[q, h, :] = sum_j w_j V_hat[j, h / G, :],  w = softmax_j(scale * <Q[q, h, :], K_hat[j, h / G, :]>),  G = Hq / Hkv
+ * over the keys j <= p, j > p - window where window > 0, or all j < seq_lens[b] where causal is 0 (then without a
+ * window). lse (f32 [Tq, Hq], nullable) receives the natural logarithm of the sum of the exponentials. A row without
+ * keys (an empty sequence, more queries than keys) is 0, its lse -infinity.
+ *   Q          bf16 or f16 (q_dtype) [Tq, Hq, D], the D values of a head contiguous, 16-byte aligned strides
+ *   out        [Tq, Hq, D] contiguous, of q_dtype or f32 (out_dtype)
+ *   block_table int32 [B, max_blocks]  page of every page_size tokens of a sequence; a value outside [0, pages) is a page
+ *              that is not there, whose tokens no row keeps
+ *   seq_lens   int32 [B]     tokens of each sequence in the cache, the queries' own among them; at most max_kv count
+ *   q_offsets  int32 [B + 1] sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1; NULL: Tq / B each
+ *   max_q, max_kv            no sequence has more queries (those beyond are not computed) or tokens; max_kv is at most
+ *              max_blocks * page_size and 2^27
+ * Rows of out and lse that belong to no sequence, or lie beyond max_q, are left as they were. Logits, softmax
+ * statistics and sums are f32; K_hat and V_hat enter unrounded, a softmax term is rounded to 11 bits (f16) before it
+ * multiplies V_hat, and so is Q below 2^-39 of its row's largest magnitude.
+ * algo: AUTO or STREAM, reported in *algo_used (host, nullable). workspace: attn_kv_nvfp4_workspace_bytes() bytes of
+ * device memory (16-byte aligned; NULL if 0), for f32 results of parts of long sequences; nothing in it needs
+ * clearing, and calls that may overlap need one each.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE, HIP.
+ * ------------------------------------------------------------------------------------------- */
+int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_token_stride, int64_t q_head_stride,
+                  const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                  const float* k_tensor_scale, const float* v_tensor_scale, int64_t pages, int page_size, int Hkv, int D,
+                  const int32_t* block_table, int64_t B, int64_t max_blocks, const int32_t* seq_lens,
+                  const int32_t* q_offsets, int64_t max_q, int64_t max_kv, float scale, int causal, int64_t window,
+                  void* out, int out_dtype, float* lse, int algo, int* algo_used, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that attn_kv_nvfp4 needs for these sizes on the current device (-1 if they are refused). */
+int64_t attn_kv_nvfp4_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv);
 
 /* ---------------------------------------------------------------------------------------------
  * Calibration (measurement only; no product path calls it). The roofline of the compute-bound

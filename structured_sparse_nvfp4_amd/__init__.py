@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -65,6 +66,13 @@ _SIGS = {
     "moe_permute_backward": ([_vp, _int, _i64, _vp, _vp, _i64, _int, _i64, _vp, _vp, _vp, _vp], _int),
     "moe_unpermute": ([_vp, _int, _i64, _vp, _vp, _i64, _int, _i64, _vp, _int, _vp], _int),
     "moe_unpermute_backward": ([_vp, _int, _i64, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _vp], _int),
+    "kv_nvfp4_append": ([_vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int,
+                         _int, _int, _vp, _vp], _int),
+    "kv_nvfp4_read": ([_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _vp, _vp, _int, _vp], _int),
+    "attn_kv_nvfp4": ([_vp, _int, _i64, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _vp,
+                       _i64, _i64, _vp, _vp, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _int, _vp, _int, _vp, _vp,
+                       _i64, _vp], _int),
+    "attn_kv_nvfp4_workspace_bytes": ([_i64, _int, _int, _int, _i64, _i64], _i64),
     "mfma_probe_sink_floats": ([], _i64),
     "mfma_probe": ([_int, _int, _int, ctypes.c_uint32, _vp, _vp, _vp], _int),
 }
@@ -744,6 +752,135 @@ def moe_unpermute_backward(dout, row_of, R, topk_weights=None, Yp=None, y_dtype=
     y, dweights, dw = _dweights(dev, dweights, Yp, "Yp", y_dtype, (R, D), T, k)
     cargs = (dout.data_ptr(), odt, T, k, D, ro, w, R, y, _on(dev, dYp, y_dtype, "dYp", (R, D)), ydt, dw)
     return _run_on(dev, "moe_unpermute_backward", cargs, prepare, (dout, row_of, topk_weights, Yp), (dYp, dweights))
+
+
+# ------------------------------------------------------------------------------------------------
+# 4-bit cache of keys and values, and attention over it
+
+
+class KvNvfp4(NamedTuple):
+    """A cache of keys and values in NVFP4: pages of page_size tokens (a multiple of 16), heads of width D (a multiple of
+    32, at most 256). The tensors are the caller's; kv_nvfp4_empty makes them."""
+    k_codes: torch.Tensor           # u8 [pages, Hkv, page_size, D/2]
+    k_scales: torch.Tensor          # u8 [pages, Hkv, page_size, D/16]
+    v_codes: torch.Tensor           # u8 [pages, Hkv, page_size, D/2]
+    v_scales: torch.Tensor          # u8 [pages, Hkv, D/16, page_size]
+    k_tensor_scale: torch.Tensor    # f32 [Hkv]
+    v_tensor_scale: torch.Tensor    # f32 [Hkv]
+
+
+def kv_nvfp4_empty(pages, page_size, D, k_tensor_scale, v_tensor_scale):
+    """An unwritten cache for the heads' tensor scales (f32 [Hkv] device tensors: the largest magnitude of a head over
+    2688, from calibration or from its first tokens)."""
+    H, new = k_tensor_scale.shape[0], k_tensor_scale.new_empty
+    u8 = dict(dtype=torch.uint8)
+    return KvNvfp4(new((pages, H, page_size, D // 2), **u8), new((pages, H, page_size, D // 16), **u8),
+                   new((pages, H, page_size, D // 2), **u8), new((pages, H, D // 16, page_size), **u8),
+                   k_tensor_scale, v_tensor_scale)
+
+
+def _kv(dev, cache):
+    """(addresses of the cache's tensors, (pages, page_size, Hkv, D))."""
+    kc, ks, vc, vs, kt, vt = cache
+    P, H, S, Dh = _size(kc, 4, "k_codes")
+    D, u8, f32 = 2 * Dh, torch.uint8, torch.float32
+    return (_on(dev, kc, u8, "k_codes", (P, H, S, Dh)), _on(dev, ks, u8, "k_scales", (P, H, S, D // 16)),
+            _on(dev, vc, u8, "v_codes", (P, H, S, Dh)), _on(dev, vs, u8, "v_scales", (P, H, D // 16, S)),
+            _on(dev, kt, f32, "k_tensor_scale", (H,)), _on(dev, vt, f32, "v_tensor_scale", (H,))), (P, S, H, D)
+
+
+def _rows(dev, t, dtype, name, shape):
+    """(address, stride of a token, stride of a head) of a tensor whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be a device tensor on {dev}, it is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    token, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
+
+
+def kv_nvfp4_append(K, V, slots, cache, bad_slots=None, prepare=False):
+    """Quantise keys and values [T, Hkv, D] (f32, bf16 or f16, one type; rows may be strided) into the cache: token t goes
+    to slots[t] (int64 [T] device: page * page_size + place; negative: nowhere). bad_slots (int64 [1] device), where
+    given, receives the count of slots beyond the cache. Returns the cache."""
+    T = _size(K, 3, "K")[0]
+    dev = K.device
+    at, (P, S, H, D) = _kv(dev, cache)
+    k, kt, kh = _rows(dev, K, K.dtype, "K", (T, H, D))
+    v, vt, vh = _rows(dev, V, K.dtype, "V", (T, H, D))
+    cargs = (k, v, _code(K.dtype, "K", _ANY), T, kt, kh, vt, vh, _on(dev, slots, torch.int64, "slots", (T,)), *at, P, S, H,
+             D, None if bad_slots is None else _on(dev, bad_slots, torch.int64, "bad_slots", (1,)))
+    return _run_on(dev, "kv_nvfp4_append", cargs, prepare, (K, V, slots, bad_slots), cache)
+
+
+def kv_nvfp4_read(slots, cache, out_dtype=torch.bfloat16, K=None, V=None, prepare=False):
+    """The cached keys and values of any slots (int64 [T] device): (K, V) [T, Hkv, D] of out_dtype (f32, bf16 or f16);
+    zeros where a slot is negative or beyond the cache."""
+    (T,) = _size(slots, 1, "slots")
+    dev = slots.device
+    at, (P, S, H, D) = _kv(dev, cache)
+    K = K if K is not None else slots.new_empty((T, H, D), dtype=out_dtype)
+    V = V if V is not None else slots.new_empty((T, H, D), dtype=K.dtype)
+    dt = _code(K.dtype, "K", _ANY)
+    cargs = (_on(dev, slots, torch.int64, "slots", (T,)), T, *at, P, S, H, D, _on(dev, K, K.dtype, "K", (T, H, D)),
+             _on(dev, V, K.dtype, "V", (T, H, D)), dt)
+    return _run_on(dev, "kv_nvfp4_read", cargs, prepare, (slots, cache), (K, V))
+
+
+def attn_kv_nvfp4(Q, cache, block_table, seq_lens, q_offsets=None, max_q=None, max_kv=None, scale=None, causal=True,
+                  window=0, out_dtype=None, with_lse=False, algo=ALGO_AUTO, out=None, lse=None, workspace=None,
+                  prepare=False):
+    """Attention of B sequences' newest tokens over the cache, their own keys and values in it already. Q bf16 or f16
+    [Tq, Hq, D] (rows may be strided), Hq a multiple of the cache's heads; block_table int32 [B, blocks]; seq_lens int32
+    [B], the queries' tokens included; q_offsets int32 [B+1] where sequences have different numbers of queries (else
+    Tq / B each). max_q and max_kv bound a sequence's queries and tokens (host numbers that size the launch: Tq, or
+    Tq / B, and the table's width unless given). scale: 1 / sqrt(D) unless given. window > 0: a query keeps its last
+    `window` keys. Returns (out [Tq, Hq, D] of Q's type unless out_dtype is float32, lse f32 [Tq, Hq] if with_lse or
+    given else None, algorithm that ran); rows of no sequence keep what out held, rows without keys are 0."""
+    (Tq, Hq, D) = _size(Q, 3, "Q")
+    dev, qdt = Q.device, _code(Q.dtype, "Q", _HALVES)
+    at, (P, S, H, Dc) = _kv(dev, cache)
+    q, qt, qh = _rows(dev, Q, Q.dtype, "Q", (Tq, Hq, Dc))
+    B, blocks = _size(block_table, 2, "block_table")
+    if max_q is None:
+        max_q = Tq if q_offsets is not None else Tq // B if B else 0
+    if max_kv is None:
+        max_kv = min(blocks * S, 1 << 27)
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = Q.new_empty((Tq, Hq, D), dtype=out_dtype)
+    odt = _code(out.dtype, "out", (torch.float32, Q.dtype))
+    if lse is None and with_lse:
+        lse = Q.new_empty((Tq, Hq), dtype=torch.float32)
+    L = _lib or lib()
+    if dev.type == "cuda" and dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            nws = L.attn_kv_nvfp4_workspace_bytes(B, Hq, H, D, max_q, max_kv)
+    else:
+        nws = L.attn_kv_nvfp4_workspace_bytes(B, Hq, H, D, max_q, max_kv)
+    if nws < 0:
+        _check(SSN_E_SHAPE)
+    if workspace is None and nws:
+        workspace = Q.new_empty(nws, dtype=torch.uint8)
+    elif workspace is not None:
+        _on(dev, workspace, torch.uint8, "workspace", workspace.shape)
+    used = ctypes.c_int(-1)
+    cargs = (q, qdt, Tq, Hq, qt, qh, *at, P, S, H, D, _on(dev, block_table, torch.int32, "block_table", (B, blocks)), B,
+             blocks, _on(dev, seq_lens, torch.int32, "seq_lens", (B,)),
+             None if q_offsets is None else _on(dev, q_offsets, torch.int32, "q_offsets", (B + 1,)), max_q, max_kv, scale,
+             causal, window, _on(dev, out, out.dtype, "out", (Tq, Hq, D)), odt,
+             None if lse is None else _on(dev, lse, torch.float32, "lse", (Tq, Hq)), algo, ctypes.byref(used),
+             None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+    res = _run_on(dev, "attn_kv_nvfp4", cargs, prepare,
+                  (Q, cache, block_table, seq_lens, q_offsets, workspace, used), (out, lse))
+    return (res[0], (out, lse, used)) if prepare else (out, lse, used.value)
 
 
 def mfma_probe_sink_floats():

@@ -666,6 +666,153 @@ int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, in
 }  // extern "C"
 
 // ---------------------------------------------------------------------------------------------
+// 4-bit cache of keys and values, and attention over it
+namespace {
+
+constexpr int64_t kMaxKvTokens = (int64_t)1 << 26;    // of one append or read: their grids
+constexpr int64_t kMaxSeq = (int64_t)1 << 27;         // of one sequence: 32-bit token numbers, page_div
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;        // workgroups of 512 threads at most
+
+int check_cache(const char* fn, const ssn::KvCache& c, int64_t pages, int64_t page_size, int64_t heads, int64_t D) {
+  if (D < 32 || D > 256 || D % 32)
+    return fail(SSN_E_SHAPE, "%s: D=%lld is not a multiple of 32 in [32, 256]", fn, (long long)D);
+  if (page_size < 16 || page_size > (1 << 20) || page_size % 16)
+    return fail(SSN_E_SHAPE, "%s: page_size=%lld is not a multiple of 16 in [16, 2^20]", fn, (long long)page_size);
+  if (heads < 1 || heads > 4096) return fail(SSN_E_RANGE, "%s: Hkv=%lld outside [1, 4096]", fn, (long long)heads);
+  if (pages < 1 || pages > kMaxRows) return fail(SSN_E_SHAPE, "%s: pages=%lld outside [1, 2^31 - 1024]", fn, (long long)pages);
+  uint8_t *const k_codes = c.k_codes, *const k_scales = c.k_scales, *const v_codes = c.v_codes, *const v_scales = c.v_scales;
+  const float *const k_tensor_scale = c.k_ts, *const v_tensor_scale = c.v_ts;
+  REQUIRE_PTR(k_codes); REQUIRE_PTR(k_scales); REQUIRE_PTR(v_codes); REQUIRE_PTR(v_scales);
+  REQUIRE_ELEM_PTR(k_tensor_scale); REQUIRE_ELEM_PTR(v_tensor_scale);
+  return SSN_OK;
+}
+
+// rows of 16-byte pieces: strides of a [tokens, heads, D] tensor in elements of `size` bytes
+int check_strides(const char* fn, const char* name, int64_t token, int64_t head, int size) {
+  if (token < 0 || head < 0 || token > ((int64_t)1 << 40) || head > ((int64_t)1 << 40))
+    return fail(SSN_E_SHAPE, "%s: strides of %s (%lld, %lld) outside [0, 2^40]", fn, name, (long long)token, (long long)head);
+  if (token * size % 16 || head * size % 16)
+    return fail(SSN_E_ALIGN, "%s: rows of %s are not 16-byte aligned (strides %lld, %lld)", fn, name, (long long)token,
+                (long long)head);
+  return SSN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_nvfp4_append(const void* K, const void* V, int dtype, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
+                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots, uint8_t* k_codes,
+                    uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, const float* k_tensor_scale,
+                    const float* v_tensor_scale, int64_t pages, int page_size, int Hkv, int D, int64_t* bad_slots,
+                    void* stream) {
+  const char* fn = "kv_nvfp4_append";
+  int st;
+  ssn::KvAppendArgs a{K, V, T, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, bad_slots,
+                      {k_codes, k_scales, v_codes, v_scales, k_tensor_scale, v_tensor_scale, pages, page_size, Hkv, D}, dtype};
+  if (T < 0 || T > kMaxKvTokens) return fail(SSN_E_SHAPE, "%s: T=%lld outside [0, 2^26]", fn, (long long)T);
+  if ((st = check_type(fn, dtype, "dtype", true)) || (st = check_cache(fn, a.c, pages, page_size, Hkv, D))) return st;
+  const int size = dtype == SSN_F32 ? 4 : 2;
+  if ((st = check_strides(fn, "K", k_token_stride, k_head_stride, size)) ||
+      (st = check_strides(fn, "V", v_token_stride, v_head_stride, size))) return st;
+  REQUIRE_OPT_ELEM_PTR(bad_slots);
+  if (T > 0) { REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_ELEM_PTR(slots); }
+  else if (!bad_slots) return ok();
+  return hip_status(ssn::launch_kv_append(a, as_stream(stream)), fn);
+}
+
+int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                  const uint8_t* v_scales, const float* k_tensor_scale, const float* v_tensor_scale, int64_t pages,
+                  int page_size, int Hkv, int D, void* K, void* V, int out_dtype, void* stream) {
+  const char* fn = "kv_nvfp4_read";
+  int st;
+  ssn::KvReadArgs a{slots, T, K, V,
+                    {(uint8_t*)k_codes, (uint8_t*)k_scales, (uint8_t*)v_codes, (uint8_t*)v_scales, k_tensor_scale,
+                     v_tensor_scale, pages, page_size, Hkv, D}, out_dtype};
+  if (T < 0 || T > kMaxKvTokens) return fail(SSN_E_SHAPE, "%s: T=%lld outside [0, 2^26]", fn, (long long)T);
+  if ((st = check_type(fn, out_dtype, "out_dtype", true)) || (st = check_cache(fn, a.c, pages, page_size, Hkv, D))) return st;
+  if (T == 0) return ok();
+  REQUIRE_ELEM_PTR(slots); REQUIRE_PTR(K); REQUIRE_PTR(V);
+  return hip_status(ssn::launch_kv_read(a, as_stream(stream)), fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_attn(const char* fn, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_kv) {
+  if (B < 0 || B > (1 << 20) || max_q < 0 || max_kv < 0 || max_kv > kMaxSeq)
+    return fail(SSN_E_SHAPE, "%s: bad sizes (B=%lld, max_q=%lld, max_kv=%lld; B <= 2^20, max_kv <= 2^27)", fn,
+                (long long)B, (long long)max_q, (long long)max_kv);
+  if (Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq % Hkv || Hq > (1 << 20))
+    return fail(SSN_E_RANGE, "%s: Hq=%lld is not a multiple of Hkv=%lld (in [1, 4096])", fn, (long long)Hq, (long long)Hkv);
+  if (D < 32 || D > 256 || D % 32)
+    return fail(SSN_E_SHAPE, "%s: D=%lld is not a multiple of 32 in [32, 256]", fn, (long long)D);
+  if (max_q > ((int64_t)1 << 30) / (Hq / Hkv))
+    return fail(SSN_E_SHAPE, "%s: max_q=%lld has too many rows", fn, (long long)max_q);
+  return SSN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t attn_kv_nvfp4_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv) {
+  if (check_attn("attn_kv_nvfp4_workspace_bytes", B, Hq, Hkv, D, max_q, max_kv)) return -1;
+  if (B == 0 || max_q == 0) return 0;
+  ssn::AttnArgs a{};
+  a.B = B; a.Hq = Hq; a.c.heads = Hkv; a.c.D = D; a.max_q = max_q; a.max_kv = max_kv;
+  return ssn::attn_workspace(a);
+}
+
+int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_token_stride, int64_t q_head_stride,
+                  const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                  const float* k_tensor_scale, const float* v_tensor_scale, int64_t pages, int page_size, int Hkv, int D,
+                  const int32_t* block_table, int64_t B, int64_t max_blocks, const int32_t* seq_lens,
+                  const int32_t* q_offsets, int64_t max_q, int64_t max_kv, float scale, int causal, int64_t window,
+                  void* out, int out_dtype, float* lse, int algo, int* algo_used, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+  const char* fn = "attn_kv_nvfp4";
+  int st;
+  ssn::AttnArgs a{Q, q_token_stride, q_head_stride, out, lse,
+                  {(uint8_t*)k_codes, (uint8_t*)k_scales, (uint8_t*)v_codes, (uint8_t*)v_scales, k_tensor_scale,
+                   v_tensor_scale, pages, page_size, Hkv, D},
+                  block_table, seq_lens, q_offsets, Tq, B, max_blocks, max_q, max_kv, Hq, q_dtype, out_dtype, causal != 0,
+                  (int)window, scale, workspace};
+  if ((st = check_attn(fn, B, Hq, Hkv, D, max_q, max_kv))) return st;
+  if ((st = check_cache(fn, a.c, pages, page_size, Hkv, D))) return st;
+  if ((st = check_type(fn, q_dtype, "q_dtype", false)) || (st = check_side_types(fn, q_dtype, out_dtype, "out_dtype"))) return st;
+  if (Tq < 0 || Tq > kMaxRows || max_blocks < 0 || max_blocks > kMaxRows)
+    return fail(SSN_E_SHAPE, "%s: bad sizes (Tq=%lld, max_blocks=%lld)", fn, (long long)Tq, (long long)max_blocks);
+  if (window < 0 || window > kMaxRows) return fail(SSN_E_RANGE, "%s: window=%lld outside [0, 2^31 - 1024]", fn, (long long)window);
+  if (window && !causal) return fail(SSN_E_RANGE, "%s: a window needs causal", fn);
+  if (!(scale - scale == 0.f)) return fail(SSN_E_RANGE, "%s: scale is not finite", fn);
+  if (!q_offsets && B > 0 && Tq % B)
+    return fail(SSN_E_SHAPE, "%s: without q_offsets Tq=%lld must be a multiple of B=%lld", fn, (long long)Tq, (long long)B);
+  if (algo != SSN_ALGO_AUTO && algo != SSN_ALGO_STREAM)
+    return fail(SSN_E_ALGO, "%s: algorithm %d is not available (STREAM)", fn, algo);
+  if ((st = check_strides(fn, "Q", q_token_stride, q_head_stride, 2))) return st;
+  REQUIRE_OPT_ELEM_PTR(lse);
+  if (max_kv > max_blocks * page_size)
+    return fail(SSN_E_SHAPE, "%s: max_kv=%lld is more than max_blocks=%lld pages hold", fn, (long long)max_kv, (long long)max_blocks);
+  if (algo_used) *algo_used = SSN_ALGO_STREAM;
+  if (Tq == 0 || B == 0 || max_q == 0) return ok();
+  REQUIRE_PTR(Q); REQUIRE_PTR(out); REQUIRE_ELEM_PTR(seq_lens); REQUIRE_OPT_ELEM_PTR(q_offsets);
+  if (max_blocks > 0) REQUIRE_ELEM_PTR(block_table);
+  const int64_t need = ssn::attn_workspace(a);
+  if (need > 0) {
+    REQUIRE_PTR(workspace);
+    if (workspace_bytes < need)
+      return fail(SSN_E_RANGE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)need);
+  }
+  if (ssn::attn_workgroups(a) > kMaxGrid)
+    return fail(SSN_E_SHAPE, "%s: B * Hkv * rows need more than 2^23 workgroups", fn);
+  return hip_status(ssn::launch_attn_stream(a, as_stream(stream)), fn);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
 // Calibration
 extern "C" {
 

@@ -1,0 +1,151 @@
+// Shared by the attention kernels over the 4-bit cache (k_attn.hip: few query rows to a key head, k_attn_tile.hip:
+// many): what a workgroup is to do, and codes to operands.
+//
+//   y[r, j] = scale log2(e) q_r . K_hat_j,   out_r = sum_j 2^(y[r, j] - m_r) V_hat_j / sum_j 2^(y[r, j] - m_r)
+//
+// The query heads that share a key head are rows like the queries themselves: row r of (sequence, key head) is query
+// r / G, head r % G of its G. Both kernels form S^T = K . Q^T and O^T = V^T . P^T on the matrix cores, so a lane
+// holds one row's logits of several keys, which are its own operand of the second product: P never leaves its
+// registers. K_hat and V_hat without their f32 scale are E2M1 * E4M3: at most six significant bits, in 2^-10 .. 2688,
+// so exact in f16, and f16 is what both products take: p then has 11 bits where bf16 would have 8. A query row is
+// brought into f16's range by a power of two, which its logits' factor takes back: no bit of an f16 or bf16 value is
+// lost down to 2^-39 of the row's largest.
+#pragma once
+#include "common.hpp"
+#include "launch.hpp"
+#include "types.hpp"
+
+namespace ssn {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// p is held as 2^(y - m + 7): f16's normal range then reaches down to 2^-21 of a row's largest and its subnormals to
+// 2^-31. The reference m of a row is raised only where some y - m passes 8, so p stays below 2^15.
+constexpr float kShift = 7.f, kTop = 15.f;
+constexpr float kUnset = -3e38f;                 // m of a row that has met no key
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+// tokens to (page, place): n / d for n < 2^23, d < 2^17 by a multiplication
+struct PageDiv {
+  uint64_t m;
+  uint32_t d;
+};
+inline PageDiv page_div(uint32_t d) { return {((1ull << 40) + d - 1) / d, d}; }
+__device__ __forceinline__ uint32_t div_by(PageDiv p, uint32_t n) { return (uint32_t)((n * p.m) >> 40); }
+
+struct AttnLaunch {
+  AttnArgs a;
+  PageDiv pd;                  // by the 16-token units of a page
+  int G, row_tiles, splits;
+  float* part_o;               // [item][split][R][D]
+  float* part_ml;              // [item][split][R][2]
+};
+
+// one workgroup's part: its rows and its keys
+struct Work {
+  int b, h, row0, rows;        // rows: of the sequence and key head in all
+  int64_t q0;                  // the sequence's first query
+  int first_pos;               // position of query 0 (negative: more queries than keys)
+  int len;
+  int lo, hi;                  // keys that some row of the workgroup keeps
+  int lo_all, hi_all;          // keys that all its rows keep
+};
+
+// rows r0 .. r0 + R - 1 of sequence b
+__device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int rt, int R, Work& w) {
+  const AttnArgs& a = L.a;
+  int64_t q0, n;
+  if (a.q_offsets) {
+    q0 = a.q_offsets[b];
+    n = (int64_t)a.q_offsets[b + 1] - q0;
+    if (q0 < 0 || q0 > a.Tq) return false;
+  } else {
+    n = a.Tq / a.B;
+    q0 = b * n;
+  }
+  n = min(min(n, a.max_q), a.Tq - q0);
+  if (n <= 0) return false;
+  const int64_t rows = n * L.G, row0 = (int64_t)rt * R;
+  if (row0 >= rows) return false;
+  w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = q0;
+  w.len = (int)min((int64_t)max(a.lens[b], 0), a.max_kv);
+  w.first_pos = w.len - (int)n;
+  const int i0 = (int)row0 / L.G, i1 = ((int)min(row0 + R, rows) - 1) / L.G;
+  w.lo = w.lo_all = 0;
+  w.hi = w.hi_all = w.len;
+  if (a.causal) {
+    w.hi = max(0, w.first_pos + i1 + 1);
+    w.hi_all = w.first_pos + i0 + 1;
+    if (a.window > 0) {
+      w.lo = max(0, w.first_pos + i0 + 1 - a.window);
+      w.lo_all = max(0, w.first_pos + i1 + 1 - a.window);
+    }
+  }
+  return true;
+}
+
+// keys [lo, hi) that row r keeps; none for rows behind the last
+__device__ __forceinline__ void row_keys(const AttnLaunch& L, const Work& w, int r, int& lo, int& hi) {
+  lo = 0; hi = w.len;
+  if (L.a.causal) {
+    hi = w.first_pos + r / L.G + 1;
+    if (L.a.window > 0) lo = hi - L.a.window;
+  }
+  if (r >= w.rows) hi = 0;
+}
+
+// the page that holds 16-token unit u of sequence b, or -1; place: the unit's first token in it
+__device__ __forceinline__ int page_of(const AttnLaunch& L, int b, int u, int& place) {
+  const uint32_t i = div_by(L.pd, (uint32_t)u);
+  place = (u - (int)(i * L.pd.d)) * 16;
+  const int p = i < (uint64_t)L.a.max_blocks ? L.a.table[(int64_t)b * L.a.max_blocks + i] : -1;
+  return p >= 0 && p < L.a.c.pages ? p : -1;
+}
+
+__device__ __forceinline__ f16x2 as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
+
+// two E2M1 nibbles of byte SEL times a pair of scales
+template <int SEL>
+__device__ __forceinline__ uint32_t fp4x2_f16(uint32_t w, f16x2 s) {
+  const f16x2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL);
+  return __builtin_bit_cast(uint32_t, v * s);
+}
+
+// E4M3 bytes HALF * 2 and HALF * 2 + 1 of w
+template <bool HALF>
+__device__ __forceinline__ f16x2 e4m3x2_f16(uint32_t w) { return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HALF); }
+
+__device__ __forceinline__ f16x8 as_f16x8(u32x4 v) { return __builtin_bit_cast(f16x8, v); }
+
+// eight codes of one token times one scale
+__device__ __forceinline__ f16x8 fp4x8_f16(uint32_t w, _Float16 s) {
+  const f16x2 ss = {s, s};
+  return as_f16x8(u32x4{fp4x2_f16<0>(w, ss), fp4x2_f16<1>(w, ss), fp4x2_f16<2>(w, ss), fp4x2_f16<3>(w, ss)});
+}
+
+// Codes of two tokens, nibble by nibble of the same d: byte x of even holds d = 2x (the first token in its low
+// nibble), of odd d = 2x + 1. Four instructions for sixteen codes, before they are converted.
+__device__ __forceinline__ void pair_tokens(uint32_t t0, uint32_t t1, uint32_t& even, uint32_t& odd) {
+  constexpr uint32_t m = 0x0F0F0F0Fu;
+  even = (t0 & m) | ((t1 << 4) & ~m);
+  odd = ((t0 >> 4) & m) | (t1 & ~m);
+}
+
+// two f32 rounded to f16
+__device__ __forceinline__ uint32_t pk_f16(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Exponent shift that brings a row's largest magnitude into [2^15, 2^16); 0 for a row of zeros or not finite.
+__device__ __forceinline__ int row_shift(float amax) {
+  if (!(amax > 0.f) || !(amax < __builtin_inff())) return 0;
+  int e;
+  (void)frexpf(amax, &e);                          // amax = f 2^e, f in [1/2, 1)
+  return 16 - e;
+}
+
+}  // namespace ssn

@@ -121,6 +121,48 @@ struct PermuteArgs {
 hipError_t launch_moe_scatter(const PermuteArgs& a, hipStream_t s);
 hipError_t launch_moe_gather(const PermuteArgs& a, hipStream_t s);
 
+// 4-bit cache of keys and values in pages (layout in include/ssnvfp4.h), and attention over it
+struct KvCache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const float *k_ts, *v_ts;   // [heads]
+  int64_t pages;
+  int page, heads, D;         // tokens of a page (a multiple of 16), key heads, width (a multiple of 32, <= 256)
+};
+struct KvAppendArgs {
+  const void *K, *V;          // [T, heads, D] of type, a head's D values contiguous
+  int64_t T, k_token, k_head, v_token, v_head;   // strides in elements
+  const int64_t* slots;       // [T]: page * tokens of a page + place; negative: no slot
+  int64_t* bad;               // [1] or nullptr: slots beyond the cache
+  KvCache c;
+  int type;
+};
+struct KvReadArgs {
+  const int64_t* slots;
+  int64_t T;
+  void *K, *V;                // [T, heads, D] contiguous
+  KvCache c;
+  int type;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s);
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
+struct AttnArgs {
+  const void* Q;              // [Tq, Hq, D] of q_type, a head's D values contiguous
+  int64_t q_token, q_head;    // strides in elements
+  void* out;                  // [Tq, Hq, D] contiguous
+  float* lse;                 // [Tq, Hq] or nullptr
+  KvCache c;
+  const int32_t* table;       // [B, max_blocks]
+  const int32_t* lens;        // [B]
+  const int32_t* q_offsets;   // [B + 1] or nullptr: Tq / B queries each
+  int64_t Tq, B, max_blocks, max_q, max_kv;
+  int Hq, q_type, out_type, causal, window;
+  float scale;
+  void* ws;                   // attn_workspace() bytes
+};
+int64_t attn_workspace(const AttnArgs& a);   // bytes for the partial results, 0 if none are made
+int64_t attn_workgroups(const AttnArgs& a);
+hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t s);
+
 // calibration: register-resident matrix ops on random operands (cu_count() * waves_per_simd
 // workgroups of 256 threads; sink holds one float per thread)
 hipError_t launch_mfma_probe(int kind, int waves_per_simd, int iters, uint32_t seed, float* sink, hipStream_t s);

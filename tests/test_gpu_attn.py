@@ -1,0 +1,360 @@
+"""GPU parity of attention over the 4-bit cache against the float64 oracle, within the bound of its f32 evaluation."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import structured_sparse_nvfp4_amd as ssn
+from oracle import kv
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+class Batch:
+    """Sequences of the given lengths and numbers of queries in a shuffled cache whose unused slots hold 0xFF (NaN
+    scales) and whose unused table entries are no pages."""
+
+    def __init__(self, lens, qs, Hq, H, D, page, seed=0, x="bf16", spread=1.0, spare=2):
+        rng = np.random.default_rng([seed, D, page])
+        self.lens, self.qs, self.Hq, self.H, self.D, self.page, self.x = list(lens), list(qs), Hq, H, D, page, x
+        used = [-(-n // page) for n in lens]
+        pages = sum(used) + spare
+        ts = (rng.random((2, H)) * 1e-3 + 1e-3).astype(np.float32)
+        self.cache = ssn.kv_nvfp4_empty(pages, page, D, torch.from_numpy(ts[0]).cuda(), torch.from_numpy(ts[1]).cuda())
+        for t in self.cache[:4]:
+            t.fill_(0xFF)
+        order = rng.permutation(pages)
+        self.table = np.full((len(lens), max(used + [0]) + 1), -1, np.int32)
+        self.slots, at = [], 0
+        for b, n in enumerate(lens):
+            self.table[b, :used[b]] = order[at:at + used[b]]
+            at += used[b]
+            j = np.arange(n)
+            self.slots.append(self.table[b, j // page].astype(np.int64) * page + j % page)
+        T = sum(lens)
+        if T:
+            slots = torch.from_numpy(np.concatenate(self.slots)).cuda()
+            K, V = (torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32) * s).cuda() for s in (spread, 1.0))
+            ssn.kv_nvfp4_append(K, V, slots, self.cache)
+        self.Q = torch.from_numpy(rng.standard_normal((sum(qs), Hq, D)).astype(np.float32)).to(TYPES[x]).cuda()
+        self.offsets = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+
+    def dev(self, a):
+        return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+    def call(self, uniform=False, **kw):
+        off = None if uniform else self.dev(self.offsets)
+        kw.setdefault("max_q", max(self.qs))
+        return ssn.attn_kv_nvfp4(kw.pop("Q", self.Q), self.cache, self.dev(self.table), self.dev(np.int32(self.lens)), off, **kw)
+
+    def values(self, b):
+        """Cached keys and values of sequence b in float64."""
+        h = [t.cpu().numpy() for t in self.cache]
+        kc, ks, vc, vs = kv.gather(*h[:4], self.slots[b], self.page)
+        return kv.dequantize_tokens(kc, ks, h[4]), kv.dequantize_tokens(vc, vs, h[5])
+
+    def check(self, out, lse=None, causal=True, window=0, scale=None, Q=None, out_type=None, seqs=None):
+        torch.cuda.synchronize()
+        Q = (self.Q if Q is None else Q).double().cpu().numpy()
+        got = out.double().cpu().numpy()
+        eps = HALF[out_type or self.x]
+        for b in range(len(self.lens)) if seqs is None else seqs:
+            q0, n, S = int(self.offsets[b]), self.qs[b], self.lens[b]
+            k, v = self.values(b)
+            want, wlse, tol, ltol = kv.attention(Q[q0:q0 + n], k, v, self.D ** -0.5 if scale is None else scale,
+                                                 kv.keeps(S, n, causal, window), eps)
+            bad = ~(np.abs(got[q0:q0 + n] - want) <= tol)
+            assert not bad.any(), (b, np.argwhere(bad)[:3].tolist(), int(bad.sum()), got[q0:q0 + n][bad][:3], want[bad][:3], tol[bad][:3])
+            if lse is not None:
+                gl = lse[q0:q0 + n].double().cpu().numpy()
+                none = np.isneginf(wlse)
+                assert np.array_equal(np.isneginf(gl), none)
+                assert np.all(np.abs(gl[~none] - wlse[~none]) <= ltol[~none])
+
+
+LENS = [1, 2, 15, 16, 17, 31, 32, 33, 47, 64, 65, 127, 129, 200, 255, 256, 257]
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("Hq,H", [(1, 1), (5, 1), (16, 2), (40, 8), (17, 1)])
+def test_single_tokens(D, Hq, H):
+    B = Batch(LENS, [1] * len(LENS), Hq, H, D, [16, 32, 48, 64, 128][(D // 32 + Hq) % 5])
+    out, lse, algo = B.call(uniform=True, with_lse=True)
+    assert algo == ssn.ALGO_STREAM and out.dtype == torch.bfloat16
+    B.check(out, lse)
+
+
+@pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_types(x, y, D):
+    B = Batch([300, 77, 1], [1, 3, 1], 6, 2, D, 16, x=x)
+    out, lse, _ = B.call(out_dtype=TYPES[y], with_lse=True)
+    assert out.dtype == TYPES[y]
+    B.check(out, lse, out_type=y)
+
+
+@pytest.mark.parametrize("window", [0, 1, 2, 16, 17, 50, 4096])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 9, 16, 33])
+def test_several_tokens_and_windows(n, window):
+    """Up to 33 queries a sequence over one, two and four sets of 16 rows; rows that leave some keys only."""
+    lens = [n, n + 1, n + 15, 40 + n, 100, 257]
+    B = Batch(lens, [n] * len(lens), 10, 2, 128, 16, seed=n)
+    out, lse, _ = B.call(uniform=True, with_lse=True, window=window)
+    B.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("D", [64, 160, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_ragged_batch(D, causal):
+    B = Batch([70, 0, 1, 130, 33, 290], [70, 3, 1, 7, 33, 1], 8, 4, D, 32, seed=7)
+    out, lse, _ = B.call(with_lse=True, causal=causal)
+    B.check(out, lse, causal=causal)
+    assert int(out[70:73].count_nonzero()) == 0 and bool(torch.isneginf(lse[70:73]).all())
+
+
+def test_more_queries_than_keys():
+    B = Batch([3, 20], [9, 20], 4, 1, 128, 16)
+    out, lse, _ = B.call(with_lse=True)
+    B.check(out, lse)
+    assert int(out[:6].count_nonzero()) == 0 and bool(torch.isneginf(lse[:6]).all())
+
+
+def test_rows_of_no_sequence_are_left():
+    B = Batch([50, 60], [4, 2], 4, 2, 64, 16)
+    Q = torch.cat([B.Q[:1], B.Q, B.Q[:3]])
+    B.offsets = B.offsets + 1
+    out, lse = torch.full((10, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((10, 4), 7.0, device="cuda")
+    o, l, _ = B.call(Q=Q, out=out, lse=lse)
+    assert o is out and l is lse
+    B.check(out, lse, Q=Q)
+    for t in (out, lse):
+        assert bool((t[:1] == 7).all()) and bool((t[7:] == 7).all())
+    # of a sequence with more than max_q queries the first max_q are computed, as of a sequence of that many
+    out.fill_(7.0)
+    B.call(Q=Q, out=out, max_q=2)
+    assert bool((out[3:5] == 7).all()) and bool((out[1:3] != 7).any())
+    B.check(out, Q=Q, seqs=[1])
+
+
+def test_max_kv_bounds_the_lengths():
+    B = Batch([100, 40], [1, 1], 4, 1, 128, 16)
+    out, _, _ = B.call(max_kv=64)
+    C = Batch([100, 40], [1, 1], 4, 1, 128, 16)
+    C.lens, C.slots = [64, 40], [C.slots[0][:64], C.slots[1]]
+    C.check(out)
+
+
+def test_pages_that_are_not_there():
+    """Tokens of a page outside [0, pages) count for no row."""
+    B = Batch([200, 90], [2, 1], 4, 2, 128, 32)
+    pages = B.cache.k_codes.shape[0]
+    gone = {0: [0, 3], 1: [1]}
+    k = [B.values(b) for b in range(2)]
+    for b, ps in gone.items():
+        for i, p in enumerate(ps):
+            B.table[b, p] = [-1, pages, 1 << 30, -(1 << 31)][(i + b) % 4]
+    out, lse, _ = B.call(with_lse=True)
+    Q = B.Q.double().cpu().numpy()
+    for b in range(2):
+        keep = kv.keeps(B.lens[b], B.qs[b], True, 0)
+        for p in gone[b]:
+            keep[:, p * 32:(p + 1) * 32] = False
+        q0 = int(B.offsets[b])
+        want, wl, tol, lt = kv.attention(Q[q0:q0 + B.qs[b]], *k[b], 128 ** -0.5, keep, HALF["bf16"])
+        got, gl = out[q0:q0 + B.qs[b]].double().cpu().numpy(), lse[q0:q0 + B.qs[b]].double().cpu().numpy()
+        assert np.all(np.abs(got - want) <= tol) and np.all(np.abs(gl - wl) <= lt)
+    B.table[:] = -1
+    out, lse, _ = B.call(with_lse=True)
+    assert int(out.count_nonzero()) == 0 and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-6, 1.0, 30.0])
+def test_scales(scale):
+    B = Batch([150, 33], [3, 1], 4, 2, 64, 16, x="f16")
+    out, lse, _ = B.call(scale=scale, with_lse=True)
+    B.check(out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e-20, 1e-4, 300.0, 1e6, 1e30])
+def test_queries_of_any_size(size):
+    """bf16 queries of any magnitude: logits next to nothing, or one key alone."""
+    B = Batch([130, 40], [2, 1], 4, 2, 96, 16)
+    Q = (B.Q.float() * size).to(torch.bfloat16)
+    Q[0, 0, ::3] = 0
+    Q[1, 1, :] = 0
+    if size < 1e20:
+        out, lse, _ = B.call(Q=Q, with_lse=True)
+        B.check(out, lse, Q=Q)
+    else:
+        out, lse, _ = B.call(Q=Q, with_lse=True, scale=1e-30)
+        B.check(out, lse, Q=Q, scale=1e-30)
+
+
+def test_a_row_that_is_not_finite_touches_no_other():
+    B = Batch([130, 40], [2, 1], 8, 2, 128, 16)
+    want, _, _ = B.call()
+    Q = B.Q.clone()
+    Q[0, 1, 5], Q[1, 6, 0], Q[2, 3, 127] = float("nan"), float("inf"), float("-inf")
+    out, _, _ = B.call(Q=Q)
+    hit = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[1, 6] = hit[2, 3] = True
+    assert torch.equal(out[~hit], want[~hit]) and bool(out[0, 1].isnan().all())
+
+
+@pytest.mark.parametrize("spread", [0.0, 8.0, 40.0])
+def test_flat_and_sharp_rows(spread):
+    """Every key alike, and rows where the largest logit grows by hundreds along the sequence."""
+    B = Batch([600, 257], [1, 4], 6, 2, 128, 64, spread=spread)
+    out, lse, _ = B.call(with_lse=True)
+    B.check(out, lse)
+
+
+def test_growing_logits():
+    """Keys ordered so that the reference is raised in nearly every tile."""
+    B = Batch([512], [1], 4, 1, 64, 16)
+    K = torch.linspace(0, 2.6, 512, device="cuda")[:, None, None] * torch.ones(512, 1, 64, device="cuda")
+    ssn.kv_nvfp4_append(K, torch.randn(512, 1, 64, device="cuda"), B.dev(B.slots[0]), B.cache)
+    B.Q = torch.ones_like(B.Q) * torch.tensor([1.0, -1.0, 4.0, -4.0], device="cuda", dtype=B.Q.dtype)[:, None]
+    out, lse, _ = B.call(with_lse=True)
+    B.check(out, lse)
+
+
+@pytest.mark.parametrize("D,Hq,H,n,window", [(128, 16, 2, 1, 0), (64, 4, 4, 1, 0), (256, 8, 1, 1, 0), (128, 10, 2, 9, 0),
+                                             (160, 3, 1, 2, 3000), (128, 8, 1, 1, 700)])
+def test_long_sequences_are_split(D, Hq, H, n, window):
+    B = Batch([9001, 4100], [n, n], Hq, H, D, 64)
+    out, lse, _ = B.call(uniform=True, with_lse=True, window=window)
+    B.check(out, lse, window=window)
+    again, lse2, _ = B.call(uniform=True, with_lse=True, window=window)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_split_with_short_sequences_among_long():
+    """Splits that get no keys of a sequence."""
+    B = Batch([5000, 1, 0, 40, 700], [1, 1, 1, 1, 1], 8, 1, 128, 16)
+    out, lse, _ = B.call(uniform=True, with_lse=True)
+    B.check(out, lse)
+
+
+def test_strided_queries():
+    B = Batch([90, 30], [3, 2], 4, 2, 96, 16)
+    wide = torch.zeros(5, 12, 96, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:7] = B.Q
+    want, _, _ = B.call()
+    out, _, _ = B.call(Q=wide[:, 3:7])
+    assert torch.equal(out, want) and out.is_contiguous()
+    out, _, _ = B.call(Q=B.Q.transpose(0, 1).contiguous().transpose(0, 1))
+    assert torch.equal(out, want)
+
+
+def test_offsets_beyond_32_bits():
+    H, D, page = 8, 256, 256
+    pages = (1 << 32) // (H * page * D // 2) + 8
+    B = Batch([300], [1], 8, H, D, page)
+    ts = B.cache.k_tensor_scale, B.cache.v_tensor_scale
+    big = ssn.kv_nvfp4_empty(pages, page, D, *ts)
+    for i, p in enumerate(B.table[0, :2]):
+        for s, d in zip(B.cache[:4], big[:4]):
+            d[pages - 1 - i] = s[int(p)]
+    want, _, _ = B.call()
+    small, B.cache = B.cache, big
+    B.table[0, :2] = [pages - 1, pages - 2]
+    out, _, _ = B.call()
+    assert torch.equal(out, want)
+
+
+def test_captured_and_replayed_beside_another():
+    """Two captured calls with workspaces of their own; lengths, pages and queries of the replay's time."""
+    A, B = Batch([4000, 2500], [1, 1], 8, 1, 128, 16, seed=1), Batch([3000], [2], 4, 1, 64, 16, seed=2)
+    st = []
+    for X in (A, B):
+        t = dict(Q=X.Q, table=X.dev(X.table), lens=X.dev(np.int32(X.lens)), out=torch.zeros_like(X.Q))
+        t["args"] = (t["Q"], X.cache, t["table"], t["lens"])
+        t["kw"] = dict(out=t["out"], max_kv=4096 if X.table.shape[1] * 16 >= 4096 else None)
+        ssn.attn_kv_nvfp4(*t["args"], **t["kw"])
+        st.append(t)
+    torch.cuda.synchronize()
+    graphs = []
+    for t in st:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ssn.attn_kv_nvfp4(*t["args"], **t["kw"])
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for i in range(4):
+        for X, t in zip((A, B), st):
+            t["Q"].copy_(torch.randn_like(t["Q"]))
+            t["lens"].copy_(torch.tensor([n - 700 * i for n in X.lens], dtype=torch.int32))
+            t["out"].zero_()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for t in st:
+            got = t["out"].clone()
+            want, _, _ = ssn.attn_kv_nvfp4(*t["args"], max_kv=t["kw"]["max_kv"])
+            assert torch.equal(got, want)
+
+
+def test_two_calls_on_two_streams():
+    A, B = Batch([6000], [1], 8, 1, 128, 16, seed=3), Batch([7000], [1], 8, 1, 128, 16, seed=4)
+    want = [X.call()[0].clone() for X in (A, B)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for X, s in zip((A, B), streams):
+            with torch.cuda.stream(s):
+                got.append(X.call()[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_prepared_call():
+    B = Batch([600, 90], [1, 1], 8, 2, 128, 16)
+    want, _, _ = B.call()
+    call, (out, _, used) = B.call(prepare=True)
+    call(); call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and used.value == ssn.ALGO_STREAM
+
+
+def test_a_model_decodes():
+    """A prompt and six decoded tokens through append and attention, as a layer uses them: every step equals attention
+    over what the cache holds."""
+    torch.manual_seed(5)
+    Hq, H, D, page, pages = 8, 2, 64, 16, 12
+    ts = torch.full((H,), 4.5 / 2688, device="cuda")
+    cache = ssn.kv_nvfp4_empty(pages, page, D, ts, ts)
+    for t in cache[:4]:
+        t.fill_(0xFF)
+    table = torch.randperm(pages, device="cuda").to(torch.int32).view(2, 6)
+    lens = torch.tensor([37, 20], device="cuda", dtype=torch.int32)
+    offsets = torch.tensor([0, 37, 57], device="cuda", dtype=torch.int32)
+    done = torch.zeros(2, dtype=torch.int64)
+    for step in range(7):
+        qs = [37, 20] if step == 0 else [1, 1]
+        qkv = torch.randn(sum(qs), Hq + 2 * H, D, device="cuda").to(torch.bfloat16)
+        slots = torch.cat([table[b].long()[(p := torch.arange(int(done[b]), int(done[b]) + qs[b], device="cuda")) // page]
+                           * page + p % page for b in range(2)])
+        done += torch.tensor(qs)
+        ssn.kv_nvfp4_append(qkv[:, Hq:Hq + H], qkv[:, Hq + H:], slots, cache)
+        if step:
+            lens += 1
+        out, _, _ = ssn.attn_kv_nvfp4(qkv[:, :Hq], cache, table, lens, offsets if step == 0 else None,
+                                      max_q=max(qs))
+        at = 0
+        for b in range(2):
+            S, n = int(done[b]), qs[b]
+            j = torch.arange(S, device="cuda")
+            K, V = ssn.kv_nvfp4_read(table[b].long()[j // page] * page + j % page, cache, out_dtype=torch.float32)
+            want, _, tol, _ = kv.attention(qkv[at:at + n, :Hq].double().cpu().numpy(), K.double().cpu().numpy(),
+                                           V.double().cpu().numpy(), D ** -0.5, kv.keeps(S, n, True, 0), 2.0 ** -8)
+            # K and V were read back rounded to f32: half a step more of every logit and value, of which the bound counts many
+            assert np.all(np.abs(out[at:at + n].double().cpu().numpy() - want) <= tol)
+            at += n
