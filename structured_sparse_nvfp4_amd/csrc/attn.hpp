@@ -38,6 +38,7 @@ struct AttnLaunch {
   AttnArgs a;
   PageDiv pd;                  // by the 16-token units of a page
   int G, row_tiles, splits;
+  int64_t each;                // queries of a sequence without q_offsets
   float* part_o;               // [item][split][R][D]
   float* part_ml;              // [item][split][R][2]
 };
@@ -52,20 +53,26 @@ struct Work {
   int lo_all, hi_all;          // keys that all its rows keep
 };
 
-// rows r0 .. r0 + R - 1 of sequence b
-__device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int rt, int R, Work& w) {
+// the first query and the number of queries of sequence b
+__device__ __forceinline__ bool find_queries(const AttnLaunch& L, int b, int64_t& q0, int64_t& n) {
   const AttnArgs& a = L.a;
-  int64_t q0, n;
   if (a.q_offsets) {
     q0 = a.q_offsets[b];
     n = (int64_t)a.q_offsets[b + 1] - q0;
     if (q0 < 0 || q0 > a.Tq) return false;
   } else {
-    n = a.Tq / a.B;
+    n = L.each;
     q0 = b * n;
   }
   n = min(min(n, a.max_q), a.Tq - q0);
-  if (n <= 0) return false;
+  return n > 0;
+}
+
+// rows rt R .. rt R + R - 1 of sequence b
+__device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int rt, int R, Work& w) {
+  const AttnArgs& a = L.a;
+  int64_t q0, n;
+  if (!find_queries(L, b, q0, n)) return false;
   const int64_t rows = n * L.G, row0 = (int64_t)rt * R;
   if (row0 >= rows) return false;
   w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = q0;
@@ -95,13 +102,14 @@ __device__ __forceinline__ void row_keys(const AttnLaunch& L, const Work& w, int
   if (r >= w.rows) hi = 0;
 }
 
-// the page that holds 16-token unit u of sequence b, or -1; place: the unit's first token in it
+// The table's entry for 16-token unit u of sequence b, and the unit's first token in its page. A unit behind the last
+// token may be asked for: the table's last entry stands in, and its tokens are masked by the caller.
 __device__ __forceinline__ int page_of(const AttnLaunch& L, int b, int u, int& place) {
   const uint32_t i = div_by(L.pd, (uint32_t)u);
   place = (u - (int)(i * L.pd.d)) * 16;
-  const int p = i < (uint64_t)L.a.max_blocks ? L.a.table[(int64_t)b * L.a.max_blocks + i] : -1;
-  return p >= 0 && p < L.a.c.pages ? p : -1;
+  return L.a.table[(int64_t)b * L.a.max_blocks + min((int64_t)i, L.a.max_blocks - 1)];
 }
+__device__ __forceinline__ bool is_page(const AttnLaunch& L, int p) { return p >= 0 && p < L.a.c.pages; }
 
 __device__ __forceinline__ f16x2 as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
 

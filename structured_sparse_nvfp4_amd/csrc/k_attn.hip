@@ -16,18 +16,22 @@
 
 #include "attn.hpp"
 #include "device_once.hpp"
+#include "pipeline.hpp"
 
 namespace ssn {
 namespace {
 
-// one tile's codes and scales as loaded
+// One tile's codes and scales as loaded. (Types as wide as the loads: widened at the load they would be waited for
+// there.)
 template <int DP>
 struct Tile {
+  using KeyScales = std::conditional_t<DP == 64, uint8_t, std::conditional_t<DP == 128, uint16_t, u32x2>>;
+  using ValueWord = std::conditional_t<DP == 64, uint16_t, uint32_t>;
   static constexpr int KU = DP >= 128 ? DP / 128 : 1;       // 16-byte pieces of keys a lane and half (DP 64: half of one)
   static constexpr int VW = DP == 256 ? 2 : 1;              // words of values a lane and token (DP 64: half of one)
   u32x4 k[2][KU];
-  uint32_t ks[2];                                           // the keys' scales: DP / 64 bytes
-  uint32_t v[8][VW];                                        // token 4 a + i
+  KeyScales ks[2];                                          // the keys' scales: DP / 64 bytes
+  ValueWord v[8][VW];                                       // token 4 a + i
   uint32_t vs[2];                                           // the values' scales of four tokens
 };
 
@@ -53,46 +57,61 @@ __device__ __forceinline__ LaneAt lane_at(int D, int page, int lane) {
   return o;
 }
 
+// A wave-uniform base in a buffer resource and a lane offset that never changes: a load costs no vector instruction
+// but itself.
 template <int DP, int DC>
 __device__ __forceinline__ void load_half(Tile<DP>& t, int a, const AttnLaunch& L, int h, int page, int place,
                                           const LaneAt& o) {
   const KvCache& c = L.a.c;
   const int D = DC ? DC : c.D;
   const int64_t head = (int64_t)page * c.heads + h, row = head * c.page + place;
-  const uint8_t* kc = c.k_codes + row * (D / 2);
-  const uint8_t* ks = c.k_scales + row * (D / 16);
-  const uint8_t* vc = c.v_codes + row * (D / 2);
-  const uint8_t* vs = c.v_scales + head * (D / 16) * c.page + place;
+  const auto kc = buf_rsrc(c.k_codes + row * (D / 2)), ks = buf_rsrc(c.k_scales + row * (D / 16));
+  const auto vc = buf_rsrc(c.v_codes + row * (D / 2)), vs = buf_rsrc(c.v_scales + head * (D / 16) * c.page + place);
   if constexpr (DP == 64) {
-    const u32x2 k = *(const u32x2*)(kc + o.k[0]);
+    const auto k = __builtin_amdgcn_raw_buffer_load_b64(kc, o.k[0], 0, 0);
     t.k[a][0][0] = k[0]; t.k[a][0][1] = k[1];
   } else {
 #pragma unroll
-    for (int u = 0; u < Tile<DP>::KU; ++u) t.k[a][u] = *(const u32x4*)(kc + o.k[u]);
+    for (int u = 0; u < Tile<DP>::KU; ++u) t.k[a][u] = __builtin_amdgcn_raw_buffer_load_b128(kc, o.k[u], 0, 0);
   }
-  if constexpr (DP == 64) t.ks[a] = ks[o.ks[0]];
-  else if constexpr (DP == 128) t.ks[a] = *(const uint16_t*)(ks + o.ks[0]);
-  else if constexpr (DC == 256) t.ks[a] = *(const uint32_t*)(ks + o.ks[0]);
-  else t.ks[a] = *(const uint16_t*)(ks + o.ks[0]) | (uint32_t)*(const uint16_t*)(ks + o.ks[1]) << 16;
+  if constexpr (DP == 64) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b8(ks, o.ks[0], 0, 0);
+  else if constexpr (DP == 128) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
+  else if constexpr (DC == 256) t.ks[a][0] = __builtin_amdgcn_raw_buffer_load_b32(ks, o.ks[0], 0, 0);
+  else {
+    t.ks[a][0] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
+    t.ks[a][1] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[1], 0, 0);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint8_t* p = vc + o.v + i * (D / 2);
-    if constexpr (DP == 64) t.v[4 * a + i][0] = *(const uint16_t*)p;
-    else if constexpr (DP == 128) t.v[4 * a + i][0] = *(const uint32_t*)p;
+    const uint32_t p = o.v + i * (D / 2);
+    if constexpr (DP == 64) t.v[4 * a + i][0] = __builtin_amdgcn_raw_buffer_load_b16(vc, p, 0, 0);
+    else if constexpr (DP == 128) t.v[4 * a + i][0] = __builtin_amdgcn_raw_buffer_load_b32(vc, p, 0, 0);
     else {
-      const u32x2 v = *(const u32x2*)p;
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(vc, p, 0, 0);
       t.v[4 * a + i][0] = v[0]; t.v[4 * a + i][1] = v[1];
     }
   }
-  t.vs[a] = *(const uint32_t*)(vs + o.vs);
+  t.vs[a] = __builtin_amdgcn_raw_buffer_load_b32(vs, o.vs, 0, 0);
 }
 
-// scale of dword j (eight codes) of a lane's keys
-template <int DP>
-__device__ __forceinline__ _Float16 key_scale(const f16x2 (&s)[2], int j) { return s[j / 4][(j / 2) & 1]; }
+// N consecutive values (a multiple of four) of type t at element i
+template <int N>
+__device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float* x) {
+  if (t == kF32) {
+#pragma unroll
+    for (int u = 0; u < N / 4; ++u) ((f32x4*)((float*)p + i))[u] = f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]};
+  } else {
+    u32x2 w[N / 4];
+#pragma unroll
+    for (int u = 0; u < N / 2; ++u)
+      w[u / 2][u & 1] = t == kBF16 ? pk_bf16_rne(x[2 * u], x[2 * u + 1]) : pk_f16(x[2 * u], x[2 * u + 1]);
+#pragma unroll
+    for (int u = 0; u < N / 4; ++u) ((u32x2*)((uint16_t*)p + i))[u] = w[u];
+  }
+}
 
 template <int DP, int NT, int DC, int W>
-__global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(AttnLaunch L) {
+__global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2) void k_attn_stream(AttnLaunch L) {
   constexpr int R = 16 * NT, KS = DP / 32, MV = DP / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kb = lane >> 4;
@@ -108,20 +127,56 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
   float c[NT];
   int lo_r[NT], hi_r[NT];
   const float sc = L.a.scale * L.a.c.k_ts[h] * kLog2e;
+  u32x4 raw[NT][KS];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = w.row0 + 16 * n + col;
+    const int r = w.row0 + 16 * n + col, rr = min(r, w.rows - 1), i = rr / L.G;
     row_keys(L, w, r, lo_r[n], hi_r[n]);
-    u32x4 raw[KS];
-    const int i = r / L.G;
-    const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (r - i * L.G)) * L.a.q_head;
-    float amax = 0.f;
+    const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
       const int d = DP / 4 * kb + 8 * j;
-      raw[j] = r < w.rows && d < D ? *(const u32x4*)(src + d) : u32x4{0, 0, 0, 0};
+      raw[n][j] = *(const u32x4*)(src + (DC || d < D ? d : 0));
+    }
+  }
+
+  // this workgroup's tiles of 32 keys
+  const int t0 = w.lo >> 5, t1 = (w.hi + 31) >> 5;
+  const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
+  const int ta = t0 + split * per, tb = min(t1, ta + per);
+  const LaneAt at = lane_at<DP>(D, L.a.c.page, lane);
+  struct Pages {
+    int p[2], place[2];
+  };
+  // The pages of tile t, or of the last one: every load is made, so that the waits can count them.
+  auto pages_of = [&](int t) {
+    Pages p;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(float16_of((uint16_t)(raw[j][e / 2] >> (16 * (e & 1))), L.a.q_type)));
+    for (int a = 0; a < 2; ++a) p.p[a] = page_of(L, b, 2 * min(t, tb - 1) + a, p.place[a]);
+    return p;
+  };
+  auto load = [&](Tile<DP>& t, const Pages& p) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) load_half<DP, DC>(t, a, L, h, is_page(L, p.p[a]) ? p.p[a] : 0, p.place[a], at);
+  };
+  Tile<DP> A, B;
+  Pages pa, pb;
+  int t = ta + wave;
+  const bool any = t < tb;
+  if (any) {
+    pa = pages_of(t);
+    pb = pages_of(t + W);
+    load(A, pa);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool row = w.row0 + 16 * n + col < w.rows;
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      if (!row || (!DC && DP / 4 * kb + 8 * j >= D)) raw[n][j] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(float16_of((uint16_t)(raw[n][j][e / 2] >> (16 * (e & 1))), L.a.q_type)));
     }
     amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
@@ -132,8 +187,8 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
       u32x4 x;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        x[e] = pk_f16(sign * ldexpf(float16_of((uint16_t)raw[j][e], L.a.q_type), sh),
-                      sign * ldexpf(float16_of((uint16_t)(raw[j][e] >> 16), L.a.q_type), sh));
+        x[e] = pk_f16(sign * ldexpf(float16_of((uint16_t)raw[n][j][e], L.a.q_type), sh),
+                      sign * ldexpf(float16_of((uint16_t)(raw[n][j][e] >> 16), L.a.q_type), sh));
       q[n][j] = as_f16x8(x);
     }
     c[n] = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);   // not 0, which -inf would turn into NaN
@@ -144,49 +199,30 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
 #pragma unroll
   for (int n = 0; n < NT; ++n) { mc[n] = kUnset; l[n] = 0.f; }
 
-  // this workgroup's tiles of 32 keys
-  const int t0 = w.lo >> 5, t1 = (w.hi + 31) >> 5;
-  const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
-  const int ta = t0 + split * per, tb = min(t1, ta + per);
-  const LaneAt at = lane_at<DP>(D, L.a.c.page, lane);
-
-  Tile<DP> cur, nxt;
-  int pg[2] = {}, pn[2] = {}, place[2];
-  int t = ta + wave;
-  if (t < tb) {
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      pg[a] = page_of(L, b, 2 * t + a, place[a]);
-      load_half<DP, DC>(cur, a, L, h, max(pg[a], 0), place[a], at);
-    }
-  }
-  for (; t < tb; t += W) {
-    const int tn = t + W;
-    if (tn < tb) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        pn[a] = page_of(L, b, 2 * tn + a, place[a]);
-        load_half<DP, DC>(nxt, a, L, h, max(pn[a], 0), place[a], at);
-      }
-    }
+  auto compute = [&](const Tile<DP>& cur, const Pages& pg, int t) {
     // logits
     f32x4 s[NT][2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       f16x2 ks[2];
-      ks[0] = e4m3x2_f16<false>(cur.ks[a]);
-      ks[1] = e4m3x2_f16<true>(cur.ks[a]);
+      if constexpr (DP == 256) {
+        ks[0] = e4m3x2_f16<false>(cur.ks[a][0]);
+        ks[1] = DC ? e4m3x2_f16<true>(cur.ks[a][0]) : e4m3x2_f16<false>(cur.ks[a][1]);
+      } else {
+        ks[0] = e4m3x2_f16<false>(cur.ks[a]);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const f16x8 k = fp4x8_f16(cur.k[a][j / 4][j % 4], key_scale<DP>(ks, j));
+        const f16x8 k = fp4x8_f16(cur.k[a][j / 4][j % 4], ks[j / 4][(j / 2) & 1]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][j], s[n][a], 0, 0, 0);
       }
     }
     uint32_t vs[2] = {cur.vs[0], cur.vs[1]};
-    const bool whole = 32 * t >= w.lo_all && 32 * t + 32 <= w.hi_all && pg[0] >= 0 && pg[1] >= 0;
+    const bool there[2] = {is_page(L, pg.p[0]), is_page(L, pg.p[1])};
+    const bool whole = 32 * t >= w.lo_all && 32 * t + 32 <= w.hi_all && there[0] && there[1];
     if (!whole) {
 #pragma unroll
       for (int a = 0; a < 2; ++a)
@@ -195,9 +231,9 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
           const int tok = 32 * t + 16 * a + 4 * kb + i;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (!(pg[a] >= 0 && tok >= lo_r[n] && tok < hi_r[n])) s[n][a][i] = -__builtin_inff();
+            if (!(there[a] && tok >= lo_r[n] && tok < hi_r[n])) s[n][a][i] = -__builtin_inff();
           // what lies in a slot that no row keeps may be anything: its value's scale becomes 0
-          if (!(pg[a] >= 0 && tok >= w.lo && tok < w.hi)) vs[a] &= ~(0xFFu << (8 * i));
+          if (!(there[a] && tok >= w.lo && tok < w.hi)) vs[a] &= ~(0xFFu << (8 * i));
         }
     }
     // reference and p
@@ -256,8 +292,21 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
     SSN_VALUE(0) SSN_VALUE(1) SSN_VALUE(2) SSN_VALUE(3) SSN_VALUE(4) SSN_VALUE(5) SSN_VALUE(6) SSN_VALUE(7)
     SSN_VALUE(8) SSN_VALUE(9) SSN_VALUE(10) SSN_VALUE(11) SSN_VALUE(12) SSN_VALUE(13) SSN_VALUE(14) SSN_VALUE(15)
 #undef SSN_VALUE
-    cur = nxt;
-    pg[0] = pn[0]; pg[1] = pn[1];
+  };
+
+  // two tiles a turn, each loaded while the other is worked on; page numbers a tile further ahead
+  while (t < tb) {
+    Pages pn = pages_of(t + 2 * W);
+    load(B, pb);
+    compute(A, pa, t);
+    t += W;
+    if (t >= tb) break;
+    pa = pn;
+    pn = pages_of(t + 2 * W);
+    load(A, pa);
+    compute(B, pb, t);
+    t += W;
+    pb = pn;
   }
 
   // the waves' results brought to one reference and added up, the upper half into the lower until one is left
@@ -300,59 +349,103 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : 2) void k_attn_stream(
   for (int n = 0; n < NT; ++n) {
     const int r = w.row0 + 16 * n + col;
     if (r >= w.rows) continue;
+    const int64_t part = ((int64_t)item * L.splits + split) * R + 16 * n + col;
+    const int i0 = r / L.G;
+    const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
     if (L.splits > 1) {
-      const int64_t at0 = ((int64_t)item * L.splits + split) * R + 16 * n + col;
-      if (kb == 0) { L.part_ml[2 * at0] = mc[n]; L.part_ml[2 * at0 + 1] = l[n]; }
+      if (kb == 0) *(f32x2*)(L.part_ml + 2 * part) = f32x2{mc[n], l[n]};
       if (!(l[n] != 0.f)) continue;                 // the join skips a part without keys
+    } else if (L.a.lse && kb == 0) {
+      L.a.lse[head] = l[n] != 0.f ? (mc[n] + log2f(l[n])) * kLn2 : -__builtin_inff();
+    }
+    const float f = L.splits > 1 ? 1.f : l[n] != 0.f ? L.a.c.v_ts[h] / l[n] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const int d = MV * (4 * kb + i);
+      if (!DC && d >= D) continue;
+      float x[MV];
 #pragma unroll
-        for (int v = 0; v < MV; ++v) {
-          const int d = MV * (4 * kb + i) + v;
-          if (d < D) L.part_o[at0 * D + d] = o[n][v][i];
-        }
-    } else {
-      const int i0 = r / L.G;
-      const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
-      const float f = l[n] != 0.f ? L.a.c.v_ts[h] / l[n] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int v = 0; v < MV; ++v) {
-          const int d = MV * (4 * kb + i) + v;
-          if (d < D) store_elem(L.a.out, L.a.out_type, head * D + d, o[n][v][i] * f);
-        }
-      if (L.a.lse && kb == 0) L.a.lse[head] = l[n] != 0.f ? (mc[n] + log2f(l[n])) * kLn2 : -__builtin_inff();
+      for (int v = 0; v < MV; ++v) x[v] = o[n][v][i] * f;
+      if (L.splits > 1) store_run<MV>(L.part_o, kF32, part * D + d, x);
+      else store_run<MV>(L.a.out, L.a.out_type, head * D + d, x);
     }
   }
 }
 
-// out = sum over the parts of O 2^(m - M) / sum of l 2^(m - M), one workgroup a row
-constexpr int kJoin = 256;
-__global__ __launch_bounds__(kJoin) void k_attn_join(AttnLaunch L, int R) {
-  const int item = blockIdx.x / R, rl = blockIdx.x % R;
-  const int rt = item % L.row_tiles, bh = item / L.row_tiles;
+// out = sum over the parts of O 2^(m - M) / sum of l 2^(m - M). TR lanes share a row (a wave, or the workgroup where
+// there are many parts): a lane takes four d of every G-th part, and its loads wait for nothing but the row's number.
+constexpr int kMaxSplits = 256;
+template <int TR>
+__global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L, int R, int max_rows) {
+  constexpr int RW = TR == 64 ? 4 : 1, NS = kMaxSplits / 64, U = 4;
+  const int t = threadIdx.x % TR, rw = threadIdx.x / TR, lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * RW + rw;
+  const int bh = (int)(id / max_rows), r = (int)(id - (int64_t)bh * max_rows);
   const int h = bh % L.a.c.heads, b = bh / L.a.c.heads, D = L.a.c.D;
-  Work w;
-  if (!find_work(L, b, h, rt, R, w)) return;
-  const int r = w.row0 + rl;
-  if (r >= w.rows) return;
-  const int64_t at0 = (int64_t)item * L.splits * R + rl;
-  float m = kUnset;
-  for (int s = 0; s < L.splits; ++s) m = fmaxf(m, L.part_ml[2 * (at0 + (int64_t)s * R)]);
-  float sum = 0.f, acc = 0.f;
-  const int d = threadIdx.x;
-  for (int s = 0; s < L.splits; ++s) {
-    const int64_t at = at0 + (int64_t)s * R;
-    const float l = L.part_ml[2 * at + 1], f = exp2_hw(L.part_ml[2 * at] - m);
-    if (!(l != 0.f)) continue;
-    sum += l * f;
-    if (d < D) acc += L.part_o[at * D + d] * f;
+  int64_t q0, n;
+  const bool live = b < L.a.B && find_queries(L, b, q0, n) && r < n * L.G;
+  __shared__ f32x4 acc[RW][TR];
+  const int rt = live ? r / R : 0;
+  const int64_t at0 = live ? ((int64_t)bh * L.row_tiles + rt) * L.splits * R + (r - rt * R) : 0;
+  // m and l of part s in lane s % 64
+  float m[NS], l[NS], top = kUnset, sum = 0.f;
+  const int ns = (L.splits + 63) / 64;
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    m[x] = kUnset; l[x] = 0.f;
+    if (x < ns && 64 * x + lane < L.splits) {
+      const f32x2 ml = *(const f32x2*)(L.part_ml + 2 * (at0 + (int64_t)(64 * x + lane) * R));
+      m[x] = ml[0]; l[x] = ml[1];
+    }
   }
+  const int D4 = D / 4, groups = TR / D4, g = t / D4, d = 4 * (t - g * D4);
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  const float* src = L.part_o + at0 * D + d;
+  f32x4 first[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) first[u] = g < groups && g + u * groups < L.splits ? *(const f32x4*)(src + (int64_t)(g + u * groups) * R * D) : o;
+#pragma unroll
+  for (int x = 0; x < NS; ++x) top = fmaxf(top, m[x]);
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    m[x] = l[x] != 0.f ? exp2_hw(m[x] - top) : 0.f;     // a part without keys wrote no O: its factor 0 drops what is read
+    if (m[x] != 0.f) sum += l[x] * m[x];
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x, 64);
+  auto factor = [&](int s) {
+    float f = __shfl(m[0], s & 63, 64);
+#pragma unroll
+    for (int x = 1; x < NS; ++x)
+      if (x < ns) { const float y = __shfl(m[x], s & 63, 64); if (s / 64 == x) f = y; }
+    return f;
+  };
+  for (int s0 = 0; s0 < L.splits; s0 += U * groups) {
+    f32x4 next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + g + (u + U) * groups;
+      next[u] = g < groups && s < L.splits ? *(const f32x4*)(src + (int64_t)s * R * D) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = factor(min(s0 + g + u * groups, L.splits - 1));
+      if (f != 0.f && s0 + g + u * groups < L.splits) o += first[u] * f;
+      first[u] = next[u];
+    }
+  }
+  acc[rw][t] = o;
+  __syncthreads();
+  if (!live || t >= D4) return;
+  for (int x = 1; x < groups; ++x) o += acc[rw][t + x * D4];
   const int i0 = r / L.G;
-  const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
-  if (d < D) store_elem(L.a.out, L.a.out_type, head * D + d, sum != 0.f ? acc * (L.a.c.v_ts[h] / sum) : 0.f);
-  if (L.a.lse && d == 0) L.a.lse[head] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -__builtin_inff();
+  const int64_t head = (q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
+  const float by = sum != 0.f ? L.a.c.v_ts[h] / sum : 0.f;
+  const float x[4] = {o[0] * by, o[1] * by, o[2] * by, o[3] * by};
+  store_run<4>(L.a.out, L.a.out_type, head * D + d, x);
+  if (L.a.lse && t == 0) L.a.lse[head] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
 constexpr int kWaves = 4;
@@ -362,17 +455,23 @@ struct Shape {
   int64_t items;
 };
 
-// Rows of a workgroup: the fewest of 16, 32 and (up to a width of 128) 64 that hold a sequence's rows. Splits: some 16 waves a compute unit,
-// each with four tiles at least.
+// Rows of a workgroup: the fewest sets of 16 that hold a sequence's rows, four at most (two beyond a width of 128).
+// Splits: as many workgroups as the card holds at once, each wave with kMinTiles tiles at least.
+constexpr int kMinTiles = 4;
 Shape shape_of(const AttnArgs& a) {
   Shape s;
   const int64_t rows = a.max_q * (a.Hq / a.c.heads);
-  s.R = rows <= 16 ? 16 : rows <= 32 || a.c.D > 128 ? 32 : 64;
+  const int most = a.c.D > 128 ? 2 : 4;
+  const int nt = (int)std::min<int64_t>((rows + 15) / 16, most);
+  s.R = 16 * nt;
   s.row_tiles = (int)((rows + s.R - 1) / s.R);
   s.items = a.B * a.c.heads * s.row_tiles;
-  const int64_t tiles = (a.max_kv + 31) / 32;
-  const int64_t want = (4 * (int64_t)cu_count() + s.items - 1) / s.items;
-  s.splits = (int)std::max<int64_t>(1, std::min(want, tiles / (4 * kWaves)));
+  // keys that a workgroup's rows can keep
+  const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + s.R + 31) : a.max_kv;
+  const int64_t tiles = (keys + 31) / 32;
+  const int resident = nt * (a.c.D > 128 ? 2 : 1) >= 4 ? 1 : nt * (a.c.D > 128 ? 2 : 1) >= 2 ? 2 : 3;
+  const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
+  s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
   return s;
 }
 
@@ -381,7 +480,10 @@ void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
   const dim3 grid((unsigned)(s.items * s.splits)), block(64 * kWaves);
   if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
   else if (s.R == 32) hipLaunchKernelGGL((k_attn_stream<DP, 2, DC, kWaves>), grid, block, 0, st, L);
-  else if constexpr (DP <= 128) hipLaunchKernelGGL((k_attn_stream<DP, 4, DC, kWaves>), grid, block, 0, st, L);
+  else if constexpr (DP <= 128) {
+    if (s.R == 48) hipLaunchKernelGGL((k_attn_stream<DP, 3, DC, kWaves>), grid, block, 0, st, L);
+    else hipLaunchKernelGGL((k_attn_stream<DP, 4, DC, kWaves>), grid, block, 0, st, L);
+  }
 }
 
 }  // namespace
@@ -402,6 +504,7 @@ hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t st) {
   L.a = a;
   L.pd = page_div((uint32_t)(a.c.page / 16));
   L.G = a.Hq / a.c.heads;
+  L.each = a.q_offsets ? 0 : a.Tq / a.B;
   L.row_tiles = s.row_tiles;
   L.splits = s.splits;
   L.part_o = (float*)a.ws;
@@ -413,7 +516,13 @@ hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t st) {
   else if (D < 128) launch<128, 0>(L, s, st);
   else if (D == 256) launch<256, 256>(L, s, st);
   else launch<256, 0>(L, s, st);
-  if (s.splits > 1) hipLaunchKernelGGL(k_attn_join, dim3((unsigned)(s.items * s.R)), dim3(kJoin), 0, st, L, s.R);
+  if (s.splits > 1) {
+    const int max_rows = (int)(a.max_q * L.G);
+    const int64_t rows = a.B * a.c.heads * max_rows;
+    if (s.splits > 64) hipLaunchKernelGGL((k_attn_join<1024>), dim3((unsigned)rows), dim3(1024), 0, st, L, s.R, max_rows);
+    else if (s.splits > 16) hipLaunchKernelGGL((k_attn_join<256>), dim3((unsigned)rows), dim3(256), 0, st, L, s.R, max_rows);
+    else hipLaunchKernelGGL((k_attn_join<64>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, L, s.R, max_rows);
+  }
   return hipGetLastError();
 }
 
