@@ -789,13 +789,14 @@ int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_toke
   if (!(scale - scale == 0.f)) return fail(SSN_E_RANGE, "%s: scale is not finite", fn);
   if (!q_offsets && B > 0 && Tq % B)
     return fail(SSN_E_SHAPE, "%s: without q_offsets Tq=%lld must be a multiple of B=%lld", fn, (long long)Tq, (long long)B);
-  if (algo != SSN_ALGO_AUTO && algo != SSN_ALGO_STREAM)
-    return fail(SSN_E_ALGO, "%s: algorithm %d is not available (STREAM)", fn, algo);
+  if (algo != SSN_ALGO_AUTO && algo != SSN_ALGO_STREAM && algo != SSN_ALGO_MFMA)
+    return fail(SSN_E_ALGO, "%s: algorithm %d is not available (STREAM, MFMA)", fn, algo);
   if ((st = check_strides(fn, "Q", q_token_stride, q_head_stride, 2))) return st;
   REQUIRE_OPT_ELEM_PTR(lse);
   if (max_kv > max_blocks * page_size)
     return fail(SSN_E_SHAPE, "%s: max_kv=%lld is more than max_blocks=%lld pages hold", fn, (long long)max_kv, (long long)max_blocks);
-  if (algo_used) *algo_used = SSN_ALGO_STREAM;
+  const bool tile = algo == SSN_ALGO_MFMA || (algo == SSN_ALGO_AUTO && ssn::attn_takes_tile(a));
+  if (algo_used) *algo_used = tile ? SSN_ALGO_MFMA : SSN_ALGO_STREAM;
   if (Tq == 0 || B == 0 || max_q == 0) return ok();
   REQUIRE_PTR(Q); REQUIRE_PTR(out); REQUIRE_ELEM_PTR(seq_lens); REQUIRE_OPT_ELEM_PTR(q_offsets);
   if (max_blocks > 0) REQUIRE_ELEM_PTR(block_table);
@@ -805,9 +806,9 @@ int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_toke
     if (workspace_bytes < need)
       return fail(SSN_E_RANGE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)need);
   }
-  if (ssn::attn_workgroups(a) > kMaxGrid)
+  if (ssn::attn_workgroups(a, tile) > kMaxGrid)
     return fail(SSN_E_SHAPE, "%s: B * Hkv * rows need more than 2^23 workgroups", fn);
-  return hip_status(ssn::launch_attn_stream(a, as_stream(stream)), fn);
+  return hip_status(ssn::launch_attn(a, tile, as_stream(stream)), fn);
 }
 
 }  // extern "C"

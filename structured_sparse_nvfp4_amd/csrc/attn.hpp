@@ -146,6 +146,22 @@ __device__ __forceinline__ uint32_t pk_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
+// N consecutive values (a multiple of four) of type t at element i
+template <int N>
+__device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float* x) {
+  if (t == kF32) {
+#pragma unroll
+    for (int u = 0; u < N / 4; ++u) ((f32x4*)((float*)p + i))[u] = f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]};
+  } else {
+    u32x2 w[N / 4];
+#pragma unroll
+    for (int u = 0; u < N / 2; ++u)
+      w[u / 2][u & 1] = t == kBF16 ? pk_bf16_rne(x[2 * u], x[2 * u + 1]) : pk_f16(x[2 * u], x[2 * u + 1]);
+#pragma unroll
+    for (int u = 0; u < N / 4; ++u) ((u32x2*)((uint16_t*)p + i))[u] = w[u];
+  }
+}
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Exponent shift that brings a row's largest magnitude into [2^15, 2^16); 0 for a row of zeros or not finite.
@@ -155,5 +171,8 @@ __device__ __forceinline__ int row_shift(float amax) {
   (void)frexpf(amax, &e);                          // amax = f 2^e, f in [1/2, 1)
   return 16 - e;
 }
+
+constexpr int kTileRows = 128;                   // of a workgroup of k_attn_tile
+hipError_t launch_attn_tile(const AttnLaunch& L, int64_t groups, hipStream_t s);
 
 }  // namespace ssn

@@ -94,22 +94,6 @@ __device__ __forceinline__ void load_half(Tile<DP>& t, int a, const AttnLaunch& 
   t.vs[a] = __builtin_amdgcn_raw_buffer_load_b32(vs, o.vs, 0, 0);
 }
 
-// N consecutive values (a multiple of four) of type t at element i
-template <int N>
-__device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float* x) {
-  if (t == kF32) {
-#pragma unroll
-    for (int u = 0; u < N / 4; ++u) ((f32x4*)((float*)p + i))[u] = f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]};
-  } else {
-    u32x2 w[N / 4];
-#pragma unroll
-    for (int u = 0; u < N / 2; ++u)
-      w[u / 2][u & 1] = t == kBF16 ? pk_bf16_rne(x[2 * u], x[2 * u + 1]) : pk_f16(x[2 * u], x[2 * u + 1]);
-#pragma unroll
-    for (int u = 0; u < N / 4; ++u) ((u32x2*)((uint16_t*)p + i))[u] = w[u];
-  }
-}
-
 template <int DP, int NT, int DC, int W>
 __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2) void k_attn_stream(AttnLaunch L) {
   constexpr int R = 16 * NT, KS = DP / 32, MV = DP / 16;
@@ -455,24 +439,29 @@ struct Shape {
   int64_t items;
 };
 
-// Rows of a workgroup: the fewest sets of 16 that hold a sequence's rows, four at most (two beyond a width of 128).
-// Splits: as many workgroups as the card holds at once, each wave with kMinTiles tiles at least.
+// STREAM. Rows of a workgroup: the fewest sets of 16 that hold a sequence's rows, four at most (two beyond a width of
+// 128). Splits: as many workgroups as the card holds at once, each wave with kMinTiles tiles at least.
+// MFMA: 128 rows; splits likewise, of eight tiles at least.
 constexpr int kMinTiles = 4;
-Shape shape_of(const AttnArgs& a) {
+Shape shape_of(const AttnArgs& a, bool tile) {
   Shape s;
   const int64_t rows = a.max_q * (a.Hq / a.c.heads);
-  const int most = a.c.D > 128 ? 2 : 4;
-  const int nt = (int)std::min<int64_t>((rows + 15) / 16, most);
-  s.R = 16 * nt;
+  const int wide = a.c.D > 128 ? 2 : 1;
+  const int nt = (int)std::min<int64_t>((rows + 15) / 16, 4 / wide);
+  s.R = tile ? kTileRows : 16 * nt;
   s.row_tiles = (int)((rows + s.R - 1) / s.R);
   s.items = a.B * a.c.heads * s.row_tiles;
   // keys that a workgroup's rows can keep
   const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + s.R + 31) : a.max_kv;
   const int64_t tiles = (keys + 31) / 32;
-  const int resident = nt * (a.c.D > 128 ? 2 : 1) >= 4 ? 1 : nt * (a.c.D > 128 ? 2 : 1) >= 2 ? 2 : 3;
+  const int resident = tile ? 2 : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 3;
   const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
   s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
   return s;
+}
+
+int64_t workspace_of(const AttnArgs& a, const Shape& s) {
+  return s.splits > 1 ? s.items * s.splits * s.R * (a.c.D + 2) * 4 : 0;
 }
 
 template <int DP, int DC>
@@ -488,18 +477,20 @@ void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
 
 }  // namespace
 
+// The tiles where a sequence has more rows than one workgroup of the stream takes.
+bool attn_takes_tile(const AttnArgs& a) { return a.max_q * (a.Hq / a.c.heads) > (a.c.D > 128 ? 32 : 64); }
+
 int64_t attn_workspace(const AttnArgs& a) {
-  const Shape s = shape_of(a);
-  return s.splits > 1 ? s.items * s.splits * s.R * (a.c.D + 2) * 4 : 0;
+  return std::max(workspace_of(a, shape_of(a, false)), workspace_of(a, shape_of(a, true)));
 }
 
-int64_t attn_workgroups(const AttnArgs& a) {
-  const Shape s = shape_of(a);
+int64_t attn_workgroups(const AttnArgs& a, bool tile) {
+  const Shape s = shape_of(a, tile);
   return s.items * s.splits;
 }
 
-hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t st) {
-  const Shape s = shape_of(a);
+hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {
+  const Shape s = shape_of(a, tile);
   AttnLaunch L;
   L.a = a;
   L.pd = page_div((uint32_t)(a.c.page / 16));
@@ -510,7 +501,10 @@ hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t st) {
   L.part_o = (float*)a.ws;
   L.part_ml = L.part_o + (s.splits > 1 ? s.items * s.splits * s.R * a.c.D : 0);
   const int D = a.c.D;
-  if (D == 64) launch<64, 64>(L, s, st);
+  if (tile) {
+    const hipError_t e = launch_attn_tile(L, s.items * s.splits, st);
+    if (e != hipSuccess) return e;
+  } else if (D == 64) launch<64, 64>(L, s, st);
   else if (D < 64) launch<64, 0>(L, s, st);
   else if (D == 128) launch<128, 128>(L, s, st);
   else if (D < 128) launch<128, 0>(L, s, st);

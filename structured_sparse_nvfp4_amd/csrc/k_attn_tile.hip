@@ -1,0 +1,298 @@
+// Attention over the 4-bit cache for many query rows to a key head: prompts and chunks of prompts.
+//
+// Bound by the matrix cores and, beside them, by the exponentials. A workgroup takes 32 rows a wave and walks tiles of
+// TK keys: all its threads decode a tile's keys and values once, to f16 in LDS, while the loads of the next tile are in
+// flight; two buffers, one barrier a tile. With v_mfma_f32_32x32x16_f16, l the lane and h = l / 32:
+//   S^T: A = keys from LDS (token l % 32, d = 16 s + 8 h ..), B = Q from registers. The result has token
+//        8 (i / 4) + 4 h + i % 4 of 32 in register i, row l % 32.
+//   O^T: B = P, the lane's own eight tokens of every 16 (8 (x / 4) + 4 h + x % 4); A = values, stored transposed and in
+//        that order of tokens, so an operand is one 16-byte read. Row p of tile m is d = (DP / 32) p + m, which gives the
+//        decoding threads, eight d of four tokens each, rows whose LDS banks do not meet (rows are 16 bytes longer than
+//        their data for that), and a lane of the result runs of DP / 8 consecutive d.
+#include <algorithm>
+
+#include "attn.hpp"
+#include "device_once.hpp"
+
+namespace ssn {
+namespace {
+
+// LDS writes done before, LDS reads after; global loads stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <int DP, int TK>
+struct Lds {
+  static constexpr int KS = DP * 2 + 16, VS = TK * 2 + 16;   // bytes of a row: of a token's keys, of a d's values
+  uint8_t k[TK * KS];
+  uint8_t v[DP * VS];
+  uint32_t there[4];                                         // byte u % 4 of word u / 4: unit u of 16 tokens has a page
+};
+
+template <int DP, int W, int TK>
+__global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
+  static_assert(32 * W == kTileRows, "");
+  constexpr int R = 32 * W, NTH = 64 * W, KS = DP / 16, MT = DP / 32, AT = TK / 32;
+  constexpr int NK = TK * DP / 32, IT = 2 * NK / NTH;        // pieces of 16 bytes of keys, as many of values; a thread's
+  static_assert(NK % 64 == 0 && 2 * NK % NTH == 0, "");
+  using Buf = Lds<DP, TK>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_raw[];
+  Buf* const lds = (Buf*)lds_raw;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int split = blockIdx.x % L.splits, id = blockIdx.x / L.splits;
+  const int nbh = (int)L.a.B * L.a.c.heads;
+  // the last rows of all sequences first: with causal they have the most keys
+  const int rt = L.row_tiles - 1 - id / nbh, bh = id % nbh;
+  const int h = bh % L.a.c.heads, b = bh / L.a.c.heads;
+  const KvCache& c = L.a.c;
+  const int D = c.D;
+  Work w;
+  if (!find_work(L, b, h, rt, R, w)) return;
+
+  // what this thread brings of every tile
+  int tok[IT], dd[IT];
+  bool isv[IT];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int p = it * NTH + tid;
+    isv[it] = it * NTH + 64 * wave >= NK;
+    const int q = isv[it] ? p - NK : p;
+    tok[it] = isv[it] ? q / (DP / 8) * 4 : q / (DP / 32);
+    dd[it] = isv[it] ? q % (DP / 8) * 8 : q % (DP / 32) * 32;
+  }
+  const int t0 = w.lo / TK, t1 = (w.hi + TK - 1) / TK;
+  const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
+  const int ta = t0 + split * per, tb = min(t1, ta + per);
+
+  u32x4 raw[IT];
+  uint32_t scl[IT];
+  int pg[IT], place[IT];
+  auto find_pages = [&](int t) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) pg[it] = page_of(L, b, (t * TK + tok[it]) >> 4, place[it]);
+  };
+  auto load = [&]() {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const bool ok = is_page(L, pg[it]);
+      const int64_t head = (int64_t)(ok ? pg[it] : 0) * c.heads + h;
+      const int at = place[it] + (tok[it] & 15);
+      const int64_t row = head * c.page + at;
+      raw[it] = u32x4{0, 0, 0, 0};
+      scl[it] = 0;
+      if (dd[it] < D) {
+        if (isv[it]) {
+          const uint8_t* p = c.v_codes + row * (D / 2) + dd[it] / 2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[it][i] = *(const uint32_t*)(p + i * (D / 2));
+          scl[it] = *(const uint32_t*)(c.v_scales + (head * (D / 16) + dd[it] / 16) * c.page + at);
+        } else {
+          raw[it] = *(const u32x4*)(c.k_codes + row * (D / 2) + dd[it] / 2);
+          scl[it] = *(const uint16_t*)(c.k_scales + row * (D / 16) + dd[it] / 16);
+        }
+      }
+    }
+  };
+  auto stage = [&](Buf& f, int t) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const bool ok = is_page(L, pg[it]);
+      if (isv[it]) {
+        uint32_t s = scl[it];
+        // what lies in a slot that no row keeps may be anything: its value's scale becomes 0
+        if (!ok || t * TK < w.lo || t * TK + TK > w.hi) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = t * TK + tok[it] + i;
+            if (!ok || x < w.lo || x >= w.hi) s &= ~(0xFFu << (8 * i));
+          }
+        }
+        const f16x2 s01 = e4m3x2_f16<false>(s), s23 = e4m3x2_f16<true>(s);
+        uint32_t e01, o01, e23, o23;
+        pair_tokens(raw[it][0], raw[it][1], e01, o01);
+        pair_tokens(raw[it][2], raw[it][3], e23, o23);
+        const u32x2 d[8] = {{fp4x2_f16<0>(e01, s01), fp4x2_f16<0>(e23, s23)}, {fp4x2_f16<0>(o01, s01), fp4x2_f16<0>(o23, s23)},
+                            {fp4x2_f16<1>(e01, s01), fp4x2_f16<1>(e23, s23)}, {fp4x2_f16<1>(o01, s01), fp4x2_f16<1>(o23, s23)},
+                            {fp4x2_f16<2>(e01, s01), fp4x2_f16<2>(e23, s23)}, {fp4x2_f16<2>(o01, s01), fp4x2_f16<2>(o23, s23)},
+                            {fp4x2_f16<3>(e01, s01), fp4x2_f16<3>(e23, s23)}, {fp4x2_f16<3>(o01, s01), fp4x2_f16<3>(o23, s23)}};
+        // token 16 s + 8 x + 4 h + e is at 16 s + 8 h + 4 x + e
+        const int pos = (tok[it] & ~15) | (tok[it] & 4) << 1 | (tok[it] & 8) >> 1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rho = (dd[it] + j) / MT, m = j % MT;
+          *(u32x2*)(f.v + (m * 32 + rho) * Buf::VS + pos * 2) = d[j];
+        }
+      } else {
+        const f16x2 s = e4m3x2_f16<false>(scl[it]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *(f16x8*)(f.k + tok[it] * Buf::KS + (dd[it] + 8 * j) * 2) = fp4x8_f16(raw[it][j], s[j / 2]);
+        if (dd[it] == 0 && !(tok[it] & 15)) ((uint8_t*)f.there)[tok[it] >> 4] = ok;
+      }
+    }
+  };
+  if (ta < tb) {
+    find_pages(ta);
+    load();
+  }
+
+  // queries: the lane's row, d = 16 s + 8 half ..
+  const int r = w.row0 + 32 * wave + col;
+  int lo_r, hi_r;
+  row_keys(L, w, r, lo_r, hi_r);
+  const float sc = L.a.scale * c.k_ts[h] * kLog2e;
+  f16x8 q[KS];
+  float cf;
+  {
+    const int rr = min(r, w.rows - 1), i = rr / L.G;
+    const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
+    u32x4 x[KS];
+    float amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = 16 * s + 8 * half;
+      x[s] = *(const u32x4*)(src + (d < D ? d : 0));
+      if (r >= w.rows || d >= D) x[s] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(float16_of((uint16_t)(x[s][e / 2] >> (16 * (e & 1))), L.a.q_type)));
+    }
+    amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
+    const int sh = row_shift(amax);
+    const float sign = sc < 0.f ? -1.f : 1.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      u32x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = pk_f16(sign * ldexpf(float16_of((uint16_t)x[s][e], L.a.q_type), sh),
+                      sign * ldexpf(float16_of((uint16_t)(x[s][e] >> 16), L.a.q_type), sh));
+      q[s] = as_f16x8(y);
+    }
+    cf = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);    // not 0, which -inf would turn into NaN
+  }
+  // keys that some row, and that every row, of this wave keeps (rows behind the last aside)
+  const int first = w.row0 + 32 * wave, last = min(first + 31, w.rows - 1);
+  int wlo, whi, wlo_all, whi_all;
+  row_keys(L, w, min(first, w.rows - 1), wlo, whi_all);
+  row_keys(L, w, max(last, 0), wlo_all, whi);
+  wlo = max(wlo, 0);
+  if (first >= w.rows) whi = 0;
+
+  f32x16 o[MT] = {};
+  float mc = kUnset, l = 0.f;
+
+  for (int t = ta; t < tb; ++t) {
+    Buf& f = lds[(t - ta) & 1];
+    stage(f, t);
+    if (t + 1 < tb) {
+      find_pages(t + 1);
+      load();
+    }
+    lds_barrier();
+    const int k0 = t * TK;
+    if (k0 >= whi || k0 + TK <= wlo) continue;       // nothing for this wave (it still brings its part)
+    f32x16 s[AT];
+#pragma unroll
+    for (int a = 0; a < AT; ++a) {
+      s[a] = f32x16{};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const f16x8 k = *(const f16x8*)(f.k + (32 * a + col) * Buf::KS + (16 * x + 8 * half) * 2);
+        s[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x], s[a], 0, 0, 0);
+      }
+    }
+    constexpr uint32_t all = TK == 64 ? 0x01010101u : 0x0101u;
+    const uint32_t there = __builtin_amdgcn_readfirstlane(f.there[0]) & (TK == 64 ? ~0u : 0xFFFFu);
+    if (k0 < wlo_all || k0 + TK > whi_all || there != all) {
+#pragma unroll
+      for (int a = 0; a < AT; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int x = 32 * a + 8 * (i / 4) + 4 * half + i % 4;
+          if (!((there >> (8 * (2 * a + i / 8)) & 1) && k0 + x >= lo_r && k0 + x < hi_r)) s[a][i] = -__builtin_inff();
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16 * AT; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+    if (__any(top * cf - mc > kTop)) {
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float to = fmaxf(mc, top * cf - kShift), by = exp2_hw(mc - to);
+      mc = to;
+      l *= by;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) o[m] *= by;
+    }
+    f16x8 p[2 * AT];
+#pragma unroll
+    for (int y = 0; y < 2 * AT; ++y) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = exp2_hw(fmaf(s[y / 2][8 * (y & 1) + i], cf, -mc));
+        l += e[i];
+      }
+      p[y] = as_f16x8(u32x4{pk_f16(e[0], e[1]), pk_f16(e[2], e[3]), pk_f16(e[4], e[5]), pk_f16(e[6], e[7])});
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int y = 0; y < 2 * AT; ++y) {
+        const f16x8 v = *(const f16x8*)(f.v + (m * 32 + col) * Buf::VS + (16 * y + 8 * half) * 2);
+        o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[y], o[m], 0, 0, 0);
+      }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (r >= w.rows) return;
+  const int64_t part = (((int64_t)bh * L.row_tiles + rt) * L.splits + split) * R + 32 * wave + col;
+  const int i0 = r / L.G;
+  const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
+  if (L.splits > 1) {
+    if (half == 0) *(f32x2*)(L.part_ml + 2 * part) = f32x2{mc, l};
+    if (!(l != 0.f)) return;
+  } else if (L.a.lse && half == 0) {
+    L.a.lse[head] = l != 0.f ? (mc + log2f(l)) * kLn2 : -__builtin_inff();
+  }
+  const float by = L.splits > 1 ? 1.f : l != 0.f ? c.v_ts[h] / l : 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int d = MT * (8 * u + 4 * half);           // 4 MT consecutive d
+    float x[4 * MT];
+#pragma unroll
+    for (int e = 0; e < 4 * MT; ++e) x[e] = o[e % MT][4 * u + e / MT] * by;
+#pragma unroll
+    for (int e = 0; e < 4 * MT; e += 8) {
+      if (d + e >= D) break;
+      if (L.splits > 1) store_run<8>(L.part_o, kF32, part * D + d + e, x + e);
+      else store_run<8>(L.a.out, L.a.out_type, head * D + d + e, x + e);
+    }
+  }
+}
+
+template <int DP, int W, int TK>
+hipError_t launch(const AttnLaunch& L, int64_t groups, hipStream_t st) {
+  constexpr size_t bytes = 2 * sizeof(Lds<DP, TK>);
+  static PerDeviceOnce once;
+  const hipError_t e = once_per_device(once, [] {
+    return hipFuncSetAttribute((const void*)k_attn_tile<DP, W, TK>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_attn_tile<DP, W, TK>), dim3((unsigned)groups), dim3(64 * W), bytes, st, L);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_tile(const AttnLaunch& L, int64_t groups, hipStream_t st) {
+  const int D = L.a.c.D;
+  if (D <= 64) return launch<64, 4, 64>(L, groups, st);
+  if (D <= 128) return launch<128, 4, 64>(L, groups, st);
+  return launch<256, 4, 32>(L, groups, st);
+}
+
+}  // namespace ssn

@@ -159,9 +159,10 @@ struct AttnArgs {
   float scale;
   void* ws;                   // attn_workspace() bytes
 };
-int64_t attn_workspace(const AttnArgs& a);   // bytes for the partial results, 0 if none are made
-int64_t attn_workgroups(const AttnArgs& a);
-hipError_t launch_attn_stream(const AttnArgs& a, hipStream_t s);
+int64_t attn_workspace(const AttnArgs& a);              // bytes for the partial results, 0 if none are made
+bool attn_takes_tile(const AttnArgs& a);                // AUTO's choice
+int64_t attn_workgroups(const AttnArgs& a, bool tile);
+hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t s);
 
 // calibration: register-resident matrix ops on random operands (cu_count() * waves_per_simd
 // workgroups of 256 threads; sink holds one float per thread)

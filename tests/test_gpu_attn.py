@@ -1,154 +1,98 @@
 """GPU parity of attention over the 4-bit cache against the float64 oracle, within the bound of its f32 evaluation."""
-import math
-
 import numpy as np
 import pytest
 import torch
 
 import structured_sparse_nvfp4_amd as ssn
+from attn_util import HALF, TYPES, Batch
 from oracle import kv
 
 pytestmark = pytest.mark.gpu
 
-TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
-HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
-
-
-class Batch:
-    """Sequences of the given lengths and numbers of queries in a shuffled cache whose unused slots hold 0xFF (NaN
-    scales) and whose unused table entries are no pages."""
-
-    def __init__(self, lens, qs, Hq, H, D, page, seed=0, x="bf16", spread=1.0, spare=2):
-        rng = np.random.default_rng([seed, D, page])
-        self.lens, self.qs, self.Hq, self.H, self.D, self.page, self.x = list(lens), list(qs), Hq, H, D, page, x
-        used = [-(-n // page) for n in lens]
-        pages = sum(used) + spare
-        ts = (rng.random((2, H)) * 1e-3 + 1e-3).astype(np.float32)
-        self.cache = ssn.kv_nvfp4_empty(pages, page, D, torch.from_numpy(ts[0]).cuda(), torch.from_numpy(ts[1]).cuda())
-        for t in self.cache[:4]:
-            t.fill_(0xFF)
-        order = rng.permutation(pages)
-        self.table = np.full((len(lens), max(used + [0]) + 1), -1, np.int32)
-        self.slots, at = [], 0
-        for b, n in enumerate(lens):
-            self.table[b, :used[b]] = order[at:at + used[b]]
-            at += used[b]
-            j = np.arange(n)
-            self.slots.append(self.table[b, j // page].astype(np.int64) * page + j % page)
-        T = sum(lens)
-        if T:
-            slots = torch.from_numpy(np.concatenate(self.slots)).cuda()
-            K, V = (torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32) * s).cuda() for s in (spread, 1.0))
-            ssn.kv_nvfp4_append(K, V, slots, self.cache)
-        self.Q = torch.from_numpy(rng.standard_normal((sum(qs), Hq, D)).astype(np.float32)).to(TYPES[x]).cuda()
-        self.offsets = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
-
-    def dev(self, a):
-        return torch.from_numpy(np.ascontiguousarray(a)).cuda()
-
-    def call(self, uniform=False, **kw):
-        off = None if uniform else self.dev(self.offsets)
-        kw.setdefault("max_q", max(self.qs))
-        return ssn.attn_kv_nvfp4(kw.pop("Q", self.Q), self.cache, self.dev(self.table), self.dev(np.int32(self.lens)), off, **kw)
-
-    def values(self, b):
-        """Cached keys and values of sequence b in float64."""
-        h = [t.cpu().numpy() for t in self.cache]
-        kc, ks, vc, vs = kv.gather(*h[:4], self.slots[b], self.page)
-        return kv.dequantize_tokens(kc, ks, h[4]), kv.dequantize_tokens(vc, vs, h[5])
-
-    def check(self, out, lse=None, causal=True, window=0, scale=None, Q=None, out_type=None, seqs=None):
-        torch.cuda.synchronize()
-        Q = (self.Q if Q is None else Q).double().cpu().numpy()
-        got = out.double().cpu().numpy()
-        eps = HALF[out_type or self.x]
-        for b in range(len(self.lens)) if seqs is None else seqs:
-            q0, n, S = int(self.offsets[b]), self.qs[b], self.lens[b]
-            k, v = self.values(b)
-            want, wlse, tol, ltol = kv.attention(Q[q0:q0 + n], k, v, self.D ** -0.5 if scale is None else scale,
-                                                 kv.keeps(S, n, causal, window), eps)
-            bad = ~(np.abs(got[q0:q0 + n] - want) <= tol)
-            assert not bad.any(), (b, np.argwhere(bad)[:3].tolist(), int(bad.sum()), got[q0:q0 + n][bad][:3], want[bad][:3], tol[bad][:3])
-            if lse is not None:
-                gl = lse[q0:q0 + n].double().cpu().numpy()
-                none = np.isneginf(wlse)
-                assert np.array_equal(np.isneginf(gl), none)
-                assert np.all(np.abs(gl[~none] - wlse[~none]) <= ltol[~none])
-
+STREAM, TILE = ssn.ALGO_STREAM, ssn.ALGO_MFMA
+both = pytest.mark.parametrize("algo", [STREAM, TILE], ids=["stream", "tile"])
 
 LENS = [1, 2, 15, 16, 17, 31, 32, 33, 47, 64, 65, 127, 129, 200, 255, 256, 257]
 
 
+@both
 @pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
 @pytest.mark.parametrize("Hq,H", [(1, 1), (5, 1), (16, 2), (40, 8), (17, 1)])
-def test_single_tokens(D, Hq, H):
+def test_single_tokens(D, Hq, H, algo):
     B = Batch(LENS, [1] * len(LENS), Hq, H, D, [16, 32, 48, 64, 128][(D // 32 + Hq) % 5])
-    out, lse, algo = B.call(uniform=True, with_lse=True)
-    assert algo == ssn.ALGO_STREAM and out.dtype == torch.bfloat16
+    out, lse, used = B.call(uniform=True, with_lse=True, algo=algo)
+    assert used == algo and out.dtype == torch.bfloat16
     B.check(out, lse)
 
 
+@both
 @pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
 @pytest.mark.parametrize("D", [64, 96, 128, 256])
-def test_types(x, y, D):
+def test_types(x, y, D, algo):
     B = Batch([300, 77, 1], [1, 3, 1], 6, 2, D, 16, x=x)
-    out, lse, _ = B.call(out_dtype=TYPES[y], with_lse=True)
+    out, lse, _ = B.call(algo=algo, out_dtype=TYPES[y], with_lse=True)
     assert out.dtype == TYPES[y]
     B.check(out, lse, out_type=y)
 
 
+@both
 @pytest.mark.parametrize("window", [0, 1, 2, 16, 17, 50, 4096])
 @pytest.mark.parametrize("n", [1, 2, 3, 5, 9, 16, 33])
-def test_several_tokens_and_windows(n, window):
+def test_several_tokens_and_windows(n, window, algo):
     """Up to 33 queries a sequence over one, two and four sets of 16 rows; rows that leave some keys only."""
     lens = [n, n + 1, n + 15, 40 + n, 100, 257]
     B = Batch(lens, [n] * len(lens), 10, 2, 128, 16, seed=n)
-    out, lse, _ = B.call(uniform=True, with_lse=True, window=window)
+    out, lse, _ = B.call(algo=algo, uniform=True, with_lse=True, window=window)
     B.check(out, lse, window=window)
 
 
+@both
 @pytest.mark.parametrize("D", [64, 160, 256])
 @pytest.mark.parametrize("causal", [True, False])
-def test_ragged_batch(D, causal):
+def test_ragged_batch(D, causal, algo):
     B = Batch([70, 0, 1, 130, 33, 290], [70, 3, 1, 7, 33, 1], 8, 4, D, 32, seed=7)
-    out, lse, _ = B.call(with_lse=True, causal=causal)
+    out, lse, _ = B.call(algo=algo, with_lse=True, causal=causal)
     B.check(out, lse, causal=causal)
     assert int(out[70:73].count_nonzero()) == 0 and bool(torch.isneginf(lse[70:73]).all())
 
 
-def test_more_queries_than_keys():
+@both
+def test_more_queries_than_keys(algo):
     B = Batch([3, 20], [9, 20], 4, 1, 128, 16)
-    out, lse, _ = B.call(with_lse=True)
+    out, lse, _ = B.call(algo=algo, with_lse=True)
     B.check(out, lse)
     assert int(out[:6].count_nonzero()) == 0 and bool(torch.isneginf(lse[:6]).all())
 
 
-def test_rows_of_no_sequence_are_left():
+@both
+def test_rows_of_no_sequence_are_left(algo):
     B = Batch([50, 60], [4, 2], 4, 2, 64, 16)
     Q = torch.cat([B.Q[:1], B.Q, B.Q[:3]])
     B.offsets = B.offsets + 1
     out, lse = torch.full((10, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((10, 4), 7.0, device="cuda")
-    o, l, _ = B.call(Q=Q, out=out, lse=lse)
+    o, l, _ = B.call(algo=algo, Q=Q, out=out, lse=lse)
     assert o is out and l is lse
     B.check(out, lse, Q=Q)
     for t in (out, lse):
         assert bool((t[:1] == 7).all()) and bool((t[7:] == 7).all())
     # of a sequence with more than max_q queries the first max_q are computed, as of a sequence of that many
     out.fill_(7.0)
-    B.call(Q=Q, out=out, max_q=2)
+    B.call(algo=algo, Q=Q, out=out, max_q=2)
     assert bool((out[3:5] == 7).all()) and bool((out[1:3] != 7).any())
     B.check(out, Q=Q, seqs=[1])
 
 
-def test_max_kv_bounds_the_lengths():
+@both
+def test_max_kv_bounds_the_lengths(algo):
     B = Batch([100, 40], [1, 1], 4, 1, 128, 16)
-    out, _, _ = B.call(max_kv=64)
+    out, _, _ = B.call(algo=algo, max_kv=64)
     C = Batch([100, 40], [1, 1], 4, 1, 128, 16)
     C.lens, C.slots = [64, 40], [C.slots[0][:64], C.slots[1]]
     C.check(out)
 
 
-def test_pages_that_are_not_there():
+@both
+def test_pages_that_are_not_there(algo):
     """Tokens of a page outside [0, pages) count for no row."""
     B = Batch([200, 90], [2, 1], 4, 2, 128, 32)
     pages = B.cache.k_codes.shape[0]
@@ -157,7 +101,7 @@ def test_pages_that_are_not_there():
     for b, ps in gone.items():
         for i, p in enumerate(ps):
             B.table[b, p] = [-1, pages, 1 << 30, -(1 << 31)][(i + b) % 4]
-    out, lse, _ = B.call(with_lse=True)
+    out, lse, _ = B.call(algo=algo, with_lse=True)
     Q = B.Q.double().cpu().numpy()
     for b in range(2):
         keep = kv.keeps(B.lens[b], B.qs[b], True, 0)
@@ -168,90 +112,99 @@ def test_pages_that_are_not_there():
         got, gl = out[q0:q0 + B.qs[b]].double().cpu().numpy(), lse[q0:q0 + B.qs[b]].double().cpu().numpy()
         assert np.all(np.abs(got - want) <= tol) and np.all(np.abs(gl - wl) <= lt)
     B.table[:] = -1
-    out, lse, _ = B.call(with_lse=True)
+    out, lse, _ = B.call(algo=algo, with_lse=True)
     assert int(out.count_nonzero()) == 0 and bool(torch.isneginf(lse).all())
 
 
+@both
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1e-6, 1.0, 30.0])
-def test_scales(scale):
+def test_scales(scale, algo):
     B = Batch([150, 33], [3, 1], 4, 2, 64, 16, x="f16")
-    out, lse, _ = B.call(scale=scale, with_lse=True)
+    out, lse, _ = B.call(algo=algo, scale=scale, with_lse=True)
     B.check(out, lse, scale=scale)
 
 
+@both
 @pytest.mark.parametrize("size", [1e-38, 1e-20, 1e-4, 300.0, 1e6, 1e30])
-def test_queries_of_any_size(size):
+def test_queries_of_any_size(size, algo):
     """bf16 queries of any magnitude: logits next to nothing, or one key alone."""
     B = Batch([130, 40], [2, 1], 4, 2, 96, 16)
     Q = (B.Q.float() * size).to(torch.bfloat16)
     Q[0, 0, ::3] = 0
     Q[1, 1, :] = 0
     if size < 1e20:
-        out, lse, _ = B.call(Q=Q, with_lse=True)
+        out, lse, _ = B.call(algo=algo, Q=Q, with_lse=True)
         B.check(out, lse, Q=Q)
     else:
-        out, lse, _ = B.call(Q=Q, with_lse=True, scale=1e-30)
+        out, lse, _ = B.call(algo=algo, Q=Q, with_lse=True, scale=1e-30)
         B.check(out, lse, Q=Q, scale=1e-30)
 
 
-def test_a_row_that_is_not_finite_touches_no_other():
+@both
+def test_a_row_that_is_not_finite_touches_no_other(algo):
     B = Batch([130, 40], [2, 1], 8, 2, 128, 16)
-    want, _, _ = B.call()
+    want, _, _ = B.call(algo=algo)
     Q = B.Q.clone()
     Q[0, 1, 5], Q[1, 6, 0], Q[2, 3, 127] = float("nan"), float("inf"), float("-inf")
-    out, _, _ = B.call(Q=Q)
+    out, _, _ = B.call(algo=algo, Q=Q)
     hit = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
     hit[0, 1] = hit[1, 6] = hit[2, 3] = True
     assert torch.equal(out[~hit], want[~hit]) and bool(out[0, 1].isnan().all())
 
 
+@both
 @pytest.mark.parametrize("spread", [0.0, 8.0, 40.0])
-def test_flat_and_sharp_rows(spread):
+def test_flat_and_sharp_rows(spread, algo):
     """Every key alike, and rows where the largest logit grows by hundreds along the sequence."""
     B = Batch([600, 257], [1, 4], 6, 2, 128, 64, spread=spread)
-    out, lse, _ = B.call(with_lse=True)
+    out, lse, _ = B.call(algo=algo, with_lse=True)
     B.check(out, lse)
 
 
-def test_growing_logits():
+@both
+def test_growing_logits(algo):
     """Keys ordered so that the reference is raised in nearly every tile."""
     B = Batch([512], [1], 4, 1, 64, 16)
     K = torch.linspace(0, 2.6, 512, device="cuda")[:, None, None] * torch.ones(512, 1, 64, device="cuda")
     ssn.kv_nvfp4_append(K, torch.randn(512, 1, 64, device="cuda"), B.dev(B.slots[0]), B.cache)
     B.Q = torch.ones_like(B.Q) * torch.tensor([1.0, -1.0, 4.0, -4.0], device="cuda", dtype=B.Q.dtype)[:, None]
-    out, lse, _ = B.call(with_lse=True)
+    out, lse, _ = B.call(algo=algo, with_lse=True)
     B.check(out, lse)
 
 
+@both
 @pytest.mark.parametrize("D,Hq,H,n,window", [(128, 16, 2, 1, 0), (64, 4, 4, 1, 0), (256, 8, 1, 1, 0), (128, 10, 2, 9, 0),
                                              (160, 3, 1, 2, 3000), (128, 8, 1, 1, 700)])
-def test_long_sequences_are_split(D, Hq, H, n, window):
+def test_long_sequences_are_split(D, Hq, H, n, window, algo):
     B = Batch([9001, 4100], [n, n], Hq, H, D, 64)
-    out, lse, _ = B.call(uniform=True, with_lse=True, window=window)
+    out, lse, _ = B.call(algo=algo, uniform=True, with_lse=True, window=window)
     B.check(out, lse, window=window)
-    again, lse2, _ = B.call(uniform=True, with_lse=True, window=window)
+    again, lse2, _ = B.call(algo=algo, uniform=True, with_lse=True, window=window)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
-def test_split_with_short_sequences_among_long():
+@both
+def test_split_with_short_sequences_among_long(algo):
     """Splits that get no keys of a sequence."""
     B = Batch([5000, 1, 0, 40, 700], [1, 1, 1, 1, 1], 8, 1, 128, 16)
-    out, lse, _ = B.call(uniform=True, with_lse=True)
+    out, lse, _ = B.call(algo=algo, uniform=True, with_lse=True)
     B.check(out, lse)
 
 
-def test_strided_queries():
+@both
+def test_strided_queries(algo):
     B = Batch([90, 30], [3, 2], 4, 2, 96, 16)
     wide = torch.zeros(5, 12, 96, dtype=torch.bfloat16, device="cuda")
     wide[:, 3:7] = B.Q
-    want, _, _ = B.call()
-    out, _, _ = B.call(Q=wide[:, 3:7])
+    want, _, _ = B.call(algo=algo)
+    out, _, _ = B.call(algo=algo, Q=wide[:, 3:7])
     assert torch.equal(out, want) and out.is_contiguous()
-    out, _, _ = B.call(Q=B.Q.transpose(0, 1).contiguous().transpose(0, 1))
+    out, _, _ = B.call(algo=algo, Q=B.Q.transpose(0, 1).contiguous().transpose(0, 1))
     assert torch.equal(out, want)
 
 
-def test_offsets_beyond_32_bits():
+@both
+def test_offsets_beyond_32_bits(algo):
     H, D, page = 8, 256, 256
     pages = (1 << 32) // (H * page * D // 2) + 8
     B = Batch([300], [1], 8, H, D, page)
@@ -260,10 +213,10 @@ def test_offsets_beyond_32_bits():
     for i, p in enumerate(B.table[0, :2]):
         for s, d in zip(B.cache[:4], big[:4]):
             d[pages - 1 - i] = s[int(p)]
-    want, _, _ = B.call()
+    want, _, _ = B.call(algo=algo)
     small, B.cache = B.cache, big
     B.table[0, :2] = [pages - 1, pages - 2]
-    out, _, _ = B.call()
+    out, _, _ = B.call(algo=algo)
     assert torch.equal(out, want)
 
 
@@ -358,3 +311,44 @@ def test_a_model_decodes():
             # K and V were read back rounded to f32: half a step more of every logit and value, of which the bound counts many
             assert np.all(np.abs(out[at:at + n].double().cpu().numpy() - want) <= tol)
             at += n
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("Hq,H,lens,qs", [(1, 1, [300, 129, 128, 127], [300, 129, 1, 127]),
+                                          (5, 1, [64, 65, 200], [64, 33, 77]), (16, 2, [150, 40], [60, 40]),
+                                          (6, 6, [131], [131])])
+def test_prompts(D, Hq, H, lens, qs):
+    """Whole prompts and chunks, of one query head to a key head up to eight; rows over several workgroups."""
+    B = Batch(lens, qs, Hq, H, D, [16, 32, 48, 64, 128][(D // 32 + Hq) % 5], x="f16" if D % 64 else "bf16")
+    out, lse, used = B.call(with_lse=True)
+    assert used == (TILE if max(qs) * (Hq // H) > (32 if D > 128 else 64) else STREAM)
+    B.check(out, lse)
+
+
+@pytest.mark.parametrize("window", [1, 31, 33, 64, 100, 129])
+@pytest.mark.parametrize("D,Hq", [(64, 1), (128, 3), (256, 2)])
+def test_prompts_with_a_window(D, Hq, window):
+    B = Batch([333, 70], [333, 20], Hq, 1, D, 16)
+    out, lse, _ = B.call(with_lse=True, window=window)
+    B.check(out, lse, window=window)
+
+
+def test_chunk_after_a_long_context():
+    """Few rows and many keys: the tiles split too."""
+    B = Batch([6000, 2100], [30, 25], 8, 2, 128, 32)
+    out, lse, used = B.call(with_lse=True)
+    assert used == TILE and ssn.lib().attn_kv_nvfp4_workspace_bytes(2, 8, 2, 128, 30, 6000) > 0
+    B.check(out, lse)
+    again, _, _ = B.call()
+    assert torch.equal(out, again)
+
+
+def test_both_ways_agree():
+    """The two kernels differ by the roundings of their sums alone: far less than a step of bf16 of the largest value."""
+    B = Batch([700, 300, 90], [40, 3, 90], 12, 4, 96, 48)
+    a, la, _ = B.call(algo=STREAM, out_dtype=torch.float32, with_lse=True)
+    b, lb, _ = B.call(algo=TILE, out_dtype=torch.float32, with_lse=True)
+    # each is within its bound of the same value: terms of 2^-11, sums of f32
+    B.check(a, la, out_type="f32")
+    B.check(b, lb, out_type="f32")
+    assert float((a - b).abs().max()) <= 2 * 2.0 ** -10 * float(a.abs().max())
