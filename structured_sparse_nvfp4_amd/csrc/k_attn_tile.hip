@@ -13,6 +13,7 @@
 
 #include "attn.hpp"
 #include "device_once.hpp"
+#include "pipeline.hpp"
 
 namespace ssn {
 namespace {
@@ -31,6 +32,35 @@ struct Lds {
   uint8_t v[DP * VS];
   uint32_t there[4];                                         // byte u % 4 of word u / 4: unit u of 16 tokens has a page
 };
+
+// The first token and d of lane l's piece of keys (one token, 32 d) or values (four tokens, eight d), the wave's first
+// token being base: an order in which the rows that 8 and 16 lanes write together lie in different LDS banks.
+template <int DP>
+__device__ __forceinline__ void piece(bool values, int base, int l, int& tok, int& d) {
+  if (values) {
+    if constexpr (DP == 64) {
+      tok = base + 4 * ((l >> 1) & 7);
+      d = 8 * ((l & 1) | (l >> 4) << 1);
+    } else if constexpr (DP == 128) {
+      tok = base + 4 * ((l >> 2) & 3);
+      d = 8 * ((l & 3) | (l >> 4) << 2);
+    } else {                                       // tokens 8 apart, so that the two halves of a 16-byte piece are written together
+      tok = (base & ~15) + (base & 8) / 2 + 8 * ((l >> 3) & 1);
+      d = 8 * ((l & 7) | (l >> 4) << 3);
+    }
+  } else {
+    if constexpr (DP == 64) {
+      tok = base + ((l & 3) | (l & 8) | (l & 16) >> 2 | (l & 32) >> 1);
+      d = 32 * ((l >> 2) & 1);
+    } else if constexpr (DP == 128) {
+      tok = base + ((l & 3) | (l >> 4) << 2);
+      d = 32 * ((l >> 2) & 3);
+    } else {
+      tok = base + ((l & 3) | (l & 32) >> 3);
+      d = 32 * ((l >> 2) & 7);
+    }
+  }
+}
 
 template <int DP, int W, int TK>
 __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
@@ -53,16 +83,19 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
   Work w;
   if (!find_work(L, b, h, rt, R, w)) return;
 
-  // what this thread brings of every tile
+  // What this thread brings of every tile: of each piece the first token and d. A wave's pieces lie in UW units of 16
+  // tokens, so pages are found once a wave, in scalar registers, and a lane's offsets never change.
+  constexpr int TW = 64 * 32 / DP, UW = (TW + 15) / 16;          // tokens and units of a wave
   int tok[IT], dd[IT];
+  uint32_t at[IT], ats[IT];
   bool isv[IT];
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
-    const int p = it * NTH + tid;
-    isv[it] = it * NTH + 64 * wave >= NK;
-    const int q = isv[it] ? p - NK : p;
-    tok[it] = isv[it] ? q / (DP / 8) * 4 : q / (DP / 32);
-    dd[it] = isv[it] ? q % (DP / 8) * 8 : q % (DP / 32) * 32;
+    isv[it] = NK % NTH ? it * NTH + 64 * wave >= NK : it * NTH >= NK;
+    piece<DP>(isv[it], wave * TW % TK, lane, tok[it], dd[it]);
+    // beyond D an offset beyond the resource, which reads 0
+    at[it] = dd[it] < D ? (tok[it] & 15) * (D / 2) + dd[it] / 2 : 0x80000000u;
+    ats[it] = dd[it] >= D ? 0x80000000u : isv[it] ? dd[it] / 16 * c.page + (tok[it] & 15) : (tok[it] & 15) * (D / 16) + dd[it] / 16;
   }
   const int t0 = w.lo / TK, t1 = (w.hi + TK - 1) / TK;
   const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
@@ -70,37 +103,39 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
 
   u32x4 raw[IT];
   uint32_t scl[IT];
-  int pg[IT], place[IT];
+  int pg[UW], place[UW];                             // of the tile to load next
+  bool there[UW];                                    // of the tile loaded last
+  const int first_unit = (wave * TW % TK) >> 4;      // the wave's first unit in a tile, the same for keys and values
   auto find_pages = [&](int t) {
 #pragma unroll
-    for (int it = 0; it < IT; ++it) pg[it] = page_of(L, b, (t * TK + tok[it]) >> 4, place[it]);
+    for (int u = 0; u < UW; ++u) pg[u] = page_of(L, b, t * (TK / 16) + first_unit + u, place[u]);
+  };
+  auto load_unit = [&](int u) {
+    const int64_t head = (int64_t)(there[u] ? pg[u] : 0) * c.heads + h, row = head * c.page + place[u];
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      if (isv[it]) {
+        const auto vc = buf_rsrc(c.v_codes + row * (D / 2)), vs = buf_rsrc(c.v_scales + head * (D / 16) * c.page + place[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[it][i] = __builtin_amdgcn_raw_buffer_load_b32(vc, at[it], i * (D / 2), 0);
+        scl[it] = __builtin_amdgcn_raw_buffer_load_b32(vs, ats[it], 0, 0);
+      } else {
+        const auto kc = buf_rsrc(c.k_codes + row * (D / 2)), ks = buf_rsrc(c.k_scales + row * (D / 16));
+        raw[it] = __builtin_amdgcn_raw_buffer_load_b128(kc, at[it], 0, 0);
+        scl[it] = __builtin_amdgcn_raw_buffer_load_b16(ks, ats[it], 0, 0);
+      }
+    }
   };
   auto load = [&]() {
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const bool ok = is_page(L, pg[it]);
-      const int64_t head = (int64_t)(ok ? pg[it] : 0) * c.heads + h;
-      const int at = place[it] + (tok[it] & 15);
-      const int64_t row = head * c.page + at;
-      raw[it] = u32x4{0, 0, 0, 0};
-      scl[it] = 0;
-      if (dd[it] < D) {
-        if (isv[it]) {
-          const uint8_t* p = c.v_codes + row * (D / 2) + dd[it] / 2;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) raw[it][i] = *(const uint32_t*)(p + i * (D / 2));
-          scl[it] = *(const uint32_t*)(c.v_scales + (head * (D / 16) + dd[it] / 16) * c.page + at);
-        } else {
-          raw[it] = *(const u32x4*)(c.k_codes + row * (D / 2) + dd[it] / 2);
-          scl[it] = *(const uint16_t*)(c.k_scales + row * (D / 16) + dd[it] / 16);
-        }
-      }
-    }
+    for (int u = 0; u < UW; ++u) there[u] = is_page(L, pg[u]);
+    if (UW == 1 || !(tok[0] & 16)) load_unit(0);
+    else load_unit(UW - 1);
   };
   auto stage = [&](Buf& f, int t) {
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const bool ok = is_page(L, pg[it]);
+      const bool ok = UW == 1 || !(tok[it] & 16) ? there[0] : there[UW - 1];
       if (isv[it]) {
         uint32_t s = scl[it];
         // what lies in a slot that no row keeps may be anything: its value's scale becomes 0
@@ -138,6 +173,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
   if (ta < tb) {
     find_pages(ta);
     load();
+    find_pages(ta + 1);
   }
 
   // queries: the lane's row, d = 16 s + 8 half ..
@@ -189,8 +225,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
     Buf& f = lds[(t - ta) & 1];
     stage(f, t);
     if (t + 1 < tb) {
-      find_pages(t + 1);
       load();
+      find_pages(t + 2);
     }
     lds_barrier();
     const int k0 = t * TK;
@@ -206,14 +242,14 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
       }
     }
     constexpr uint32_t all = TK == 64 ? 0x01010101u : 0x0101u;
-    const uint32_t there = __builtin_amdgcn_readfirstlane(f.there[0]) & (TK == 64 ? ~0u : 0xFFFFu);
-    if (k0 < wlo_all || k0 + TK > whi_all || there != all) {
+    const uint32_t units = __builtin_amdgcn_readfirstlane(f.there[0]) & (TK == 64 ? ~0u : 0xFFFFu);
+    if (k0 < wlo_all || k0 + TK > whi_all || units != all) {
 #pragma unroll
       for (int a = 0; a < AT; ++a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int x = 32 * a + 8 * (i / 4) + 4 * half + i % 4;
-          if (!((there >> (8 * (2 * a + i / 8)) & 1) && k0 + x >= lo_r && k0 + x < hi_r)) s[a][i] = -__builtin_inff();
+          if (!((units >> (8 * (2 * a + i / 8)) & 1) && k0 + x >= lo_r && k0 + x < hi_r)) s[a][i] = -__builtin_inff();
         }
     }
     float top = s[0][0];
