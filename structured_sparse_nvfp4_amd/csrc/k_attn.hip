@@ -454,7 +454,7 @@ Shape shape_of(const AttnArgs& a, bool tile) {
   // keys that a workgroup's rows can keep
   const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + s.R + 31) : a.max_kv;
   const int64_t tiles = (keys + 31) / 32;
-  const int resident = tile ? 2 : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 3;
+  const int resident = tile ? (wide == 1 ? 3 : 2) : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 3;
   const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
   s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
   return s;

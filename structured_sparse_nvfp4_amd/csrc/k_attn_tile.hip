@@ -62,8 +62,8 @@ __device__ __forceinline__ void piece(bool values, int base, int l, int& tok, in
   }
 }
 
-template <int DP, int W, int TK>
-__global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
+template <int DP, int W, int TK, int WPS>
+__global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   static_assert(32 * W == kTileRows, "");
   constexpr int R = 32 * W, NTH = 64 * W, KS = DP / 16, MT = DP / 32, AT = TK / 32;
   constexpr int NK = TK * DP / 32, IT = 2 * NK / NTH;        // pieces of 16 bytes of keys, as many of values; a thread's
@@ -139,13 +139,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
       if (isv[it]) {
         uint32_t s = scl[it];
         // what lies in a slot that no row keeps may be anything: its value's scale becomes 0
-        if (!ok || t * TK < w.lo || t * TK + TK > w.hi) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int x = t * TK + tok[it] + i;
-            if (!ok || x < w.lo || x >= w.hi) s &= ~(0xFFu << (8 * i));
-          }
-        }
+        const int x = t * TK + tok[it], lo = min(max(w.lo - x, 0), 4), hi = min(max((ok ? w.hi : 0) - x, 0), 4);
+        s &= (hi == 4 ? ~0u : (1u << (8 * hi)) - 1u) & (lo == 4 ? 0u : ~0u << (8 * lo));
         const f16x2 s01 = e4m3x2_f16<false>(s), s23 = e4m3x2_f16<true>(s);
         uint32_t e01, o01, e23, o23;
         pair_tokens(raw[it][0], raw[it][1], e01, o01);
@@ -244,12 +239,14 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
     constexpr uint32_t all = TK == 64 ? 0x01010101u : 0x0101u;
     const uint32_t units = __builtin_amdgcn_readfirstlane(f.there[0]) & (TK == 64 ? ~0u : 0xFFFFu);
     if (k0 < wlo_all || k0 + TK > whi_all || units != all) {
+      const int lo = lo_r - k0 - 4 * half, hi = hi_r - k0 - 4 * half;
 #pragma unroll
       for (int a = 0; a < AT; ++a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int x = 32 * a + 8 * (i / 4) + 4 * half + i % 4;
-          if (!((units >> (8 * (2 * a + i / 8)) & 1) && k0 + x >= lo_r && k0 + x < hi_r)) s[a][i] = -__builtin_inff();
+          const int x = 32 * a + 8 * (i / 4) + i % 4;
+          const int page = (int)(units << (31 - 8 * (2 * a + i / 8))) >> 31;     // all ones where the unit has one
+          s[a][i] = ((x >= lo) & (x < hi) & page) ? s[a][i] : -__builtin_inff();
         }
     }
     float top = s[0][0];
@@ -310,15 +307,15 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_tile(AttnLaunch L) {
   }
 }
 
-template <int DP, int W, int TK>
+template <int DP, int W, int TK, int WPS>
 hipError_t launch(const AttnLaunch& L, int64_t groups, hipStream_t st) {
   constexpr size_t bytes = 2 * sizeof(Lds<DP, TK>);
   static PerDeviceOnce once;
   const hipError_t e = once_per_device(once, [] {
-    return hipFuncSetAttribute((const void*)k_attn_tile<DP, W, TK>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return hipFuncSetAttribute((const void*)k_attn_tile<DP, W, TK, WPS>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   });
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attn_tile<DP, W, TK>), dim3((unsigned)groups), dim3(64 * W), bytes, st, L);
+  hipLaunchKernelGGL((k_attn_tile<DP, W, TK, WPS>), dim3((unsigned)groups), dim3(64 * W), bytes, st, L);
   return hipGetLastError();
 }
 
@@ -326,9 +323,9 @@ hipError_t launch(const AttnLaunch& L, int64_t groups, hipStream_t st) {
 
 hipError_t launch_attn_tile(const AttnLaunch& L, int64_t groups, hipStream_t st) {
   const int D = L.a.c.D;
-  if (D <= 64) return launch<64, 4, 64>(L, groups, st);
-  if (D <= 128) return launch<128, 4, 64>(L, groups, st);
-  return launch<256, 4, 32>(L, groups, st);
+  if (D <= 64) return launch<64, 4, 64, 2>(L, groups, st);
+  if (D <= 128) return launch<128, 4, 32, 3>(L, groups, st);
+  return launch<256, 4, 32, 2>(L, groups, st);
 }
 
 }  // namespace ssn
