@@ -99,9 +99,11 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2
   constexpr int R = 16 * NT, KS = DP / 32, MV = DP / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kb = lane >> 4;
-  const int split = blockIdx.x % L.splits, item = blockIdx.x / L.splits;
-  const int rt = item % L.row_tiles, bh = item / L.row_tiles;
-  const int h = bh % L.a.c.heads, b = bh / L.a.c.heads;
+  // Workgroups 8 apart share an L2: there the row sets of one part of the keys follow each other.
+  const int x = blockIdx.x & 7, y = blockIdx.x >> 3, rt = y % L.row_tiles, part = y / L.row_tiles * 8 + x;
+  const int split = part % L.splits, bh = part / L.splits;
+  if (bh >= L.a.B * L.a.c.heads) return;
+  const int h = bh % L.a.c.heads, b = bh / L.a.c.heads, item = bh * L.row_tiles + rt;
   const int D = DC ? DC : L.a.c.D;
   Work w;
   if (!find_work(L, b, h, rt, R, w)) return;
@@ -333,11 +335,11 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2
   for (int n = 0; n < NT; ++n) {
     const int r = w.row0 + 16 * n + col;
     if (r >= w.rows) continue;
-    const int64_t part = ((int64_t)item * L.splits + split) * R + 16 * n + col;
+    const int64_t slot = ((int64_t)item * L.splits + split) * R + 16 * n + col;
     const int i0 = r / L.G;
     const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
     if (L.splits > 1) {
-      if (kb == 0) *(f32x2*)(L.part_ml + 2 * part) = f32x2{mc[n], l[n]};
+      if (kb == 0) *(f32x2*)(L.part_ml + 2 * slot) = f32x2{mc[n], l[n]};
       if (!(l[n] != 0.f)) continue;                 // the join skips a part without keys
     } else if (L.a.lse && kb == 0) {
       L.a.lse[head] = l[n] != 0.f ? (mc[n] + log2f(l[n])) * kLn2 : -__builtin_inff();
@@ -350,7 +352,7 @@ __global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2
       float x[MV];
 #pragma unroll
       for (int v = 0; v < MV; ++v) x[v] = o[n][v][i] * f;
-      if (L.splits > 1) store_run<MV>(L.part_o, kF32, part * D + d, x);
+      if (L.splits > 1) store_run<MV>(L.part_o, kF32, slot * D + d, x);
       else store_run<MV>(L.a.out, L.a.out_type, head * D + d, x);
     }
   }
@@ -447,7 +449,7 @@ Shape shape_of(const AttnArgs& a, bool tile) {
   Shape s;
   const int64_t rows = a.max_q * (a.Hq / a.c.heads);
   const int wide = a.c.D > 128 ? 2 : 1;
-  const int nt = (int)std::min<int64_t>((rows + 15) / 16, 4 / wide);
+  const int nt = wide == 2 ? (rows > 16 ? 2 : 1) : rows > 64 ? 3 : rows > 48 ? 2 : (int)((rows + 15) / 16);
   s.R = tile ? kTileRows : 16 * nt;
   s.row_tiles = (int)((rows + s.R - 1) / s.R);
   s.items = a.B * a.c.heads * s.row_tiles;
@@ -466,19 +468,16 @@ int64_t workspace_of(const AttnArgs& a, const Shape& s) {
 
 template <int DP, int DC>
 void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
-  const dim3 grid((unsigned)(s.items * s.splits)), block(64 * kWaves);
+  const dim3 grid((unsigned)((s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles)), block(64 * kWaves);
   if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
   else if (s.R == 32) hipLaunchKernelGGL((k_attn_stream<DP, 2, DC, kWaves>), grid, block, 0, st, L);
-  else if constexpr (DP <= 128) {
-    if (s.R == 48) hipLaunchKernelGGL((k_attn_stream<DP, 3, DC, kWaves>), grid, block, 0, st, L);
-    else hipLaunchKernelGGL((k_attn_stream<DP, 4, DC, kWaves>), grid, block, 0, st, L);
-  }
+  else if constexpr (DP <= 128) hipLaunchKernelGGL((k_attn_stream<DP, 3, DC, kWaves>), grid, block, 0, st, L);
 }
 
 }  // namespace
 
 // The tiles where a sequence has more rows than one workgroup of the stream takes.
-bool attn_takes_tile(const AttnArgs& a) { return a.max_q * (a.Hq / a.c.heads) > (a.c.D > 128 ? 32 : 64); }
+bool attn_takes_tile(const AttnArgs& a) { return a.max_q * (a.Hq / a.c.heads) > (a.c.D > 128 ? 32 : 96); }
 
 int64_t attn_workspace(const AttnArgs& a) {
   return std::max(workspace_of(a, shape_of(a, false)), workspace_of(a, shape_of(a, true)));
@@ -486,7 +485,7 @@ int64_t attn_workspace(const AttnArgs& a) {
 
 int64_t attn_workgroups(const AttnArgs& a, bool tile) {
   const Shape s = shape_of(a, tile);
-  return s.items * s.splits;
+  return (s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles;
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {
