@@ -95,7 +95,7 @@ __device__ __forceinline__ void load_half(Tile<DP>& t, int a, const AttnLaunch& 
 }
 
 template <int DP, int NT, int DC, int W>
-__global__ __launch_bounds__(64 * W, NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2) void k_attn_stream(AttnLaunch L) {
+__global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2) void k_attn_stream(AttnLaunch L) {
   constexpr int R = 16 * NT, KS = DP / 32, MV = DP / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kb = lane >> 4;
@@ -437,14 +437,15 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
 constexpr int kWaves = 4;
 
 struct Shape {
-  int R, row_tiles, splits;
+  int R, row_tiles, splits, waves;
   int64_t items;
 };
 
 // STREAM. Rows of a workgroup: the fewest sets of 16 that hold a sequence's rows, four at most (two beyond a width of
 // 128). Splits: as many workgroups as the card holds at once, each wave with kMinTiles tiles at least.
 // MFMA: 128 rows; splits likewise, of eight tiles at least.
-constexpr int kMinTiles = 4;
+// Few short sequences: one workgroup of 16 waves (8 beyond a width of 128) each, and no join.
+constexpr int kMinTiles = 4, kShort = 32;
 Shape shape_of(const AttnArgs& a, bool tile) {
   Shape s;
   const int64_t rows = a.max_q * (a.Hq / a.c.heads);
@@ -458,7 +459,12 @@ Shape shape_of(const AttnArgs& a, bool tile) {
   const int64_t tiles = (keys + 31) / 32;
   const int resident = tile ? (wide == 1 ? 3 : 2) : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 3;
   const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
+  s.waves = kWaves;
   s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
+  if (!tile && nt == 1 && s.items < cu_count() && tiles <= kShort) {
+    s.waves = 16 / wide;
+    s.splits = 1;
+  }
   return s;
 }
 
@@ -468,8 +474,10 @@ int64_t workspace_of(const AttnArgs& a, const Shape& s) {
 
 template <int DP, int DC>
 void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
-  const dim3 grid((unsigned)((s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles)), block(64 * kWaves);
-  if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
+  const dim3 grid((unsigned)((s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles)), block(64 * s.waves);
+  constexpr int many = DP > 128 ? 8 : 16;
+  if (s.waves == many) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, many>), grid, block, 0, st, L);
+  else if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
   else if (s.R == 32) hipLaunchKernelGGL((k_attn_stream<DP, 2, DC, kWaves>), grid, block, 0, st, L);
   else if constexpr (DP <= 128) hipLaunchKernelGGL((k_attn_stream<DP, 3, DC, kWaves>), grid, block, 0, st, L);
 }
