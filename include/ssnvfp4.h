@@ -531,7 +531,8 @@ int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const
  *   seq_lens   int32 [B]     tokens of each sequence in the cache, the queries' own among them; at most max_kv count
  *   q_offsets  int32 [B + 1] sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1; NULL: Tq / B each
  *   max_q, max_kv            no sequence has more queries (those beyond are not computed) or tokens; max_kv is at most
- *              max_blocks * page_size and 2^27
+ *              max_blocks * page_size and 2^27. They size the launch.
+ * B <= 65535.
  * Rows of out and lse that belong to no sequence, or lie beyond max_q, are left as they were. Logits, softmax
  * statistics and sums are f32; K_hat and V_hat enter unrounded, a softmax term is rounded to 11 bits (f16) before it
  * multiplies V_hat, and so is Q below 2^-39 of its row's largest magnitude.

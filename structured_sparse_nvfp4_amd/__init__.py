@@ -800,6 +800,8 @@ def _rows(dev, t, dtype, name, shape):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     token, head, one = t.stride()
+    if shape[0] == 0:                              # no rows: whatever strides it has
+        return t.data_ptr(), 0, 0
     if one != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0

@@ -741,8 +741,8 @@ int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const
 namespace {
 
 int check_attn(const char* fn, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_kv) {
-  if (B < 0 || B > (1 << 20) || max_q < 0 || max_kv < 0 || max_kv > kMaxSeq)
-    return fail(SSN_E_SHAPE, "%s: bad sizes (B=%lld, max_q=%lld, max_kv=%lld; B <= 2^20, max_kv <= 2^27)", fn,
+  if (B < 0 || B > 65535 || max_q < 0 || max_kv < 0 || max_kv > kMaxSeq)
+    return fail(SSN_E_SHAPE, "%s: bad sizes (B=%lld, max_q=%lld, max_kv=%lld; B <= 65535, max_kv <= 2^27)", fn,
                 (long long)B, (long long)max_q, (long long)max_kv);
   if (Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq % Hkv || Hq > (1 << 20))
     return fail(SSN_E_RANGE, "%s: Hq=%lld is not a multiple of Hkv=%lld (in [1, 4096])", fn, (long long)Hq, (long long)Hkv);
@@ -806,8 +806,8 @@ int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_toke
     if (workspace_bytes < need)
       return fail(SSN_E_RANGE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)need);
   }
-  if (ssn::attn_workgroups(a, tile) > kMaxGrid)
-    return fail(SSN_E_SHAPE, "%s: B * Hkv * rows need more than 2^23 workgroups", fn);
+  if (ssn::attn_workgroups(a, tile) > kMaxGrid || (!tile && ssn::attn_workgroups(a, tile) / (B * Hkv) > 65535))
+    return fail(SSN_E_SHAPE, "%s: B * Hkv * rows need more than 2^23 workgroups (65535 sets of rows with STREAM)", fn);
   return hip_status(ssn::launch_attn(a, tile, as_stream(stream)), fn);
 }
 

@@ -172,6 +172,33 @@ __device__ __forceinline__ int row_shift(float amax) {
   return 16 - e;
 }
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// the largest magnitude of packed 16-bit values so far, as bits (those of bf16 and of f16 ascend with the magnitude)
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const u32x4& x) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), __builtin_bit_cast(u16x2, x[e] & 0x7FFF7FFFu)));
+  return m;
+}
+__device__ __forceinline__ float max_of(uint32_t m, int type) {
+  const uint32_t b = max(m & 0xFFFFu, m >> 16);
+  return type == kF16 ? f16_of((uint16_t)b) : bf16_of((uint16_t)b);
+}
+
+// N packed pairs of type t times 2^shift, their signs turned by `flip`, as f16
+template <int T, int N>
+__device__ __forceinline__ void scale_rows(u32x4 (&x)[N], int shift, uint32_t flip) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = x[j][e];
+      const float lo = T == kF16 ? f16_of((uint16_t)w) : bf16_lo(w), hi = T == kF16 ? f16_of((uint16_t)(w >> 16)) : bf16_hi(w);
+      x[j][e] = pk_f16(ldexpf(lo, shift), ldexpf(hi, shift)) ^ flip;
+    }
+}
+
 constexpr int kTileRows = 128;                   // of a workgroup of k_attn_tile
 hipError_t launch_attn_tile(const AttnLaunch& L, int64_t groups, hipStream_t s);
 

@@ -21,18 +21,18 @@
 namespace ssn {
 namespace {
 
-// One tile's codes and scales as loaded. (Types as wide as the loads: widened at the load they would be waited for
-// there.)
+// The codes and scales of 16 tokens as loaded. (Types as wide as the loads: widened at the load they would be waited
+// for there.)
 template <int DP>
-struct Tile {
+struct Unit {
   using KeyScales = std::conditional_t<DP == 64, uint8_t, std::conditional_t<DP == 128, uint16_t, u32x2>>;
   using ValueWord = std::conditional_t<DP == 64, uint16_t, uint32_t>;
-  static constexpr int KU = DP >= 128 ? DP / 128 : 1;       // 16-byte pieces of keys a lane and half (DP 64: half of one)
+  static constexpr int KU = DP >= 128 ? DP / 128 : 1;       // 16-byte pieces of keys a lane (DP 64: half of one)
   static constexpr int VW = DP == 256 ? 2 : 1;              // words of values a lane and token (DP 64: half of one)
-  u32x4 k[2][KU];
-  KeyScales ks[2];                                          // the keys' scales: DP / 64 bytes
-  ValueWord v[8][VW];                                       // token 4 a + i
-  uint32_t vs[2];                                           // the values' scales of four tokens
+  u32x4 k[KU];
+  KeyScales ks;                                             // DP / 64 bytes
+  ValueWord v[4][VW];                                       // token 4 (l / 16) + i
+  uint32_t vs;                                              // scales of the four
 };
 
 // lane offsets into a 16-token unit of a page
@@ -57,56 +57,77 @@ __device__ __forceinline__ LaneAt lane_at(int D, int page, int lane) {
   return o;
 }
 
+// Where a unit lies: its first token's row of the codes (and of the keys' scales), and of the values' scales.
+struct Place {
+  int64_t row, vs;
+};
+
 // A wave-uniform base in a buffer resource and a lane offset that never changes: a load costs no vector instruction
 // but itself.
 template <int DP, int DC>
-__device__ __forceinline__ void load_half(Tile<DP>& t, int a, const AttnLaunch& L, int h, int page, int place,
-                                          const LaneAt& o) {
-  const KvCache& c = L.a.c;
+__device__ __forceinline__ void load_keys(Unit<DP>& t, const KvCache& c, const Place& p, const LaneAt& o) {
   const int D = DC ? DC : c.D;
-  const int64_t head = (int64_t)page * c.heads + h, row = head * c.page + place;
-  const auto kc = buf_rsrc(c.k_codes + row * (D / 2)), ks = buf_rsrc(c.k_scales + row * (D / 16));
-  const auto vc = buf_rsrc(c.v_codes + row * (D / 2)), vs = buf_rsrc(c.v_scales + head * (D / 16) * c.page + place);
+  const auto kc = buf_rsrc(c.k_codes + p.row * (D / 2)), ks = buf_rsrc(c.k_scales + p.row * (D / 16));
   if constexpr (DP == 64) {
     const auto k = __builtin_amdgcn_raw_buffer_load_b64(kc, o.k[0], 0, 0);
-    t.k[a][0][0] = k[0]; t.k[a][0][1] = k[1];
+    t.k[0][0] = k[0]; t.k[0][1] = k[1];
+    t.ks = __builtin_amdgcn_raw_buffer_load_b8(ks, o.ks[0], 0, 0);
   } else {
 #pragma unroll
-    for (int u = 0; u < Tile<DP>::KU; ++u) t.k[a][u] = __builtin_amdgcn_raw_buffer_load_b128(kc, o.k[u], 0, 0);
-  }
-  if constexpr (DP == 64) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b8(ks, o.ks[0], 0, 0);
-  else if constexpr (DP == 128) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
-  else if constexpr (DC == 256) t.ks[a][0] = __builtin_amdgcn_raw_buffer_load_b32(ks, o.ks[0], 0, 0);
-  else {
-    t.ks[a][0] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
-    t.ks[a][1] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[1], 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t p = o.v + i * (D / 2);
-    if constexpr (DP == 64) t.v[4 * a + i][0] = __builtin_amdgcn_raw_buffer_load_b16(vc, p, 0, 0);
-    else if constexpr (DP == 128) t.v[4 * a + i][0] = __builtin_amdgcn_raw_buffer_load_b32(vc, p, 0, 0);
+    for (int u = 0; u < Unit<DP>::KU; ++u) t.k[u] = __builtin_amdgcn_raw_buffer_load_b128(kc, o.k[u], 0, 0);
+    if constexpr (DP == 128) t.ks = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
+    else if constexpr (DC == 256) t.ks[0] = __builtin_amdgcn_raw_buffer_load_b32(ks, o.ks[0], 0, 0);
     else {
-      const auto v = __builtin_amdgcn_raw_buffer_load_b64(vc, p, 0, 0);
-      t.v[4 * a + i][0] = v[0]; t.v[4 * a + i][1] = v[1];
+      t.ks[0] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[0], 0, 0);
+      t.ks[1] = __builtin_amdgcn_raw_buffer_load_b16(ks, o.ks[1], 0, 0);
     }
   }
-  t.vs[a] = __builtin_amdgcn_raw_buffer_load_b32(vs, o.vs, 0, 0);
 }
 
+template <int DP, int DC>
+__device__ __forceinline__ void load_values(Unit<DP>& t, const KvCache& c, const Place& p, const LaneAt& o) {
+  const int D = DC ? DC : c.D;
+  const auto vc = buf_rsrc(c.v_codes + p.row * (D / 2)), vs = buf_rsrc(c.v_scales + p.vs);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = o.v + i * (D / 2);
+    if constexpr (DP == 64) t.v[i][0] = __builtin_amdgcn_raw_buffer_load_b16(vc, at, 0, 0);
+    else if constexpr (DP == 128) t.v[i][0] = __builtin_amdgcn_raw_buffer_load_b32(vc, at, 0, 0);
+    else {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(vc, at, 0, 0);
+      t.v[i][0] = v[0]; t.v[i][1] = v[1];
+    }
+  }
+  t.vs = __builtin_amdgcn_raw_buffer_load_b32(vs, o.vs, 0, 0);
+}
+
+// f(0) .. f(N - 1) with constants
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<N, I + 1>(f);
+  }
+}
+
+constexpr int TU = 2, TT = 16 * TU;               // units of 16 tokens of a tile, and its tokens
+
 template <int DP, int NT, int DC, int W>
-__global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * DP <= 128 ? 3 : 2) void k_attn_stream(AttnLaunch L) {
+__global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * DP <= 128 ? 4 : 2) void k_attn_stream(AttnLaunch L) {
   constexpr int R = 16 * NT, KS = DP / 32, MV = DP / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kb = lane >> 4;
-  // Workgroups 8 apart share an L2: there the row sets of one part of the keys follow each other.
-  const int x = blockIdx.x & 7, y = blockIdx.x >> 3, rt = y % L.row_tiles, part = y / L.row_tiles * 8 + x;
-  const int split = part % L.splits, bh = part / L.splits;
-  if (bh >= L.a.B * L.a.c.heads) return;
-  const int h = bh % L.a.c.heads, b = bh / L.a.c.heads, item = bh * L.row_tiles + rt;
   const int D = DC ? DC : L.a.c.D;
+  __shared__ float sm[W][R], sl[W][R];
+  __shared__ f32x4 so[W / 2][NT * MV][64];
+  // Heads first, then row sets: with eight heads (or a multiple) the row sets of one part of the keys share an L2.
+  const int h = blockIdx.x, b = blockIdx.z, split = L.row_tiles == 1 ? blockIdx.y : blockIdx.y / L.row_tiles;
+  const int rt = blockIdx.y - split * L.row_tiles;
   Work w;
   if (!find_work(L, b, h, rt, R, w)) return;
+  const int t0 = w.lo / TT, t1 = (w.hi + TT - 1) / TT;
+  const int per = L.splits == 1 ? t1 - t0 : (max(t1 - t0, 0) + L.splits - 1) / L.splits;
+  const int ta = t0 + split * per, tb = min(t1, ta + per);
 
   // queries: lane's row col of every 16, d = (DP / 4) kb + 8 j ..
   f16x8 q[NT][KS];
@@ -126,57 +147,56 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     }
   }
 
-  // this workgroup's tiles of 32 keys
-  const int t0 = w.lo >> 5, t1 = (w.hi + 31) >> 5;
-  const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
-  const int ta = t0 + split * per, tb = min(t1, ta + per);
   const LaneAt at = lane_at<DP>(D, L.a.c.page, lane);
   struct Pages {
-    int p[2], place[2];
+    int p[TU], place[TU];
   };
   // The pages of tile t, or of the last one: every load is made, so that the waits can count them.
   auto pages_of = [&](int t) {
     Pages p;
 #pragma unroll
-    for (int a = 0; a < 2; ++a) p.p[a] = page_of(L, b, 2 * min(t, tb - 1) + a, p.place[a]);
+    for (int a = 0; a < TU; ++a) p.p[a] = page_of(L, b, TU * min(t, tb - 1) + a, p.place[a]);
     return p;
   };
-  auto load = [&](Tile<DP>& t, const Pages& p) {
+  auto place_of = [&](const Pages& p, Place (&to)[TU], bool (&there)[TU]) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a) load_half<DP, DC>(t, a, L, h, is_page(L, p.p[a]) ? p.p[a] : 0, p.place[a], at);
+    for (int a = 0; a < TU; ++a) {
+      there[a] = is_page(L, p.p[a]);
+      const int64_t head = (int64_t)(there[a] ? p.p[a] : 0) * L.a.c.heads + h;
+      to[a].row = head * L.a.c.page + p.place[a];
+      to[a].vs = head * (D / 16) * L.a.c.page + p.place[a];
+    }
   };
-  Tile<DP> A, B;
-  Pages pa, pb;
+  Unit<DP> un[TU];
+  Pages pg;
+  Place pl[TU];
+  bool there[TU], there_next[TU];
   int t = ta + wave;
-  const bool any = t < tb;
-  if (any) {
-    pa = pages_of(t);
-    pb = pages_of(t + W);
-    load(A, pa);
+  if (t < tb) {
+    pg = pages_of(t);
+    place_of(pg, pl, there);
+    pg = pages_of(t + W);
+    each<TU>([&](auto u) { load_keys<DP, DC>(un[u], L.a.c, pl[u], at); });
+    each<TU>([&](auto u) { load_values<DP, DC>(un[u], L.a.c, pl[u], at); });
   }
+  const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool row = w.row0 + 16 * n + col < w.rows;
-    float amax = 0.f;
+    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
       if (!row || (!DC && DP / 4 * kb + 8 * j >= D)) raw[n][j] = u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(float16_of((uint16_t)(raw[n][j][e / 2] >> (16 * (e & 1))), L.a.q_type)));
+      m = max_bits(m, raw[n][j]);
     }
+    float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    const float sign = sc < 0.f ? -1.f : 1.f;
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], sh, flip);
+    else scale_rows<kF16>(raw[n], sh, flip);
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      u32x4 x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[e] = pk_f16(sign * ldexpf(float16_of((uint16_t)raw[n][j][e], L.a.q_type), sh),
-                      sign * ldexpf(float16_of((uint16_t)(raw[n][j][e] >> 16), L.a.q_type), sh));
-      q[n][j] = as_f16x8(x);
-    }
+    for (int j = 0; j < KS; ++j) q[n][j] = as_f16x8(raw[n][j]);
     c[n] = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);   // not 0, which -inf would turn into NaN
   }
 
@@ -185,41 +205,44 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
 #pragma unroll
   for (int n = 0; n < NT; ++n) { mc[n] = kUnset; l[n] = 0.f; }
 
-  auto compute = [&](const Tile<DP>& cur, const Pages& pg, int t) {
-    // logits
-    f32x4 s[NT][2];
+  // A tile's keys are replaced by the next tile's as soon as its logits are formed, its values when they are used: what
+  // is loaded has a tile's time to arrive.
+  for (; t < tb; t += W) {
+    f32x4 s[NT][TU];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < TU; ++a) {
       f16x2 ks[2];
       if constexpr (DP == 256) {
-        ks[0] = e4m3x2_f16<false>(cur.ks[a][0]);
-        ks[1] = DC ? e4m3x2_f16<true>(cur.ks[a][0]) : e4m3x2_f16<false>(cur.ks[a][1]);
+        ks[0] = e4m3x2_f16<false>(un[a].ks[0]);
+        ks[1] = DC ? e4m3x2_f16<true>(un[a].ks[0]) : e4m3x2_f16<false>(un[a].ks[1]);
       } else {
-        ks[0] = e4m3x2_f16<false>(cur.ks[a]);
+        ks[0] = e4m3x2_f16<false>(un[a].ks);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const f16x8 k = fp4x8_f16(cur.k[a][j / 4][j % 4], ks[j / 4][(j / 2) & 1]);
+        const f16x8 k = fp4x8_f16(un[a].k[j / 4][j % 4], ks[j / 4][(j / 2) & 1]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][j], s[n][a], 0, 0, 0);
       }
     }
-    uint32_t vs[2] = {cur.vs[0], cur.vs[1]};
-    const bool there[2] = {is_page(L, pg.p[0]), is_page(L, pg.p[1])};
-    const bool whole = 32 * t >= w.lo_all && 32 * t + 32 <= w.hi_all && there[0] && there[1];
+    place_of(pg, pl, there_next);
+    pg = pages_of(t + 2 * W);
+    each<TU>([&](auto u) { load_keys<DP, DC>(un[u], L.a.c, pl[u], at); });
+    bool whole = TT * t >= w.lo_all && TT * t + TT <= w.hi_all;
+#pragma unroll
+    for (int a = 0; a < TU; ++a) whole = whole && there[a];
     if (!whole) {
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int a = 0; a < TU; ++a)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tok = 32 * t + 16 * a + 4 * kb + i;
+          const int tok = TT * t + 16 * a + 4 * kb + i, in = there[a] ? -1 : 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (!(there[a] && tok >= lo_r[n] && tok < hi_r[n])) s[n][a][i] = -__builtin_inff();
+          for (int n = 0; n < NT; ++n) s[n][a][i] = ((tok >= lo_r[n]) & (tok < hi_r[n]) & in) ? s[n][a][i] : -__builtin_inff();
           // what lies in a slot that no row keeps may be anything: its value's scale becomes 0
-          if (!(there[a] && tok >= w.lo && tok < w.hi)) vs[a] &= ~(0xFFu << (8 * i));
+          un[a].vs &= ((tok >= w.lo) & (tok < w.hi) & in) ? ~0u : ~(0xFFu << (8 * i));
         }
     }
     // reference and p
@@ -229,7 +252,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     for (int n = 0; n < NT; ++n) {
       top[n] = s[n][0][0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], s[n][i / 4][i % 4]);
+      for (int i = 1; i < 4 * TU; ++i) top[n] = fmaxf(top[n], s[n][i / 4][i % 4]);
       raise |= top[n] * c[n] - mc[n] > kTop;
     }
     if (__any(raise)) {
@@ -246,58 +269,44 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
         for (int v = 0; v < MV; ++v) o[n][v] *= f;
       }
     }
-    f16x8 p[NT];
+    f16x8 p[NT][TU / 2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float e[8];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = exp2_hw(fmaf(s[n][i / 4][i % 4], c[n], -mc[n]));
-        l[n] += e[i];
+      for (int a = 0; a < TU / 2; ++a) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = exp2_hw(fmaf(s[n][2 * a + i / 4][i % 4], c[n], -mc[n]));
+          l[n] += e[i];
+        }
+        p[n][a] = as_f16x8(u32x4{pk_f16(e[0], e[1]), pk_f16(e[2], e[3]), pk_f16(e[4], e[5]), pk_f16(e[6], e[7])});
       }
-      p[n] = as_f16x8(u32x4{pk_f16(e[0], e[1]), pk_f16(e[2], e[3]), pk_f16(e[4], e[5]), pk_f16(e[6], e[7])});
-    }
-    // values
-    const f16x2 sv[4] = {e4m3x2_f16<false>(vs[0]), e4m3x2_f16<true>(vs[0]), e4m3x2_f16<false>(vs[1]), e4m3x2_f16<true>(vs[1])};
-    uint32_t even[4][Tile<DP>::VW], odd[4][Tile<DP>::VW];
+    // values, 32 tokens at a time
+    each<TU / 2>([&](auto a) {
+      const f16x2 sv[4] = {e4m3x2_f16<false>(un[2 * a].vs), e4m3x2_f16<true>(un[2 * a].vs),
+                           e4m3x2_f16<false>(un[2 * a + 1].vs), e4m3x2_f16<true>(un[2 * a + 1].vs)};
+      uint32_t even[4][Unit<DP>::VW], odd[4][Unit<DP>::VW];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int u = 0; u < Tile<DP>::VW; ++u) pair_tokens(cur.v[2 * x][u], cur.v[2 * x + 1][u], even[x][u], odd[x][u]);
-    auto value = [&](auto mi) {
-      constexpr int m = decltype(mi)::value, u = m / 8, sel = (m % 8) / 2;
-      if constexpr (m < MV) {
+        for (int u = 0; u < Unit<DP>::VW; ++u)
+          pair_tokens(un[2 * a + x / 2].v[2 * (x & 1)][u], un[2 * a + x / 2].v[2 * (x & 1) + 1][u], even[x][u], odd[x][u]);
+      each<MV>([&](auto m) {
+        constexpr int u = m / 8, sel = (m % 8) / 2;
         u32x4 x;
 #pragma unroll
         for (int y = 0; y < 4; ++y) x[y] = fp4x2_f16<sel>(m & 1 ? odd[y][u] : even[y][u], sv[y]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_f16x8(x), p[n], o[n][m], 0, 0, 0);
-      }
-    };
-#define SSN_VALUE(i) value(std::integral_constant<int, i>());
-    SSN_VALUE(0) SSN_VALUE(1) SSN_VALUE(2) SSN_VALUE(3) SSN_VALUE(4) SSN_VALUE(5) SSN_VALUE(6) SSN_VALUE(7)
-    SSN_VALUE(8) SSN_VALUE(9) SSN_VALUE(10) SSN_VALUE(11) SSN_VALUE(12) SSN_VALUE(13) SSN_VALUE(14) SSN_VALUE(15)
-#undef SSN_VALUE
-  };
-
-  // two tiles a turn, each loaded while the other is worked on; page numbers a tile further ahead
-  while (t < tb) {
-    Pages pn = pages_of(t + 2 * W);
-    load(B, pb);
-    compute(A, pa, t);
-    t += W;
-    if (t >= tb) break;
-    pa = pn;
-    pn = pages_of(t + 2 * W);
-    load(A, pa);
-    compute(B, pb, t);
-    t += W;
-    pb = pn;
+        for (int n = 0; n < NT; ++n) o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_f16x8(x), p[n][a], o[n][m], 0, 0, 0);
+      });
+    });
+    each<TU>([&](auto u) { load_values<DP, DC>(un[u], L.a.c, pl[u], at); });
+#pragma unroll
+    for (int a = 0; a < TU; ++a) there[a] = there_next[a];
   }
 
   // the waves' results brought to one reference and added up, the upper half into the lower until one is left
-  __shared__ float sm[W][R], sl[W][R];
-  __shared__ f32x4 so[W / 2][NT * MV][64];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] += __shfl_xor(l[n], 16, 64);
@@ -335,11 +344,11 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   for (int n = 0; n < NT; ++n) {
     const int r = w.row0 + 16 * n + col;
     if (r >= w.rows) continue;
-    const int64_t slot = ((int64_t)item * L.splits + split) * R + 16 * n + col;
+    const int64_t row = ((((int64_t)b * L.a.c.heads + h) * L.row_tiles + rt) * L.splits + split) * R + 16 * n + col;
     const int i0 = r / L.G;
     const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
     if (L.splits > 1) {
-      if (kb == 0) *(f32x2*)(L.part_ml + 2 * slot) = f32x2{mc[n], l[n]};
+      if (kb == 0) *(f32x2*)(L.part_ml + 2 * row) = f32x2{mc[n], l[n]};
       if (!(l[n] != 0.f)) continue;                 // the join skips a part without keys
     } else if (L.a.lse && kb == 0) {
       L.a.lse[head] = l[n] != 0.f ? (mc[n] + log2f(l[n])) * kLn2 : -__builtin_inff();
@@ -352,7 +361,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
       float x[MV];
 #pragma unroll
       for (int v = 0; v < MV; ++v) x[v] = o[n][v][i] * f;
-      if (L.splits > 1) store_run<MV>(L.part_o, kF32, slot * D + d, x);
+      if (L.splits > 1) store_run<MV>(L.part_o, kF32, row * D + d, x);
       else store_run<MV>(L.a.out, L.a.out_type, head * D + d, x);
     }
   }
@@ -371,15 +380,15 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   int64_t q0, n;
   const bool live = b < L.a.B && find_queries(L, b, q0, n) && r < n * L.G;
   __shared__ f32x4 acc[RW][TR];
-  const int rt = live ? r / R : 0;
-  const int64_t at0 = live ? ((int64_t)bh * L.row_tiles + rt) * L.splits * R + (r - rt * R) : 0;
+  const int rt = live ? r / R : 0, splits = live ? L.splits : 0;
+  const int64_t at0 = live ? ((int64_t)bh * L.row_tiles + rt) * splits * R + (r - rt * R) : 0;
   // m and l of part s in lane s % 64
   float m[NS], l[NS], top = kUnset, sum = 0.f;
-  const int ns = (L.splits + 63) / 64;
+  const int ns = (splits + 63) / 64;
 #pragma unroll
   for (int x = 0; x < NS; ++x) {
     m[x] = kUnset; l[x] = 0.f;
-    if (x < ns && 64 * x + lane < L.splits) {
+    if (x < ns && 64 * x + lane < splits) {
       const f32x2 ml = *(const f32x2*)(L.part_ml + 2 * (at0 + (int64_t)(64 * x + lane) * R));
       m[x] = ml[0]; l[x] = ml[1];
     }
@@ -389,7 +398,7 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   const float* src = L.part_o + at0 * D + d;
   f32x4 first[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) first[u] = g < groups && g + u * groups < L.splits ? *(const f32x4*)(src + (int64_t)(g + u * groups) * R * D) : o;
+  for (int u = 0; u < U; ++u) first[u] = g < groups && g + u * groups < splits ? *(const f32x4*)(src + (int64_t)(g + u * groups) * R * D) : o;
 #pragma unroll
   for (int x = 0; x < NS; ++x) top = fmaxf(top, m[x]);
 #pragma unroll
@@ -408,17 +417,17 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
       if (x < ns) { const float y = __shfl(m[x], s & 63, 64); if (s / 64 == x) f = y; }
     return f;
   };
-  for (int s0 = 0; s0 < L.splits; s0 += U * groups) {
+  for (int s0 = 0; s0 < splits; s0 += U * groups) {
     f32x4 next[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int s = s0 + g + (u + U) * groups;
-      next[u] = g < groups && s < L.splits ? *(const f32x4*)(src + (int64_t)s * R * D) : f32x4{0.f, 0.f, 0.f, 0.f};
+      next[u] = g < groups && s < splits ? *(const f32x4*)(src + (int64_t)s * R * D) : f32x4{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float f = factor(min(s0 + g + u * groups, L.splits - 1));
-      if (f != 0.f && s0 + g + u * groups < L.splits) o += first[u] * f;
+      const float f = factor(min(s0 + g + u * groups, splits - 1));
+      if (f != 0.f && s0 + g + u * groups < splits) o += first[u] * f;
       first[u] = next[u];
     }
   }
@@ -457,7 +466,7 @@ Shape shape_of(const AttnArgs& a, bool tile) {
   // keys that a workgroup's rows can keep
   const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_kv, (int64_t)a.window + s.R + 31) : a.max_kv;
   const int64_t tiles = (keys + 31) / 32;
-  const int resident = tile ? (wide == 1 ? 3 : 2) : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 3;
+  const int resident = tile ? (wide == 1 ? 3 : 2) : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 4;
   const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
   s.waves = kWaves;
   s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
@@ -474,7 +483,7 @@ int64_t workspace_of(const AttnArgs& a, const Shape& s) {
 
 template <int DP, int DC>
 void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
-  const dim3 grid((unsigned)((s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles)), block(64 * s.waves);
+  const dim3 grid((unsigned)L.a.c.heads, (unsigned)(s.row_tiles * s.splits), (unsigned)L.a.B), block(64 * s.waves);
   constexpr int many = DP > 128 ? 8 : 16;
   if (s.waves == many) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, many>), grid, block, 0, st, L);
   else if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
@@ -493,7 +502,7 @@ int64_t attn_workspace(const AttnArgs& a) {
 
 int64_t attn_workgroups(const AttnArgs& a, bool tile) {
   const Shape s = shape_of(a, tile);
-  return (s.items / s.row_tiles * s.splits + 7) / 8 * 8 * s.row_tiles;
+  return s.items * s.splits;
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {

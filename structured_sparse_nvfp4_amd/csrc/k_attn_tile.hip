@@ -182,27 +182,22 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     const int rr = min(r, w.rows - 1), i = rr / L.G;
     const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
     u32x4 x[KS];
-    float amax = 0.f;
+    uint32_t m = 0;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d = 16 * s + 8 * half;
       x[s] = *(const u32x4*)(src + (d < D ? d : 0));
       if (r >= w.rows || d >= D) x[s] = u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(float16_of((uint16_t)(x[s][e / 2] >> (16 * (e & 1))), L.a.q_type)));
+      m = max_bits(m, x[s]);
     }
+    float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    const float sign = sc < 0.f ? -1.f : 1.f;
+    const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(x, sh, flip);
+    else scale_rows<kF16>(x, sh, flip);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        y[e] = pk_f16(sign * ldexpf(float16_of((uint16_t)x[s][e], L.a.q_type), sh),
-                      sign * ldexpf(float16_of((uint16_t)(x[s][e] >> 16), L.a.q_type), sh));
-      q[s] = as_f16x8(y);
-    }
+    for (int s = 0; s < KS; ++s) q[s] = as_f16x8(x[s]);
     cf = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);    // not 0, which -inf would turn into NaN
   }
   // keys that some row, and that every row, of this wave keeps (rows behind the last aside)

@@ -191,6 +191,29 @@ def test_split_with_short_sequences_among_long(algo):
     B.check(out, lse)
 
 
+@pytest.mark.parametrize("B", [2, 63, 64, 65, 200, 256, 257])
+@pytest.mark.parametrize("window", [0, 2500])
+def test_batches_with_one_long_sequence(B, window):
+    """Parts of equal work: some sequences end and others begin inside one, and some have no keys or no query."""
+    rng = np.random.default_rng(B + window)
+    lens = [int(n) for n in rng.integers(0, 70, B)]
+    lens[B // 2], lens[0] = 4321, 0
+    qs = [int(q) for q in rng.integers(0, 2, B)]
+    qs[B // 2] = qs[0] = 1
+    X = Batch(lens, qs, 4, 1, 64, 16, seed=B)
+    out, lse, _ = X.call(with_lse=True, window=window, max_q=1)
+    X.check(out, lse, window=window)
+
+
+def test_batches_without_a_query():
+    X = Batch([3000, 2500], [0, 0], 8, 2, 128, 16)
+    out, _, _ = X.call(max_q=1, max_kv=3000)
+    assert out.shape == (0, 8, 128)
+    X = Batch([3000, 2500, 10], [0, 1, 0], 8, 2, 128, 16)
+    out, lse, _ = X.call(max_q=1, with_lse=True)
+    X.check(out, lse)
+
+
 @both
 def test_strided_queries(algo):
     B = Batch([90, 30], [3, 2], 4, 2, 96, 16)

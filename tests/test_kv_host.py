@@ -71,7 +71,9 @@ CASES = [(n, b, c, s) for n, b in (("kv_nvfp4_append", APPEND), ("kv_nvfp4_read"
     ("attn_kv_nvfp4", ATTN, dict(blocks=1 << 13, max_kv=1 << 17), ssn.SSN_E_NULL),
     ("attn_kv_nvfp4", ATTN, dict(blocks=1 << 13, max_kv=1 << 17, ws=P, wsb=64), ssn.SSN_E_RANGE),
     ("attn_kv_nvfp4", ATTN, dict(blocks=1 << 13, max_kv=1 << 17, ws=at(0x1004), wsb=1 << 30), ssn.SSN_E_ALIGN),
-    ("attn_kv_nvfp4", ATTN, dict(B=1 << 20, Hkv=4096, Hq=4096, Tq=1 << 20, max_q=1), ssn.SSN_E_SHAPE),
+    ("attn_kv_nvfp4", ATTN, dict(B=65535, Hkv=4096, Hq=4096, Tq=65535, max_q=1), ssn.SSN_E_SHAPE),
+    ("attn_kv_nvfp4", ATTN, dict(B=65536, Tq=65536, max_q=1), ssn.SSN_E_SHAPE),
+    ("attn_kv_nvfp4", ATTN, dict(B=1, Hkv=1, Hq=1, Tq=1 << 24, max_q=1 << 24, algo=ssn.ALGO_STREAM), ssn.SSN_E_SHAPE),
 ]
 
 
@@ -98,7 +100,7 @@ def test_workspace_sizes():
     assert f(0, 4, 2, 64, 1, 100) == 0 and f(2, 4, 2, 64, 0, 100) == 0 and f(2, 4, 2, 64, 1, 0) == 0
     assert f(2, 4, 2, 64, 1, 64) == 0
     assert f(1, 64, 8, 128, 1, 131072) > 0
-    assert f(1 << 20, 4096, 4096, 256, 1 << 20, 1 << 27) == 0
+    assert f(65535, 4096, 4096, 256, 1 << 20, 1 << 27) == 0 and f(65536, 4, 2, 64, 1, 100) == -1
 
 
 def test_the_binding_refuses():
