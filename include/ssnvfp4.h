@@ -480,7 +480,8 @@ int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, in
  * A cache of keys and values in NVFP4, and attention over it: what a decode step reads beside its weights.
  *
  * The cache is pages of page_size tokens (a multiple of 16 in [16, 2^20]); inside a page a head's tokens are one
- * run. Hkv key heads in [1, 4096], width D a multiple of 32 in [32, 256], pages in [1, 2^31 - 1024]:
+ * run. Hkv key heads in [1, 4096], width D a multiple of 32 in [32, 256], pages in [1, 2^31 - 1024], at
+ * most 2^40 tokens:
  *   k_codes   u8 [pages, Hkv, page_size, D/2]    two E2M1 nibbles a byte, the even d in the low one
  *   k_scales  u8 [pages, Hkv, page_size, D/16]   E4M3, one per 16 values along D
  *   v_codes   u8 [pages, Hkv, page_size, D/2]

@@ -680,6 +680,8 @@ int check_cache(const char* fn, const ssn::KvCache& c, int64_t pages, int64_t pa
     return fail(SSN_E_SHAPE, "%s: page_size=%lld is not a multiple of 16 in [16, 2^20]", fn, (long long)page_size);
   if (heads < 1 || heads > 4096) return fail(SSN_E_RANGE, "%s: Hkv=%lld outside [1, 4096]", fn, (long long)heads);
   if (pages < 1 || pages > kMaxRows) return fail(SSN_E_SHAPE, "%s: pages=%lld outside [1, 2^31 - 1024]", fn, (long long)pages);
+  if (pages * page_size > ((int64_t)1 << 40))
+    return fail(SSN_E_SHAPE, "%s: pages=%lld of page_size=%lld are more than 2^40 tokens", fn, (long long)pages, (long long)page_size);
   uint8_t *const k_codes = c.k_codes, *const k_scales = c.k_scales, *const v_codes = c.v_codes, *const v_scales = c.v_scales;
   const float *const k_tensor_scale = c.k_ts, *const v_tensor_scale = c.v_ts;
   REQUIRE_PTR(k_codes); REQUIRE_PTR(k_scales); REQUIRE_PTR(v_codes); REQUIRE_PTR(v_scales);

@@ -87,6 +87,33 @@ def test_append_is_the_quantiser_of_weights():
 
 
 @pytest.mark.parametrize("x_type", ["f32", "bf16", "f16"])
+def test_append_decides_as_the_quantiser_everywhere(x_type):
+    """Three million values of every size against nvfp4_quantize (exact by its own tests): quotients next to the middle
+    of two codes or scales, scales that are powers of two, tiny and huge ones, values to the end of f32."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    T, D, page = 2048, 256, 64
+    scales = [1e-3, 2.0 ** -9, 1.0, 0.3, 1.1754944e-38, 1e-42, 1e-31, 3e38, 7e29, 2.0 ** -126, 6e-5]
+    H = len(scales)
+    ts = torch.tensor(scales, device="cuda")
+    x = torch.randn((T, H, D), generator=g, device="cuda") * (ts[:, None] * 6).clamp(max=1e30)
+    x *= torch.exp2(torch.randint(-14, 12, (T, H, D // 16, 1), generator=g, device="cuda").float()).expand(T, H, D // 16, 16).reshape(T, H, D)
+    # an eighth of the blocks: multiples of s_h / 8, that is ties and their neighbours in f32
+    n = torch.randint(-4000, 4000, (T // 8, H, D), generator=g, device="cuda").float()
+    tie = n * (ts[:, None] / 8)
+    x[: T // 8] = torch.where(torch.rand(tie.shape, generator=g, device="cuda") < 0.5, tie, torch.nextafter(tie, torch.zeros_like(tie)))
+    x = x.clamp(-3e38, 3e38).nan_to_num().to(TYPES[x_type])
+    if x_type == "f16":
+        x = x.clamp(-65504, 65504)
+    cache = ssn.kv_nvfp4_empty(T // page, page, D, ts, ts)
+    ssn.kv_nvfp4_append(x, -x, torch.arange(T, device="cuda"), cache)
+    for h in range(H):
+        for X, codes, S in ((x, cache.k_codes, cache.k_scales), (-x, cache.v_codes, cache.v_scales.transpose(2, 3))):
+            c, s, _ = ssn.nvfp4_quantize(X[:, h].float().contiguous(), tensor_scale_in=ts[h:h + 1].contiguous())
+            assert torch.equal(S[:, h].reshape(T, D // 16), s), scales[h]
+            assert torch.equal(codes[:, h].reshape(T, D // 2), c), scales[h]
+
+
+@pytest.mark.parametrize("x_type", ["f32", "bf16", "f16"])
 def test_parts_of_one_projection(x_type):
     """K and V as slices of [T, (Hq + 2 Hkv) D], an expanded head, and a token stride of two tokens."""
     torch.manual_seed(1)

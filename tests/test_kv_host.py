@@ -33,6 +33,7 @@ SHARED = [
     (dict(D=48), ssn.SSN_E_SHAPE), (dict(D=0), ssn.SSN_E_SHAPE), (dict(D=288), ssn.SSN_E_SHAPE), (dict(D=-32), ssn.SSN_E_SHAPE),
     (dict(page=8), ssn.SSN_E_SHAPE), (dict(page=24), ssn.SSN_E_SHAPE), (dict(page=-16), ssn.SSN_E_SHAPE),
     (dict(page=(1 << 20) + 16), ssn.SSN_E_SHAPE), (dict(pages=0), ssn.SSN_E_SHAPE), (dict(pages=1 << 31), ssn.SSN_E_SHAPE),
+    (dict(pages=1 << 25, page=1 << 16), ssn.SSN_E_SHAPE),
     (dict(Hkv=0), ssn.SSN_E_RANGE), (dict(Hkv=4097), ssn.SSN_E_RANGE), (dict(kc=N0), ssn.SSN_E_NULL),
     (dict(ks=N0), ssn.SSN_E_NULL), (dict(vc=N0), ssn.SSN_E_NULL), (dict(vs=N0), ssn.SSN_E_NULL), (dict(kt=N0), ssn.SSN_E_NULL),
     (dict(vt=N0), ssn.SSN_E_NULL), (dict(kc=at(0x1008)), ssn.SSN_E_ALIGN), (dict(vs=at(0x1004)), ssn.SSN_E_ALIGN),
