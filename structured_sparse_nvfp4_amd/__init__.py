@@ -780,10 +780,23 @@ def kv_nvfp4_empty(pages, page_size, D, k_tensor_scale, v_tensor_scale):
 
 
 def _kv(dev, cache):
-    """(addresses of the cache's tensors, (pages, page_size, Hkv, D))."""
+    """(addresses of the cache's tensors, (pages, page_size, Hkv, D)). One combined check, 1.8 us; six by _on take 2.1
+    of a call's 8."""
     kc, ks, vc, vs, kt, vt = cache
     P, H, S, Dh = _size(kc, 4, "k_codes")
     D, u8, f32 = 2 * Dh, torch.uint8, torch.float32
+    try:
+        at = dev.index if dev.type == "cuda" else -1
+        if (kc.dtype is u8 and ks.dtype is u8 and vc.dtype is u8 and vs.dtype is u8 and kt.dtype is f32 and vt.dtype is f32
+                and kc.get_device() == at and ks.get_device() == at and vc.get_device() == at and vs.get_device() == at
+                and kt.get_device() == at and vt.get_device() == at
+                and vc.shape == kc.shape and ks.shape == (P, H, S, D // 16) and vs.shape == (P, H, D // 16, S)
+                and kt.shape == (H,) and vt.shape == (H,)
+                and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()
+                and kt.is_contiguous() and vt.is_contiguous()):
+            return (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr()), (P, S, H, D)
+    except AttributeError:
+        pass                                       # something that is no tensor: named below
     return (_on(dev, kc, u8, "k_codes", (P, H, S, Dh)), _on(dev, ks, u8, "k_scales", (P, H, S, D // 16)),
             _on(dev, vc, u8, "v_codes", (P, H, S, Dh)), _on(dev, vs, u8, "v_scales", (P, H, D // 16, S)),
             _on(dev, kt, f32, "k_tensor_scale", (H,)), _on(dev, vt, f32, "v_tensor_scale", (H,))), (P, S, H, D)

@@ -165,12 +165,6 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
       }
     }
   };
-  if (ta < tb) {
-    find_pages(ta);
-    load();
-    find_pages(ta + 1);
-  }
-
   // queries: the lane's row, d = 16 s + 8 half ..
   const int r = w.row0 + 32 * wave + col;
   int lo_r, hi_r;
@@ -200,6 +194,12 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     for (int s = 0; s < KS; ++s) q[s] = as_f16x8(x[s]);
     cf = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);    // not 0, which -inf would turn into NaN
   }
+  if (ta < tb) {
+    find_pages(ta);
+    load();
+    find_pages(ta + 1);
+  }
+
   // keys that some row, and that every row, of this wave keeps (rows behind the last aside)
   const int first = w.row0 + 32 * wave, last = min(first + 31, w.rows - 1);
   int wlo, whi, wlo_all, whi_all;

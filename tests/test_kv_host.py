@@ -113,7 +113,7 @@ def test_the_binding_refuses():
                      (dict(cache=c._replace(k_tensor_scale=torch.ones(3))), ValueError), (dict(K=K[:, :1]), ValueError),
                      (dict(V=K.half()), TypeError), (dict(K=K.double(), V=K.double()), TypeError), (dict(slots=slots.int()), TypeError),
                      (dict(slots=slots[:2]), ValueError), (dict(K=K.transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
-                     (dict(K="K"), TypeError), (dict(cache=c._replace(k_codes=c.k_codes[:, :, ::2])), ValueError)):
+                     (dict(K="K"), TypeError), (dict(cache=c._replace(v_codes=None)), TypeError), (dict(cache=c._replace(k_codes=c.k_codes[:, :, ::2])), ValueError)):
         with pytest.raises(err):
             ssn.kv_nvfp4_append(**{**dict(K=K, V=K, slots=slots, cache=c), **bad})
     with pytest.raises(ValueError, match="device tensors"):
