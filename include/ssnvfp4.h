@@ -498,8 +498,8 @@ int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, in
  * bit; a magnitude beyond 6 * 448 * s_h saturates; a head whose s_h is 0 or less holds zeros). K and V are
  * [T, Hkv, D] with the D values of a head contiguous and rows of any 16-byte aligned strides (in elements), as the
  * parts of one projection are. A token with a negative slot is not written, one beyond the cache is not written and
- * counted in bad_slots (device int64 [1], nullable, set by the call). No two tokens may own one slot. T <= 2^26.
- * K and V must be finite (a NaN is written as 0, an infinity as the largest value).
+ * counted in bad_slots (device int64 [1], nullable, set by the call). No two tokens may own one slot (it would hold a
+ * mixture of them). T <= 2^26. K and V must be finite (a NaN is written as 0, an infinity as the largest value).
  * Errors: NULL, SHAPE, ALIGN, DTYPE, RANGE (Hkv), HIP.
  * ------------------------------------------------------------------------------------------- */
 int kv_nvfp4_append(const void* K, const void* V, int dtype, int64_t T, int64_t k_token_stride, int64_t k_head_stride,
@@ -530,14 +530,16 @@ int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const
  *   block_table int32 [B, max_blocks]  page of every page_size tokens of a sequence; a value outside [0, pages) is a page
  *              that is not there, whose tokens no row keeps
  *   seq_lens   int32 [B]     tokens of each sequence in the cache, the queries' own among them; at most max_kv count
- *   q_offsets  int32 [B + 1] sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1; NULL: Tq / B each
- *   max_q, max_kv            no sequence has more queries (those beyond are not computed) or tokens; max_kv is at most
- *              max_blocks * page_size and 2^27. They size the launch.
+ *   q_offsets  int32 [B + 1] sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1; NULL: Tq / B each.
+ *              No two sequences own one query
+ *   max_q, max_kv            no sequence has more queries (those beyond are not computed) or tokens (a longer one is taken
+ *              as one of max_kv); max_kv is at most max_blocks * page_size and 2^27. They size the launch.
  * B <= 65535.
  * Rows of out and lse that belong to no sequence, or lie beyond max_q, are left as they were. Logits, softmax
  * statistics and sums are f32; K_hat and V_hat enter unrounded, a softmax term is rounded to 11 bits (f16) before it
  * multiplies V_hat, and so is Q below 2^-39 of its row's largest magnitude.
- * algo: AUTO or STREAM, reported in *algo_used (host, nullable). workspace: attn_kv_nvfp4_workspace_bytes() bytes of
+ * algo: AUTO, STREAM (few rows: Hq / Hkv times the queries of a sequence) or MFMA (many; both take any), reported in
+ * *algo_used (host, nullable). workspace: attn_kv_nvfp4_workspace_bytes() bytes of
  * device memory (16-byte aligned; NULL if 0), for f32 results of parts of long sequences; nothing in it needs
  * clearing, and calls that may overlap need one each.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, ALGO, RANGE, HIP.

@@ -3,6 +3,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "../../include/ssnvfp4.h"
 #include "device_once.hpp"
 #include "launch.hpp"
@@ -780,7 +782,7 @@ int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_toke
                   {(uint8_t*)k_codes, (uint8_t*)k_scales, (uint8_t*)v_codes, (uint8_t*)v_scales, k_tensor_scale,
                    v_tensor_scale, pages, page_size, Hkv, D},
                   block_table, seq_lens, q_offsets, Tq, B, max_blocks, max_q, max_kv, Hq, q_dtype, out_dtype, causal != 0,
-                  (int)window, scale, workspace};
+                  (int)std::min(window, max_kv), scale, workspace};   // a window of max_kv keeps every key
   if ((st = check_attn(fn, B, Hq, Hkv, D, max_q, max_kv))) return st;
   if ((st = check_cache(fn, a.c, pages, page_size, Hkv, D))) return st;
   if ((st = check_type(fn, q_dtype, "q_dtype", false)) || (st = check_side_types(fn, q_dtype, out_dtype, "out_dtype"))) return st;

@@ -47,37 +47,37 @@ struct AttnLaunch {
 struct Work {
   int b, h, row0, rows;        // rows: of the sequence and key head in all
   int64_t q0;                  // the sequence's first query
-  int first_pos;               // position of query 0 (negative: more queries than keys)
+  int first_pos;               // position of its query 0 (negative: more queries than keys)
   int len;
   int lo, hi;                  // keys that some row of the workgroup keeps
   int lo_all, hi_all;          // keys that all its rows keep
 };
 
-// the first query and the number of queries of sequence b
-__device__ __forceinline__ bool find_queries(const AttnLaunch& L, int b, int64_t& q0, int64_t& n) {
+// the first query of sequence b, its queries in all, and how many of them are computed
+__device__ __forceinline__ bool find_queries(const AttnLaunch& L, int b, int64_t& q0, int64_t& all, int64_t& n) {
   const AttnArgs& a = L.a;
   if (a.q_offsets) {
     q0 = a.q_offsets[b];
-    n = (int64_t)a.q_offsets[b + 1] - q0;
-    if (q0 < 0 || q0 > a.Tq) return false;
+    all = min((int64_t)a.q_offsets[b + 1], a.Tq) - q0;
+    if (q0 < 0) return false;
   } else {
-    n = L.each;
-    q0 = b * n;
+    all = L.each;
+    q0 = b * all;
   }
-  n = min(min(n, a.max_q), a.Tq - q0);
+  n = min(all, a.max_q);
   return n > 0;
 }
 
 // rows rt R .. rt R + R - 1 of sequence b
 __device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int rt, int R, Work& w) {
   const AttnArgs& a = L.a;
-  int64_t q0, n;
-  if (!find_queries(L, b, q0, n)) return false;
+  int64_t q0, all, n;
+  if (!find_queries(L, b, q0, all, n)) return false;
   const int64_t rows = n * L.G, row0 = (int64_t)rt * R;
   if (row0 >= rows) return false;
   w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = q0;
   w.len = (int)min((int64_t)max(a.lens[b], 0), a.max_kv);
-  w.first_pos = w.len - (int)n;
+  w.first_pos = w.len - (int)all;
   const int i0 = (int)row0 / L.G, i1 = ((int)min(row0 + R, rows) - 1) / L.G;
   w.lo = w.lo_all = 0;
   w.hi = w.hi_all = w.len;

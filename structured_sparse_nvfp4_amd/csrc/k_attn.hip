@@ -377,8 +377,8 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   const int64_t id = (int64_t)blockIdx.x * RW + rw;
   const int bh = (int)(id / max_rows), r = (int)(id - (int64_t)bh * max_rows);
   const int h = bh % L.a.c.heads, b = bh / L.a.c.heads, D = L.a.c.D;
-  int64_t q0, n;
-  const bool live = b < L.a.B && find_queries(L, b, q0, n) && r < n * L.G;
+  int64_t q0, all, n;
+  const bool live = b < L.a.B && find_queries(L, b, q0, all, n) && r < n * L.G;
   __shared__ f32x4 acc[RW][TR];
   const int rt = live ? r / R : 0, splits = live ? L.splits : 0;
   const int64_t at0 = live ? ((int64_t)bh * L.row_tiles + rt) * splits * R + (r - rt * R) : 0;

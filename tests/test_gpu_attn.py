@@ -75,11 +75,29 @@ def test_rows_of_no_sequence_are_left(algo):
     B.check(out, lse, Q=Q)
     for t in (out, lse):
         assert bool((t[:1] == 7).all()) and bool((t[7:] == 7).all())
-    # of a sequence with more than max_q queries the first max_q are computed, as of a sequence of that many
+    # of a sequence with more than max_q queries the first max_q are computed
     out.fill_(7.0)
     B.call(algo=algo, Q=Q, out=out, max_q=2)
     assert bool((out[3:5] == 7).all()) and bool((out[1:3] != 7).any())
     B.check(out, Q=Q, seqs=[1])
+
+
+@both
+@pytest.mark.parametrize("window", [0, 17])
+def test_max_q_keeps_the_positions(window, algo):
+    """The first max_q queries of a sequence keep the keys that they keep without the bound."""
+    B = Batch([50, 300, 3], [40, 2, 9], 4, 2, 64, 16)
+    out, lse = torch.full_like(B.Q, 7.0), torch.full((51, 4), 7.0, device="cuda")
+    B.call(algo=algo, window=window, max_q=5, out=out, lse=lse)
+    Q, got, gl = (t.double().cpu().numpy() for t in (B.Q, out, lse))
+    for b, (S, n) in enumerate(zip(B.lens, B.qs)):
+        q0, k = int(B.offsets[b]), min(n, 5)
+        want, wl, tol, lt = kv.attention(Q[q0:q0 + k], *B.values(b), 64 ** -0.5, kv.keeps(S, n, True, window)[:k], HALF["bf16"])
+        assert np.all(np.abs(got[q0:q0 + k] - want) <= tol)
+        none = np.isneginf(wl)
+        assert np.array_equal(np.isneginf(gl[q0:q0 + k]), none)
+        assert np.all(np.abs(gl[q0:q0 + k][~none] - wl[~none]) <= lt[~none])
+        assert np.all(got[q0 + k:q0 + n] == 7) and np.all(gl[q0 + k:q0 + n] == 7)
 
 
 @both
