@@ -840,11 +840,18 @@ def kv_nvfp4_read(slots, cache, out_dtype=torch.bfloat16, K=None, V=None, prepar
     (T,) = _size(slots, 1, "slots")
     dev = slots.device
     at, (P, S, H, D) = _kv(dev, cache)
-    K = K if K is not None else slots.new_empty((T, H, D), dtype=out_dtype)
-    V = V if V is not None else slots.new_empty((T, H, D), dtype=K.dtype)
+    if K is None:
+        K = slots.new_empty((T, H, D), dtype=out_dtype)
+        k = K.data_ptr()
+    else:
+        k = _on(dev, K, K.dtype, "K", (T, H, D))
     dt = _code(K.dtype, "K", _ANY)
-    cargs = (_on(dev, slots, torch.int64, "slots", (T,)), T, *at, P, S, H, D, _on(dev, K, K.dtype, "K", (T, H, D)),
-             _on(dev, V, K.dtype, "V", (T, H, D)), dt)
+    if V is None:
+        V = torch.empty_like(K)
+        v = V.data_ptr()
+    else:
+        v = _on(dev, V, K.dtype, "V", (T, H, D))
+    cargs = (_on(dev, slots, torch.int64, "slots", (T,)), T, *at, P, S, H, D, k, v, dt)
     return _run_on(dev, "kv_nvfp4_read", cargs, prepare, (slots, cache), (K, V))
 
 
@@ -871,6 +878,9 @@ def attn_kv_nvfp4(Q, cache, block_table, seq_lens, q_offsets=None, max_q=None, m
         scale = D ** -0.5
     if out is None:
         out = Q.new_empty((Tq, Hq, D), dtype=out_dtype)
+        o = out.data_ptr()
+    else:
+        o = _on(dev, out, out.dtype, "out", (Tq, Hq, D))
     odt = _code(out.dtype, "out", (torch.float32, Q.dtype))
     if lse is None and with_lse:
         lse = Q.new_empty((Tq, Hq), dtype=torch.float32)
@@ -882,17 +892,19 @@ def attn_kv_nvfp4(Q, cache, block_table, seq_lens, q_offsets=None, max_q=None, m
         nws = L.attn_kv_nvfp4_workspace_bytes(B, Hq, H, D, max_q, max_kv)
     if nws < 0:
         _check(SSN_E_SHAPE)
-    if workspace is None and nws:
+    if workspace is not None:
+        ws, nws = _on(dev, workspace, torch.uint8, "workspace", workspace.shape), workspace.numel()
+    elif nws:
         workspace = Q.new_empty(nws, dtype=torch.uint8)
-    elif workspace is not None:
-        _on(dev, workspace, torch.uint8, "workspace", workspace.shape)
+        ws = workspace.data_ptr()
+    else:
+        ws = None
     used = ctypes.c_int(-1)
     cargs = (q, qdt, Tq, Hq, qt, qh, *at, P, S, H, D, _on(dev, block_table, torch.int32, "block_table", (B, blocks)), B,
              blocks, _on(dev, seq_lens, torch.int32, "seq_lens", (B,)),
              None if q_offsets is None else _on(dev, q_offsets, torch.int32, "q_offsets", (B + 1,)), max_q, max_kv, scale,
-             causal, window, _on(dev, out, out.dtype, "out", (Tq, Hq, D)), odt,
-             None if lse is None else _on(dev, lse, torch.float32, "lse", (Tq, Hq)), algo, ctypes.byref(used),
-             None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+             causal, window, o, odt, None if lse is None else _on(dev, lse, torch.float32, "lse", (Tq, Hq)), algo,
+             ctypes.byref(used), ws, nws)
     res = _run_on(dev, "attn_kv_nvfp4", cargs, prepare,
                   (Q, cache, block_table, seq_lens, q_offsets, workspace, used), (out, lse))
     return (res[0], (out, lse, used)) if prepare else (out, lse, used.value)

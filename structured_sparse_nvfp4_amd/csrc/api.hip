@@ -672,7 +672,7 @@ int moe_unpermute_backward(const void* dout, int out_dtype, int64_t T, int k, in
 namespace {
 
 constexpr int64_t kMaxKvTokens = (int64_t)1 << 26;    // of one append or read: their grids
-constexpr int64_t kMaxSeq = (int64_t)1 << 27;         // of one sequence: 32-bit token numbers, page_div
+constexpr int64_t kMaxSeq = (int64_t)1 << 27;         // of one sequence: 32-bit token numbers
 constexpr int64_t kMaxGrid = (int64_t)1 << 23;        // workgroups of 512 threads at most
 
 int check_cache(const char* fn, const ssn::KvCache& c, int64_t pages, int64_t page_size, int64_t heads, int64_t D) {

@@ -26,17 +26,21 @@ constexpr float kShift = 7.f, kTop = 15.f;
 constexpr float kUnset = -3e38f;                 // m of a row that has met no key
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-// tokens to (page, place): n / d for n < 2^23, d < 2^17 by a multiplication
-struct PageDiv {
-  uint64_t m;
-  uint32_t d;
+// n / d for n < 2^31 by a multiplication: m = ceil(2^(31 + s) / d) with 2^s >= d, so m d - 2^(31 + s) < d <= 2^s and m < 2^32
+struct Divisor {
+  uint32_t m, d;
+  int shift;
 };
-inline PageDiv page_div(uint32_t d) { return {((1ull << 40) + d - 1) / d, d}; }
-__device__ __forceinline__ uint32_t div_by(PageDiv p, uint32_t n) { return (uint32_t)((n * p.m) >> 40); }
+inline Divisor divisor(uint32_t d) {
+  int s = 0;
+  while (((uint64_t)1 << s) < d) ++s;
+  return {(uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), d, 31 + s};
+}
+__device__ __forceinline__ int div_by(const Divisor& p, int n) { return (int)(((uint64_t)(uint32_t)n * p.m) >> p.shift); }
 
 struct AttnLaunch {
   AttnArgs a;
-  PageDiv pd;                  // by the 16-token units of a page
+  Divisor pd, gd, td, sd;      // by the 16-token units of a page, G, row_tiles and splits
   int G, row_tiles, splits;
   int64_t each;                // queries of a sequence without q_offsets
   float* part_o;               // [item][split][R][D]
@@ -78,7 +82,7 @@ __device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int
   w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = q0;
   w.len = (int)min((int64_t)max(a.lens[b], 0), a.max_kv);
   w.first_pos = w.len - (int)all;
-  const int i0 = (int)row0 / L.G, i1 = ((int)min(row0 + R, rows) - 1) / L.G;
+  const int i0 = div_by(L.gd, (int)row0), i1 = div_by(L.gd, (int)min(row0 + R, rows) - 1);
   w.lo = w.lo_all = 0;
   w.hi = w.hi_all = w.len;
   if (a.causal) {
@@ -96,7 +100,7 @@ __device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int
 __device__ __forceinline__ void row_keys(const AttnLaunch& L, const Work& w, int r, int& lo, int& hi) {
   lo = 0; hi = w.len;
   if (L.a.causal) {
-    hi = w.first_pos + r / L.G + 1;
+    hi = w.first_pos + div_by(L.gd, r) + 1;
     if (L.a.window > 0) lo = hi - L.a.window;
   }
   if (r >= w.rows) hi = 0;
@@ -105,8 +109,8 @@ __device__ __forceinline__ void row_keys(const AttnLaunch& L, const Work& w, int
 // The table's entry for 16-token unit u of sequence b, and the unit's first token in its page. A unit behind the last
 // token may be asked for: the table's last entry stands in, and its tokens are masked by the caller.
 __device__ __forceinline__ int page_of(const AttnLaunch& L, int b, int u, int& place) {
-  const uint32_t i = div_by(L.pd, (uint32_t)u);
-  place = (u - (int)(i * L.pd.d)) * 16;
+  const int i = div_by(L.pd, u);
+  place = (u - i * (int)L.pd.d) * 16;
   return L.a.table[(int64_t)b * L.a.max_blocks + min((int64_t)i, L.a.max_blocks - 1)];
 }
 __device__ __forceinline__ bool is_page(const AttnLaunch& L, int p) { return p >= 0 && p < L.a.c.pages; }
@@ -164,12 +168,13 @@ __device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Exponent shift that brings a row's largest magnitude into [2^15, 2^16); 0 for a row of zeros or not finite.
+// Exponent shift that brings a row's largest magnitude into [2^15, 2^16), or as near as 2^127 does (from below
+// 2^-112: its logits are nothing then); 0 for a row of zeros or not finite.
 __device__ __forceinline__ int row_shift(float amax) {
   if (!(amax > 0.f) || !(amax < __builtin_inff())) return 0;
   int e;
   (void)frexpf(amax, &e);                          // amax = f 2^e, f in [1/2, 1)
-  return 16 - e;
+  return min(16 - e, 127);
 }
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -186,16 +191,16 @@ __device__ __forceinline__ float max_of(uint32_t m, int type) {
   return type == kF16 ? f16_of((uint16_t)b) : bf16_of((uint16_t)b);
 }
 
-// N packed pairs of type t times 2^shift, their signs turned by `flip`, as f16
+// N packed pairs of type T times a power of two or its negative, as f16
 template <int T, int N>
-__device__ __forceinline__ void scale_rows(u32x4 (&x)[N], int shift, uint32_t flip) {
+__device__ __forceinline__ void scale_rows(u32x4 (&x)[N], float by) {
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = x[j][e];
       const float lo = T == kF16 ? f16_of((uint16_t)w) : bf16_lo(w), hi = T == kF16 ? f16_of((uint16_t)(w >> 16)) : bf16_hi(w);
-      x[j][e] = pk_f16(ldexpf(lo, shift), ldexpf(hi, shift)) ^ flip;
+      x[j][e] = pk_f16(lo * by, hi * by);
     }
 }
 

@@ -118,15 +118,16 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kb = lane >> 4;
   const int D = DC ? DC : L.a.c.D;
-  __shared__ float sm[W][R], sl[W][R];
-  __shared__ f32x4 so[W / 2][NT * MV][64];
+  constexpr int SLOTS = NT == 3 ? W / 2 : W;
+  __shared__ f32x2 sml[SLOTS][R];
+  __shared__ __attribute__((aligned(16))) float so[SLOTS][R][DP + 4];
   // Heads first, then row sets: with eight heads (or a multiple) the row sets of one part of the keys share an L2.
-  const int h = blockIdx.x, b = blockIdx.z, split = L.row_tiles == 1 ? blockIdx.y : blockIdx.y / L.row_tiles;
+  const int h = blockIdx.x, b = blockIdx.z, split = div_by(L.td, blockIdx.y);
   const int rt = blockIdx.y - split * L.row_tiles;
   Work w;
   if (!find_work(L, b, h, rt, R, w)) return;
   const int t0 = w.lo / TT, t1 = (w.hi + TT - 1) / TT;
-  const int per = L.splits == 1 ? t1 - t0 : (max(t1 - t0, 0) + L.splits - 1) / L.splits;
+  const int per = div_by(L.sd, max(t1 - t0, 0) + L.splits - 1);
   const int ta = t0 + split * per, tb = min(t1, ta + per);
 
   // queries: lane's row col of every 16, d = (DP / 4) kb + 8 j ..
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   u32x4 raw[NT][KS];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = w.row0 + 16 * n + col, rr = min(r, w.rows - 1), i = rr / L.G;
+    const int r = w.row0 + 16 * n + col, rr = min(r, w.rows - 1), i = div_by(L.gd, rr);
     row_keys(L, w, r, lo_r[n], hi_r[n]);
     const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
 #pragma unroll
@@ -179,7 +180,6 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     each<TU>([&](auto u) { load_keys<DP, DC>(un[u], L.a.c, pl[u], at); });
     each<TU>([&](auto u) { load_values<DP, DC>(un[u], L.a.c, pl[u], at); });
   }
-  const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const bool row = w.row0 + 16 * n + col < w.rows;
@@ -193,8 +193,9 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], sh, flip);
-    else scale_rows<kF16>(raw[n], sh, flip);
+    const float by = ldexpf(sc < 0.f ? -1.f : 1.f, sh);
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], by);
+    else scale_rows<kF16>(raw[n], by);
 #pragma unroll
     for (int j = 0; j < KS; ++j) q[n][j] = as_f16x8(raw[n][j]);
     c[n] = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);   // not 0, which -inf would turn into NaN
@@ -306,63 +307,77 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     for (int a = 0; a < TU; ++a) there[a] = there_next[a];
   }
 
-  // the waves' results brought to one reference and added up, the upper half into the lower until one is left
+  // The waves' results meet in LDS, rows of D padded so that 16 lanes' pieces lie in different banks; then each thread
+  // adds up four d of a row over the waves, brought to their common reference. Where all of them would leave LDS for
+  // one workgroup a CU only (NT 3), the upper half of the waves goes into the lower first.
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] += __shfl_xor(l[n], 16, 64);
     l[n] += __shfl_xor(l[n], 32, 64);
-    if (kb == 0) { sm[wave][16 * n + col] = mc[n]; sl[wave][16 * n + col] = l[n]; }
+  }
+  auto put = [&](int to) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (kb == 0) sml[to][16 * n + col] = f32x2{mc[n], l[n]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < MV; v += 4)
+          *(f32x4*)&so[to][16 * n + col][MV * (4 * kb + i) + v] = f32x4{o[n][v][i], o[n][v + 1][i], o[n][v + 2][i], o[n][v + 3][i]};
+    }
+  };
+  if constexpr (SLOTS < W) {
+    if (wave >= SLOTS) put(wave - SLOTS);
+    __syncthreads();
+    if (wave < SLOTS) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const f32x2 ml = sml[wave][16 * n + col];
+        const float m = fmaxf(mc[n], ml[0]), f = exp2_hw(mc[n] - m), g = exp2_hw(ml[0] - m);
+        mc[n] = m;
+        l[n] = l[n] * f + ml[1] * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int v = 0; v < MV; v += 4) {
+            const f32x4 x = *(const f32x4*)&so[wave][16 * n + col][MV * (4 * kb + i) + v];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][v + e][i] = o[n][v + e][i] * f + x[e] * g;
+          }
+      }
+      put(wave);
+    }
+  } else {
+    put(wave);
   }
   __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  const int D4 = D / 4;
+  for (int e = threadIdx.x; e < R * D4; e += 64 * W) {
+    const int row = e / D4, d = 4 * (e - row * D4), r = w.row0 + row;
+    if (r >= w.rows) break;
     float m = kUnset, sum = 0.f;
+    f32x2 ml[SLOTS];
 #pragma unroll
-    for (int x = 0; x < W; ++x) m = fmaxf(m, sm[x][16 * n + col]);
+    for (int x = 0; x < SLOTS; ++x) { ml[x] = sml[x][row]; m = fmaxf(m, ml[x][0]); }
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int x = 0; x < W; ++x) sum += sl[x][16 * n + col] * exp2_hw(sm[x][16 * n + col] - m);
-    const float f = exp2_hw(mc[n] - m);
-#pragma unroll
-    for (int v = 0; v < MV; ++v) o[n][v] *= f;
-    mc[n] = m; l[n] = sum;
-  }
-#pragma unroll
-  for (int half = W / 2; half > 0; half /= 2) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int x = 0; x < NT * MV; ++x) so[wave - half][x][lane] = o[x / MV][x % MV];
+    for (int x = 0; x < SLOTS; ++x) {
+      const float f = exp2_hw(ml[x][0] - m);
+      sum += ml[x][1] * f;
+      acc += *(const f32x4*)&so[x][row][d] * f;
     }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int x = 0; x < NT * MV; ++x) o[x / MV][x % MV] += so[wave][x][lane];
-    }
-    __syncthreads();
-  }
-  if (wave) return;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = w.row0 + 16 * n + col;
-    if (r >= w.rows) continue;
-    const int64_t row = ((((int64_t)b * L.a.c.heads + h) * L.row_tiles + rt) * L.splits + split) * R + 16 * n + col;
-    const int i0 = r / L.G;
-    const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
+    const bool any = sum != 0.f;
     if (L.splits > 1) {
-      if (kb == 0) *(f32x2*)(L.part_ml + 2 * row) = f32x2{mc[n], l[n]};
-      if (!(l[n] != 0.f)) continue;                 // the join skips a part without keys
-    } else if (L.a.lse && kb == 0) {
-      L.a.lse[head] = l[n] != 0.f ? (mc[n] + log2f(l[n])) * kLn2 : -__builtin_inff();
-    }
-    const float f = L.splits > 1 ? 1.f : l[n] != 0.f ? L.a.c.v_ts[h] / l[n] : 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = MV * (4 * kb + i);
-      if (!DC && d >= D) continue;
-      float x[MV];
-#pragma unroll
-      for (int v = 0; v < MV; ++v) x[v] = o[n][v][i] * f;
-      if (L.splits > 1) store_run<MV>(L.part_o, kF32, row * D + d, x);
-      else store_run<MV>(L.a.out, L.a.out_type, head * D + d, x);
+      const int64_t part = ((((int64_t)b * L.a.c.heads + h) * L.row_tiles + rt) * L.splits + split) * R + row;
+      if (d == 0) *(f32x2*)(L.part_ml + 2 * part) = f32x2{m, sum};
+      if (any) *(f32x4*)(L.part_o + part * D + d) = acc;      // the join skips a part without keys
+    } else {
+      const int i = div_by(L.gd, r);
+      const int64_t head = (w.q0 + i) * L.a.Hq + h * L.G + (r - i * L.G);
+      const float f = any ? L.a.c.v_ts[h] / sum : 0.f;
+      const float x[4] = {acc[0] * f, acc[1] * f, acc[2] * f, acc[3] * f};
+      store_run<4>(L.a.out, L.a.out_type, head * D + d, x);
+      if (L.a.lse && d == 0) L.a.lse[head] = any ? (m + log2f(sum)) * kLn2 : -__builtin_inff();
     }
   }
 }
@@ -435,7 +450,7 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   __syncthreads();
   if (!live || t >= D4) return;
   for (int x = 1; x < groups; ++x) o += acc[rw][t + x * D4];
-  const int i0 = r / L.G;
+  const int i0 = div_by(L.gd, r);
   const int64_t head = (q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
   const float by = sum != 0.f ? L.a.c.v_ts[h] / sum : 0.f;
   const float x[4] = {o[0] * by, o[1] * by, o[2] * by, o[3] * by};
@@ -443,7 +458,7 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   if (L.a.lse && t == 0) L.a.lse[head] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kMoreWaves = 8;
 
 struct Shape {
   int R, row_tiles, splits, waves;
@@ -468,10 +483,11 @@ Shape shape_of(const AttnArgs& a, bool tile) {
   const int64_t tiles = (keys + 31) / 32;
   const int resident = tile ? (wide == 1 ? 3 : 2) : nt * wide >= 4 ? 1 : nt * wide >= 2 ? 2 : 4;
   const int64_t want = (resident * (int64_t)cu_count() + s.items / 2) / s.items;
+  const int64_t most = std::max<int64_t>(tiles / (kMinTiles * kWaves), std::min<int64_t>(tiles / kWaves, cu_count() / s.items));
   s.waves = kWaves;
-  s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), tiles / (kMinTiles * kWaves)));
+  s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), most));
   if (!tile && nt == 1 && s.items < cu_count() && tiles <= kShort) {
-    s.waves = 16 / wide;
+    s.waves = kMoreWaves;
     s.splits = 1;
   }
   return s;
@@ -484,8 +500,7 @@ int64_t workspace_of(const AttnArgs& a, const Shape& s) {
 template <int DP, int DC>
 void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
   const dim3 grid((unsigned)L.a.c.heads, (unsigned)(s.row_tiles * s.splits), (unsigned)L.a.B), block(64 * s.waves);
-  constexpr int many = DP > 128 ? 8 : 16;
-  if (s.waves == many) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, many>), grid, block, 0, st, L);
+  if (s.waves == kMoreWaves) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kMoreWaves>), grid, block, 0, st, L);
   else if (s.R == 16) hipLaunchKernelGGL((k_attn_stream<DP, 1, DC, kWaves>), grid, block, 0, st, L);
   else if (s.R == 32) hipLaunchKernelGGL((k_attn_stream<DP, 2, DC, kWaves>), grid, block, 0, st, L);
   else if constexpr (DP <= 128) hipLaunchKernelGGL((k_attn_stream<DP, 3, DC, kWaves>), grid, block, 0, st, L);
@@ -509,8 +524,11 @@ hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {
   const Shape s = shape_of(a, tile);
   AttnLaunch L;
   L.a = a;
-  L.pd = page_div((uint32_t)(a.c.page / 16));
+  L.pd = divisor((uint32_t)(a.c.page / 16));
   L.G = a.Hq / a.c.heads;
+  L.gd = divisor((uint32_t)L.G);
+  L.td = divisor((uint32_t)s.row_tiles);
+  L.sd = divisor((uint32_t)s.splits);
   L.each = a.q_offsets ? 0 : a.Tq / a.B;
   L.row_tiles = s.row_tiles;
   L.splits = s.splits;

@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   Buf* const lds = (Buf*)lds_raw;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int split = blockIdx.x % L.splits, id = blockIdx.x / L.splits;
+  const int id = div_by(L.sd, blockIdx.x), split = blockIdx.x - id * L.splits;
   const int nbh = (int)L.a.B * L.a.c.heads;
   // the last rows of all sequences first: with causal they have the most keys
   const int rt = L.row_tiles - 1 - id / nbh, bh = id % nbh;
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     ats[it] = dd[it] >= D ? 0x80000000u : isv[it] ? dd[it] / 16 * c.page + (tok[it] & 15) : (tok[it] & 15) * (D / 16) + dd[it] / 16;
   }
   const int t0 = w.lo / TK, t1 = (w.hi + TK - 1) / TK;
-  const int per = (max(t1 - t0, 0) + L.splits - 1) / L.splits;
+  const int per = div_by(L.sd, max(t1 - t0, 0) + L.splits - 1);
   const int ta = t0 + split * per, tb = min(t1, ta + per);
 
   u32x4 raw[IT];
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   f16x8 q[KS];
   float cf;
   {
-    const int rr = min(r, w.rows - 1), i = rr / L.G;
+    const int rr = min(r, w.rows - 1), i = div_by(L.gd, rr);
     const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
     u32x4 x[KS];
     uint32_t m = 0;
@@ -187,9 +187,9 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
-    if (L.a.q_type == kBF16) scale_rows<kBF16>(x, sh, flip);
-    else scale_rows<kF16>(x, sh, flip);
+    const float by = ldexpf(sc < 0.f ? -1.f : 1.f, sh);
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(x, by);
+    else scale_rows<kF16>(x, by);
 #pragma unroll
     for (int s = 0; s < KS; ++s) q[s] = as_f16x8(x[s]);
     cf = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);    // not 0, which -inf would turn into NaN
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   l += __shfl_xor(l, 32, 64);
   if (r >= w.rows) return;
   const int64_t part = (((int64_t)bh * L.row_tiles + rt) * L.splits + split) * R + 32 * wave + col;
-  const int i0 = r / L.G;
+  const int i0 = div_by(L.gd, r);
   const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
   if (L.splits > 1) {
     if (half == 0) *(f32x2*)(L.part_ml + 2 * part) = f32x2{mc, l};
