@@ -57,31 +57,35 @@ struct Work {
   int lo_all, hi_all;          // keys that all its rows keep
 };
 
-// the first query of sequence b, its queries in all, and how many of them are computed
-__device__ __forceinline__ bool find_queries(const AttnLaunch& L, int b, int64_t& q0, int64_t& all, int64_t& n) {
+// a sequence: its first query, its queries in all, how many of them are computed, its tokens
+struct Seq {
+  int64_t q0, all, n;
+  int len;
+};
+
+__device__ __forceinline__ Seq find_seq(const AttnLaunch& L, int b) {
   const AttnArgs& a = L.a;
+  Seq s;
+  s.len = (int)min((int64_t)max(a.lens[b], 0), a.max_kv);
   if (a.q_offsets) {
-    q0 = a.q_offsets[b];
-    all = min((int64_t)a.q_offsets[b + 1], a.Tq) - q0;
-    if (q0 < 0) return false;
+    s.q0 = a.q_offsets[b];
+    s.all = s.q0 < 0 ? 0 : min((int64_t)a.q_offsets[b + 1], a.Tq) - s.q0;
   } else {
-    all = L.each;
-    q0 = b * all;
+    s.all = L.each;
+    s.q0 = b * s.all;
   }
-  n = min(all, a.max_q);
-  return n > 0;
+  s.n = max(min(s.all, a.max_q), (int64_t)0);
+  return s;
 }
 
 // rows rt R .. rt R + R - 1 of sequence b
-__device__ __forceinline__ bool find_work(const AttnLaunch& L, int b, int h, int rt, int R, Work& w) {
+__device__ __forceinline__ bool find_work(const AttnLaunch& L, const Seq& s, int b, int h, int rt, int R, Work& w) {
   const AttnArgs& a = L.a;
-  int64_t q0, all, n;
-  if (!find_queries(L, b, q0, all, n)) return false;
-  const int64_t rows = n * L.G, row0 = (int64_t)rt * R;
+  const int64_t rows = s.n * L.G, row0 = (int64_t)rt * R;
   if (row0 >= rows) return false;
-  w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = q0;
-  w.len = (int)min((int64_t)max(a.lens[b], 0), a.max_kv);
-  w.first_pos = w.len - (int)all;
+  w.b = b; w.h = h; w.row0 = (int)row0; w.rows = (int)rows; w.q0 = s.q0;
+  w.len = s.len;
+  w.first_pos = w.len - (int)s.all;
   const int i0 = div_by(L.gd, (int)row0), i1 = div_by(L.gd, (int)min(row0 + R, rows) - 1);
   w.lo = w.lo_all = 0;
   w.hi = w.hi_all = w.len;

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   const int h = blockIdx.x, b = blockIdx.z, split = div_by(L.td, blockIdx.y);
   const int rt = blockIdx.y - split * L.row_tiles;
   Work w;
-  if (!find_work(L, b, h, rt, R, w)) return;
+  if (!find_work(L, find_seq(L, b), b, h, rt, R, w)) return;
   const int t0 = w.lo / TT, t1 = (w.hi + TT - 1) / TT;
   const int per = div_by(L.sd, max(t1 - t0, 0) + L.splits - 1);
   const int ta = t0 + split * per, tb = min(t1, ta + per);
@@ -392,8 +392,8 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   const int64_t id = (int64_t)blockIdx.x * RW + rw;
   const int bh = (int)(id / max_rows), r = (int)(id - (int64_t)bh * max_rows);
   const int h = bh % L.a.c.heads, b = bh / L.a.c.heads, D = L.a.c.D;
-  int64_t q0, all, n;
-  const bool live = b < L.a.B && find_queries(L, b, q0, all, n) && r < n * L.G;
+  const Seq seq = find_seq(L, min(b, (int)L.a.B - 1));
+  const bool live = b < L.a.B && r < seq.n * L.G;
   __shared__ f32x4 acc[RW][TR];
   const int rt = live ? r / R : 0, splits = live ? L.splits : 0;
   const int64_t at0 = live ? ((int64_t)bh * L.row_tiles + rt) * splits * R + (r - rt * R) : 0;
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   if (!live || t >= D4) return;
   for (int x = 1; x < groups; ++x) o += acc[rw][t + x * D4];
   const int i0 = div_by(L.gd, r);
-  const int64_t head = (q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
+  const int64_t head = (seq.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
   const float by = sum != 0.f ? L.a.c.v_ts[h] / sum : 0.f;
   const float x[4] = {o[0] * by, o[1] * by, o[2] * by, o[3] * by};
   store_run<4>(L.a.out, L.a.out_type, head * D + d, x);

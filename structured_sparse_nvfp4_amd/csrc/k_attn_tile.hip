@@ -62,6 +62,59 @@ __device__ __forceinline__ void piece(bool values, int base, int l, int& tok, in
   }
 }
 
+// the largest of the lanes' values, none below 0
+__device__ __forceinline__ int wave_max(int x) {
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));   // from one, two, four and eight lanes below
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));   // the last of 16 lanes to the next 16
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));   // the last of 32 to the next 32
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
+// Item t of the pairs (sequence, tile of rows), those with the most keys first: workgroups start in this order, so the
+// long ones do not end alone. Tile j from the end of sequence b lies at level off_b + j of R rows below max_kv keys, so
+// C(p) = sum over b of clamp(p - off_b, 0, tiles_b) items lie above level p; the last of the levels off_b and
+// off_b + tiles_b with C <= t is found, a lane a sequence, and from there each level holds the same sequences. Beyond 64
+// sequences: the last tiles of all, then those before. False behind the last item.
+__device__ __forceinline__ bool find_item(const AttnLaunch& L, int t, int lane, int& b, int& rt, Seq& seq) {
+  const int B = (int)L.a.B;
+  if (B > 64 || B == 1) {
+    const int j = B == 1 ? t : t / B;
+    b = t - j * B;
+    rt = L.row_tiles - 1 - j;
+    seq = find_seq(L, b);
+    return true;
+  }
+  const Seq s = find_seq(L, min(lane, B - 1));
+  int off = 0, tiles = 0;
+  if (lane < B && s.n > 0) {
+    const int64_t keys = max(s.len - s.all + s.n, (int64_t)0);
+    off = (int)min(((L.a.max_kv - keys) * L.G) / kTileRows, (int64_t)1 << 29);
+    tiles = (int)((s.n * L.G + kTileRows - 1) / kTileRows);
+  }
+  int c0 = 0, c1 = 0, total = 0;
+  for (int x = 0; x < B; ++x) {
+    const int o = __builtin_amdgcn_readlane(off, x), n = __builtin_amdgcn_readlane(tiles, x);
+    c0 += min(max(off - o, 0), n);
+    c1 += min(max(off + tiles - o, 0), n);
+    total += n;
+  }
+  if (t >= total) return false;
+  const int p = wave_max(c1 <= t ? off + tiles : c0 <= t ? off : 0), above = wave_max(c1 <= t ? c1 : c0 <= t ? c0 : 0);
+  uint64_t in = __ballot(off <= p && p < off + tiles);
+  const int m = __popcll(in), j = (t - above) / m;       // m > 0: t is above the next of those levels
+  for (int x = t - above - j * m; x > 0; --x) in &= in - 1;
+  b = __ffsll((unsigned long long)in) - 1;
+  rt = __builtin_amdgcn_readlane(tiles, b) - 1 - (p + j - __builtin_amdgcn_readlane(off, b));
+  auto from = [&](int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), b) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)v, b));
+  };
+  seq = {from(s.q0), from(s.all), from(s.n), __builtin_amdgcn_readlane(s.len, b)};
+  return true;
+}
+
 template <int DP, int W, int TK, int WPS>
 __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   static_assert(32 * W == kTileRows, "");
@@ -74,14 +127,12 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int id = div_by(L.sd, blockIdx.x), split = blockIdx.x - id * L.splits;
-  const int nbh = (int)L.a.B * L.a.c.heads;
-  // the last rows of all sequences first: with causal they have the most keys
-  const int rt = L.row_tiles - 1 - id / nbh, bh = id % nbh;
-  const int h = bh % L.a.c.heads, b = bh / L.a.c.heads;
   const KvCache& c = L.a.c;
-  const int D = c.D;
+  const int D = c.D, item = id / c.heads, h = id - item * c.heads;
+  int b, rt;
+  Seq seq;
   Work w;
-  if (!find_work(L, b, h, rt, R, w)) return;
+  if (!find_item(L, item, lane, b, rt, seq) || !find_work(L, seq, b, h, rt, R, w)) return;
 
   // What this thread brings of every tile: of each piece the first token and d. A wave's pieces lie in UW units of 16
   // tokens, so pages are found once a wave, in scalar registers, and a lane's offsets never change.
@@ -277,7 +328,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
 
   l += __shfl_xor(l, 32, 64);
   if (r >= w.rows) return;
-  const int64_t part = (((int64_t)bh * L.row_tiles + rt) * L.splits + split) * R + 32 * wave + col;
+  const int64_t part = ((((int64_t)b * c.heads + h) * L.row_tiles + rt) * L.splits + split) * R + 32 * wave + col;
   const int i0 = div_by(L.gd, r);
   const int64_t head = (w.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
   if (L.splits > 1) {

@@ -57,6 +57,19 @@ def test_ragged_batch(D, causal, algo):
 
 
 @both
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B", [2, 13, 64, 65])
+def test_batches_of_many_lengths(B, causal, algo):
+    """Sequences of 0 to 400 keys and 0 to 25 queries, so that each has none to four tiles of rows."""
+    rng = np.random.default_rng(B)
+    lens, qs = rng.integers(0, 401, B), rng.integers(0, 26, B)
+    lens[0], qs[0], qs[-1] = 0, 3, 0
+    X = Batch(lens.tolist(), qs.tolist(), 16, 1, 64, 16, seed=B)
+    out, lse, _ = X.call(algo=algo, causal=causal, with_lse=True)
+    X.check(out, lse, causal=causal)
+
+
+@both
 def test_more_queries_than_keys(algo):
     B = Batch([3, 20], [9, 20], 4, 1, 128, 16)
     out, lse, _ = B.call(algo=algo, with_lse=True)
