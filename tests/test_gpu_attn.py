@@ -69,6 +69,20 @@ def test_batches_of_many_lengths(B, causal, algo):
     X.check(out, lse, causal=causal)
 
 
+@pytest.mark.parametrize("B,n,window,causal", [(2, 1, 0, True), (9, 1, 0, True), (40, 1, 0, True), (64, 2, 700, True), (3, 60, 0, True),
+                                               (3, 60, 900, True), (5, 7, 0, False), (65, 1, 0, True)])
+def test_long_sequences_among_short_ones(B, n, window, causal):
+    """Two long sequences among short and empty ones, one set of rows and several."""
+    rng = np.random.default_rng([B, n])
+    lens = rng.integers(0, 300, B)
+    lens[B // 2], lens[-1], lens[0] = 9000, 2500, 0 if B > 2 else 1200
+    qs = np.minimum(rng.integers(1, n + 1, B), 60)
+    qs[B // 2] = n
+    X = Batch(lens.tolist(), qs.tolist(), 8, 2, 64, 64, seed=B)
+    out, lse, used = X.call(algo=ssn.ALGO_STREAM, causal=causal, window=window, with_lse=True)
+    X.check(out, lse, causal=causal, window=window)
+
+
 @both
 def test_more_queries_than_keys(algo):
     B = Batch([3, 20], [9, 20], 4, 1, 128, 16)
