@@ -94,20 +94,28 @@ __device__ __forceinline__ bool find_item(const AttnLaunch& L, int t, int lane, 
     off = (int)min(((L.a.max_kv - keys) * L.G) / kTileRows, (int64_t)1 << 29);
     tiles = (int)((s.n * L.G + kTileRows - 1) / kTileRows);
   }
-  int c0 = 0, c1 = 0, total = 0;
-  for (int x = 0; x < B; ++x) {
-    const int o = __builtin_amdgcn_readlane(off, x), n = __builtin_amdgcn_readlane(tiles, x);
-    c0 += min(max(off - o, 0), n);
-    c1 += min(max(off + tiles - o, 0), n);
-    total += n;
+  const int off0 = __builtin_amdgcn_readfirstlane(off), tiles0 = __builtin_amdgcn_readfirstlane(tiles);
+  if (!__any(lane < B && (off != off0 || tiles != tiles0))) {        // all alike
+    const int j = t / B;
+    b = t - j * B;
+    rt = tiles0 - 1 - j;
+    if (rt < 0) return false;
+  } else {
+    int c0 = 0, c1 = 0, total = 0;
+    for (int x = 0; x < B; ++x) {
+      const int o = __builtin_amdgcn_readlane(off, x), n = __builtin_amdgcn_readlane(tiles, x);
+      c0 += min(max(off - o, 0), n);
+      c1 += min(max(off + tiles - o, 0), n);
+      total += n;
+    }
+    if (t >= total) return false;
+    const int p = wave_max(c1 <= t ? off + tiles : c0 <= t ? off : 0), above = wave_max(c1 <= t ? c1 : c0 <= t ? c0 : 0);
+    uint64_t in = __ballot(off <= p && p < off + tiles);
+    const int m = __popcll(in), j = (t - above) / m;     // m > 0: t is above the next of those levels
+    for (int x = t - above - j * m; x > 0; --x) in &= in - 1;
+    b = __ffsll((unsigned long long)in) - 1;
+    rt = __builtin_amdgcn_readlane(tiles, b) - 1 - (p + j - __builtin_amdgcn_readlane(off, b));
   }
-  if (t >= total) return false;
-  const int p = wave_max(c1 <= t ? off + tiles : c0 <= t ? off : 0), above = wave_max(c1 <= t ? c1 : c0 <= t ? c0 : 0);
-  uint64_t in = __ballot(off <= p && p < off + tiles);
-  const int m = __popcll(in), j = (t - above) / m;       // m > 0: t is above the next of those levels
-  for (int x = t - above - j * m; x > 0; --x) in &= in - 1;
-  b = __ffsll((unsigned long long)in) - 1;
-  rt = __builtin_amdgcn_readlane(tiles, b) - 1 - (p + j - __builtin_amdgcn_readlane(off, b));
   auto from = [&](int64_t v) {
     return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), b) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)v, b));
   };
