@@ -1,7 +1,7 @@
 // Attention over the 4-bit cache for few query rows to a key head: a decoded token, a few tokens to verify.
 //
-// Bound by reading the cache. A wave walks tiles of 32 tokens; its loads go straight to registers, a tile ahead of
-// the arithmetic. With v_mfma_f32_16x16x32_f16 and l the lane:
+// A wave walks tiles of 32 tokens; its loads go straight to registers and are replaced in place as they are used, so
+// what is loaded has a tile's time to arrive. With v_mfma_f32_16x16x32_f16 and l the lane:
 //   S^T: A = keys. Lane l holds token l % 16 of a half of the tile and d = (DP / 4) (l / 16) + 0 .. DP / 4 - 1, one run
 //        of its codes; B = Q, in registers for the wave's whole life, in the same order of d. The result has tokens
 //        4 (l / 16) + i of the half for row l % 16.
@@ -10,9 +10,18 @@
 //        interleaves two tokens' nibbles before it converts them, so no transposition through LDS is needed.
 // The row's maximum is a reference that is raised only where a logit passes it by 2^8: one comparison a tile, and the
 // lanes of a row exchange nothing until it happens. Sums of p stay in the lane until the end, in f32.
-// The waves of a workgroup take tiles in turn and add their results up in LDS; long sequences are split over
-// workgroups, whose f32 results k_attn_join adds up.
+// The waves of a workgroup take tiles in turn and meet in LDS; long sequences are split over workgroups, whose f32
+// results k_attn_join adds up.
+//
+// Measured (kernels, D = 128): 32 sequences of 2048 to 8191 keys x 8 heads, 5 queries each, 183 MB of cache in 39 us (4.7
+// TB/s) and 4.8 more to join them; one of 131072 x 8 heads, 151 MB in 33 (4.6 TB/s) and 5.9; one of 1000 x 2 heads
+// 10.0. A tile has 16 matrix instructions and some 250 vector ones, 128 of them to make operands of codes; at the first of
+// these the vector units issue 0.55 of the time, a wave waits 0.27 of its own for memory and 0.45 for its turn. The rest is
+// the start (sequence, page, keys: three dependent reads, some 7 us) and sequences of unequal length. Tried without
+// gain: parts of one size however long the sequences are (46 -> 48 us, and 56 where parts cross them), 64 tokens a step,
+// one page a tile, heads of one XCD next to each other.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.hpp"
 #include "device_once.hpp"
@@ -382,8 +391,10 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   }
 }
 
-// out = sum over the parts of O 2^(m - M) / sum of l 2^(m - M). TR lanes share a row (a wave, or the workgroup where
-// there are many parts): a lane takes four d of every G-th part, and its loads wait for nothing but the row's number.
+// out = sum over the parts of O 2^(m - M) / sum of l 2^(m - M), bound by its launch and two dependent reads. TR lanes share
+// a row (a wave; four or sixteen from 17 and 65 parts on: with one wave 128 parts of 64 rows take 8 us longer): a lane
+// takes four d of every G-th part, and its loads wait for nothing but the row's number. 4.8 us for 4 parts of 1280 rows of
+// 128, 6.3 for 4 of 5760, 5.9 for 128 of 64.
 constexpr int kMaxSplits = 256;
 template <int TR>
 __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L, int R, int max_rows) {
@@ -465,10 +476,18 @@ struct Shape {
   int64_t items;
 };
 
-// STREAM. Rows of a workgroup: the fewest sets of 16 that hold a sequence's rows, four at most (two beyond a width of
-// 128). Splits: as many workgroups as the card holds at once, each wave with kMinTiles tiles at least.
-// MFMA: 128 rows; splits likewise, of eight tiles at least.
-// Few short sequences: one workgroup of 16 waves (8 beyond a width of 128) each, and no join.
+// STREAM. A workgroup's rows: one set of up to 48 where that holds a sequence's rows (at 45 of them 33 us; as sets of 16
+// 100 against 80 at 48 rows of 32 sequences to 8191 keys), two of 32 for 49 to 64 (96 us; four of 16 115, two of 48
+// 113), two of 48 for 65 to 96 (115 at 80; three of 32 139, five of 16 146): a set more decodes the keys and values again, a
+// larger one leaves fewer waves. Beyond a width of 128 sets of 16 or 32 (32 rows: 44.9, two of 16 45.4). Rows that share
+// keys come next to each other on one XCD, whose L2 serves the second.
+// Splits: as many workgroups as the card holds at once, `resident` a CU by registers and LDS. Half of it 46.0 -> 48.8
+// us (32 sequences to 8191 keys), 33.0 -> 36.6 (16 x 9 tokens), twice 49.8 and 41.0. Down to a tile a wave as long as
+// that gives each CU a workgroup (one sequence of 4096 keys 9.7 us, 11.3 with kMinTiles alone, 2048 9.4 and 11.2),
+// kMinTiles a wave beyond (8 sequences of 4096 keys: 14.7; with two 15.5, with eight 16.8).
+// Few short sequences: one workgroup of eight waves each and no join, which saves the call a launch (1000 keys: 10.0 us
+// in the kernel, 9.2 as two, of the call's 14; 2048 keys 14.7 against 9.4, so not beyond kShort tiles; sixteen waves 10.5).
+// MFMA: 128 rows; splits likewise, of a workgroup's tiles.
 constexpr int kMinTiles = 4, kShort = 32;
 Shape shape_of(const AttnArgs& a, bool tile) {
   Shape s;
@@ -508,7 +527,10 @@ void launch(const AttnLaunch& L, const Shape& s, hipStream_t st) {
 
 }  // namespace
 
-// The tiles where a sequence has more rows than one workgroup of the stream takes.
+// The tiles where a sequence has more rows than two sets of the stream, or one of the wide, hold. 32 sequences to 8191
+// keys: 96 rows 115 us streamed, 136 as tiles, 104 rows 168 and 149; D = 64: 96 rows 84 and 93, 104 rows 110 and
+// 100; D = 256, 8 sequences of 16384: 32 rows 45 and 68, 36 rows 70 and 71, 64 rows 72 and 76. One sequence of 4096 keys
+// with 128 rows has too few workgroups for either (20 and 24).
 bool attn_takes_tile(const AttnArgs& a) { return a.max_q * (a.Hq / a.c.heads) > (a.c.D > 128 ? 32 : 96); }
 
 int64_t attn_workspace(const AttnArgs& a) {

@@ -1,14 +1,22 @@
 // Attention over the 4-bit cache for many query rows to a key head: prompts and chunks of prompts.
 //
-// Bound by the matrix cores and, beside them, by the exponentials. A workgroup takes 32 rows a wave and walks tiles of
-// TK keys: all its threads decode a tile's keys and values once, to f16 in LDS, while the loads of the next tile are in
-// flight; two buffers, one barrier a tile. With v_mfma_f32_32x32x16_f16, l the lane and h = l / 32:
+// A workgroup takes 32 rows a wave and walks tiles of TK keys: all its threads decode a tile's keys and values once, to
+// f16 in LDS, while the loads of the next tile are in flight; two buffers, one barrier a tile. With v_mfma_f32_32x32x16_f16, l the lane and h = l / 32:
 //   S^T: A = keys from LDS (token l % 32, d = 16 s + 8 h ..), B = Q from registers. The result has token
 //        8 (i / 4) + 4 h + i % 4 of 32 in register i, row l % 32.
 //   O^T: B = P, the lane's own eight tokens of every 16 (8 (x / 4) + 4 h + x % 4); A = values, stored transposed and in
 //        that order of tokens, so an operand is one 16-byte read. Row p of tile m is d = (DP / 32) p + m, which gives the
 //        decoding threads, eight d of four tokens each, rows whose LDS banks do not meet (rows are 16 bytes longer than
 //        their data for that), and a lane of the result runs of DP / 8 consecutive d.
+//
+// Measured: a prompt of 8192 tokens x 40 heads (8 of keys), D = 128, causal, 710 us (970 TFLOP/s; a large matrix product
+// reaches 1158 on this card), 7 chunks of 214 to 1500 queries over 2251 to 9001 keys, 16 heads (4), D = 256, 520 us (855).
+// Bound by the matrix cores and the vector units together: at D = 128 a wave's tile of 32 keys has 16 matrix
+// instructions, 526 clocks of a SIMD, and some 150 vector instructions (exponentials, maxima, the conversion of p, a
+// quarter of the decoding), some 650; matrix cores 0.48 and vector units 0.63 of the time, a wave waits 0.29 of its own for
+// its turn, and the clock falls to some 2.05 GHz under that load. Tried without gain: the next tile's logits before this
+// one's softmax (733 us where this took 748), 256 rows (756), the overflow of sums in place of the maxima, LDS operands
+// read ahead in a fixed order, 64 rows of two waves.
 #include <algorithm>
 
 #include "attn.hpp"
@@ -77,7 +85,8 @@ __device__ __forceinline__ int wave_max(int x) {
 // long ones do not end alone. Tile j from the end of sequence b lies at level off_b + j of R rows below max_kv keys, so
 // C(p) = sum over b of clamp(p - off_b, 0, tiles_b) items lie above level p; the last of the levels off_b and
 // off_b + tiles_b with C <= t is found, a lane a sequence, and from there each level holds the same sequences. Beyond 64
-// sequences: the last tiles of all, then those before. False behind the last item.
+// sequences: the last tiles of all, then those before. False behind the last item. 7 chunks of 214 to 1500 queries
+// over 2251 to 9001 keys: 520 us, 775 in the order of the batch; 16 prompts of 512 72 and 73 to 79.
 __device__ __forceinline__ bool find_item(const AttnLaunch& L, int t, int lane, int& b, int& rt, Seq& seq) {
   const int B = (int)L.a.B;
   if (B > 64 || B == 1) {
@@ -377,6 +386,8 @@ hipError_t launch(const AttnLaunch& L, int64_t groups, hipStream_t st) {
 
 hipError_t launch_attn_tile(const AttnLaunch& L, int64_t groups, hipStream_t st) {
   const int D = L.a.c.D;
+  // 64 keys a tile at D = 64, as four waves need for their 16-byte pieces; 32 at D = 128, where 64 leave room for two waves
+  // a SIMD (a prompt of 8192 tokens 715 us, 740 with 64; 16 of 512 73 and 88), and at 256, where LDS holds no more
   if (D <= 64) return launch<64, 4, 64, 2>(L, groups, st);
   if (D <= 128) return launch<128, 4, 32, 3>(L, groups, st);
   return launch<256, 4, 32, 2>(L, groups, st);
