@@ -13,9 +13,9 @@
 // The waves of a workgroup take tiles in turn and meet in LDS; long sequences are split over workgroups, whose f32
 // results k_attn_join adds up.
 //
-// Measured (kernels, D = 128): 32 sequences of 2048 to 8191 keys x 8 heads, 5 queries each, 183 MB of cache in 39 us (4.7
-// TB/s) and 4.8 more to join them; one of 131072 x 8 heads, 151 MB in 33 (4.6 TB/s) and 5.9; one of 1000 x 2 heads
-// 10.0. A tile has 16 matrix instructions and some 250 vector ones, 128 of them to make operands of codes; at the first of
+// Measured (kernels, D = 128): 32 sequences of 2048 to 8191 keys x 8 heads, 5 queries each, 183 MB of cache in 41 us (4.5
+// TB/s) and 4.7 more to join them; one of 131072 x 8 heads, 151 MB in 31.5 (4.8 TB/s) and 6.4; one of 1000 x 2 heads
+// 9.8. A tile has 16 matrix instructions and some 250 vector ones, 128 of them to make operands of codes; at the first of
 // these the vector units issue 0.55 of the time, a wave waits 0.27 of its own for memory and 0.45 for its turn. The rest is
 // the start (sequence, page, keys: three dependent reads, some 7 us) and sequences of unequal length. Tried without
 // gain: parts of one size however long the sequences are (46 -> 48 us, and 56 where parts cross them), 64 tokens a step,
@@ -393,8 +393,8 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
 
 // out = sum over the parts of O 2^(m - M) / sum of l 2^(m - M), bound by its launch and two dependent reads. TR lanes share
 // a row (a wave; four or sixteen from 17 and 65 parts on: with one wave 128 parts of 64 rows take 8 us longer): a lane
-// takes four d of every G-th part, and its loads wait for nothing but the row's number. 4.8 us for 4 parts of 1280 rows of
-// 128, 6.3 for 4 of 5760, 5.9 for 128 of 64.
+// takes four d of every G-th part, and its loads wait for nothing but the row's number. 4.7 us for 4 parts of 1280 rows of
+// 128, 6.6 for 4 of 5760, 6.4 for 128 of 64.
 constexpr int kMaxSplits = 256;
 template <int TR>
 __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L, int R, int max_rows) {
