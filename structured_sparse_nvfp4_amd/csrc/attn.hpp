@@ -26,7 +26,8 @@ constexpr float kShift = 7.f, kTop = 15.f;
 constexpr float kUnset = -3e38f;                 // m of a row that has met no key
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-// n / d for n < 2^31 by a multiplication: m = ceil(2^(31 + s) / d) with 2^s >= d, so m d - 2^(31 + s) < d <= 2^s and m < 2^32
+// n / d for n < 2^31 by a multiplication: m = ceil(2^(31 + s) / d) with 2^(s - 1) < d <= 2^s is below 2^32, and its excess
+// e = m d - 2^(31 + s) < d keeps n e below 2^(31 + s), so the quotient is exact
 struct Divisor {
   uint32_t m, d;
   int shift;
@@ -172,8 +173,8 @@ __device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Exponent shift that brings a row's largest magnitude into [2^15, 2^16), or as near as 2^127 does (from below
-// 2^-112: its logits are nothing then); 0 for a row of zeros or not finite.
+// Exponent shift that brings a row's largest magnitude into [2^15, 2^16), or as near as 2^127 does (which loses nothing:
+// f16 ends at 2^-24, and no bf16 lies below 2^-133); 0 for a row of zeros or not finite.
 __device__ __forceinline__ int row_shift(float amax) {
   if (!(amax > 0.f) || !(amax < __builtin_inff())) return 0;
   int e;
