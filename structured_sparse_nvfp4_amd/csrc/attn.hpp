@@ -182,6 +182,13 @@ __device__ __forceinline__ int row_shift(float amax) {
   return min(16 - e, 127);
 }
 
+// What a row of queries is multiplied by before it is rounded to f16: a power of two, with the sign of the logits' factor. NaN
+// where the row is not finite: any product with an infinite query is infinite or undefined, so the softmax of such a
+// row is undefined, and logits of -infinity alone would be taken for keys that the row does not keep.
+__device__ __forceinline__ float row_scale(float amax, float factor, int shift) {
+  return amax < __builtin_inff() ? ldexpf(factor < 0.f ? -1.f : 1.f, shift) : __builtin_nanf("");
+}
+
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // the largest magnitude of packed 16-bit values so far, as bits (those of bf16 and of f16 ascend with the magnitude)

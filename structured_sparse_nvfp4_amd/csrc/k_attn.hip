@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    const float by = ldexpf(sc < 0.f ? -1.f : 1.f, sh);
+    const float by = row_scale(amax, sc, sh);
     if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], by);
     else scale_rows<kF16>(raw[n], by);
 #pragma unroll

@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
     const int sh = row_shift(amax);
-    const float by = ldexpf(sc < 0.f ? -1.f : 1.f, sh);
+    const float by = row_scale(amax, sc, sh);
     if (L.a.q_type == kBF16) scale_rows<kBF16>(x, by);
     else scale_rows<kF16>(x, by);
 #pragma unroll
