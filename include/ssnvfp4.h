@@ -525,7 +525,8 @@ int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const
  * over the keys j <= p, j > p - window where window > 0, or all j < seq_lens[b] where causal is 0 (then without a
  * window). lse (f32 [Tq, Hq], nullable) receives the natural logarithm of the sum of the exponentials. A row without
  * keys (an empty sequence, more queries than keys) is 0, its lse -infinity. A row of queries with an infinity or NaN is NaN
- * if it has a key, and touches no other row.
+ * if it has a key, and so is one of which |scale| s_h max|Q| log2(e) is 2^107 or more, whose logits might pass f32's
+ * range; neither touches another row.
  *   Q          bf16 or f16 (q_dtype) [Tq, Hq, D], the D values of a head contiguous, 16-byte aligned strides
  *   out        [Tq, Hq, D] contiguous, of q_dtype or f32 (out_dtype)
  *   block_table int32 [B, max_blocks]  page of every page_size tokens of a sequence; a value outside [0, pages) is a page

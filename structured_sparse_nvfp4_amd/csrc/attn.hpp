@@ -182,11 +182,30 @@ __device__ __forceinline__ int row_shift(float amax) {
   return min(16 - e, 127);
 }
 
-// What a row of queries is multiplied by before it is rounded to f16: a power of two, with the sign of the logits' factor. NaN
-// where the row is not finite: any product with an infinite query is infinite or undefined, so the softmax of such a
-// row is undefined, and logits of -infinity alone would be taken for keys that the row does not keep.
-__device__ __forceinline__ float row_scale(float amax, float factor, int shift) {
-  return amax < __builtin_inff() ? ldexpf(factor < 0.f ? -1.f : 1.f, shift) : __builtin_nanf("");
+// scale s_h log2(e) as m 2^e: the product itself may leave f32's range where the queries bring the logits back into it
+struct Factor {
+  float m;
+  int e;
+};
+__device__ __forceinline__ Factor factor_of(float scale, float ts) {
+  int a, b;
+  const float m = frexpf(scale, &a) * frexpf(ts, &b) * kLog2e;
+  return {m, a + b};
+}
+
+// What a row of queries is multiplied by before it is rounded to f16, a power of two with the factor's sign, and what takes
+// its products with K_hat to logits in powers of two: 1e-30 at least (not 0, which -inf would turn into NaN; the
+// largest sum of products is 2^36). NaN for a row that is not finite: any product with an infinite query is infinite or
+// undefined, so its softmax is undefined, and logits of -infinity alone would be taken for keys that it does not
+// keep. NaN too where |factor| times the row's largest magnitude is 2^107 or more: below, no sum of 256 products with
+// 2688 at most passes 2^127, and a logit is -infinity only where it is masked.
+struct RowScale {
+  float by, c;
+};
+__device__ __forceinline__ RowScale row_scale(float amax, const Factor& f) {
+  const int sh = row_shift(amax);
+  const float c = fminf(fmaxf(ldexpf(fabsf(f.m), f.e - sh), 1e-30f), 0x1p100f);
+  return {c * ldexpf(amax, sh) < 0x1p107f ? ldexpf(f.m < 0.f ? -1.f : 1.f, sh) : __builtin_nanf(""), c};
 }
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));

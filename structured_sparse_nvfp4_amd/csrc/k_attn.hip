@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   f16x8 q[NT][KS];
   float c[NT];
   int lo_r[NT], hi_r[NT];
-  const float sc = L.a.scale * L.a.c.k_ts[h] * kLog2e;
+  const Factor factor = factor_of(L.a.scale, L.a.c.k_ts[h]);
   u32x4 raw[NT][KS];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -201,13 +201,12 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
-    const int sh = row_shift(amax);
-    const float by = row_scale(amax, sc, sh);
-    if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], by);
-    else scale_rows<kF16>(raw[n], by);
+    const RowScale scale = row_scale(amax, factor);
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(raw[n], scale.by);
+    else scale_rows<kF16>(raw[n], scale.by);
 #pragma unroll
     for (int j = 0; j < KS; ++j) q[n][j] = as_f16x8(raw[n][j]);
-    c[n] = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);   // not 0, which -inf would turn into NaN
+    c[n] = scale.c;
   }
 
   f32x4 o[NT][MV] = {};

@@ -237,7 +237,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   const int r = w.row0 + 32 * wave + col;
   int lo_r, hi_r;
   row_keys(L, w, r, lo_r, hi_r);
-  const float sc = L.a.scale * c.k_ts[h] * kLog2e;
+  const Factor factor = factor_of(L.a.scale, c.k_ts[h]);
   f16x8 q[KS];
   float cf;
   {
@@ -254,13 +254,12 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     }
     float amax = max_of(m, L.a.q_type);
     amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
-    const int sh = row_shift(amax);
-    const float by = row_scale(amax, sc, sh);
-    if (L.a.q_type == kBF16) scale_rows<kBF16>(x, by);
-    else scale_rows<kF16>(x, by);
+    const RowScale scale = row_scale(amax, factor);
+    if (L.a.q_type == kBF16) scale_rows<kBF16>(x, scale.by);
+    else scale_rows<kF16>(x, scale.by);
 #pragma unroll
     for (int s = 0; s < KS; ++s) q[s] = as_f16x8(x[s]);
-    cf = fmaxf(ldexpf(fabsf(sc), -sh), 1e-30f);    // not 0, which -inf would turn into NaN
+    cf = scale.c;
   }
   if (ta < tb) {
     find_pages(ta);

@@ -1,4 +1,6 @@
-"""Attention over the 4-bit cache at the ends of its numbers' range: queries that are not finite."""
+"""Attention over the 4-bit cache at the ends of its numbers' range: queries that are not finite, scales
+whose product with s_h leaves f32's range, logits that would."""
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +47,35 @@ def test_queries_that_are_not_finite(D, Hq, H, lens, qs, bad, algo):
         none = torch.isneginf(wl)
         assert bool(out[hit & ~none].isnan().all()) and bool(lse[hit & ~none].isnan().all())
         assert torch.equal(out[~hit | none], want[~hit | none]) and torch.equal(lse[~hit | none], wl[~hit | none])
+
+
+@both
+@pytest.mark.parametrize("scale,size,k_scale,spread", [(1e-38, 3e38, 1.3e-5, 0.03), (3e38, 1e-38, 4.0, 0.1), (-3e38, 3e-38, 4.0, 0.1),
+                                                       (1e-30, 1e33, 1e-6, 0.001), (1e-20, 1e36, 1e-20, 3e-18)])
+def test_scales_and_queries_that_meet_in_the_middle(scale, size, k_scale, spread, algo):
+    """The product of scale and s_h lies beyond f32's range, or among its subnormals, the logits do not."""
+    B = Batch([200, 60], [2, 3], 4, 2, 64, 16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for b, S in enumerate(B.lens):
+        K, V = (torch.randn((S, 2, 64), generator=g, device="cuda") for _ in range(2))
+        write(B, b, K * spread, V, k_scale)
+    B.Q.copy_(torch.randn(B.Q.shape, generator=g, device="cuda").clamp(-1, 1) * size)
+    assert bool(B.Q.isfinite().all())
+    out, lse, _ = B.call(algo=algo, scale=scale, with_lse=True, out_dtype=torch.float32)
+    B.check(out, lse, scale=float(np.float32(scale)), out_type="f32")
+
+
+@both
+@pytest.mark.parametrize("scale,size", [(1.0, 3e38), (-1.0, 3e38), (3e38, 100.0), (3e38, 3e38)])
+def test_logits_beyond_f32(scale, size, algo):
+    """A row whose |scale| s_h max|Q| log2(e) is 2^107 or more is undefined; the rows beside it are what they are."""
+    B = Batch([150, 2], [2, 4], 4, 2, 128, 16)
+    want, wl, _ = B.call(algo=algo, scale=scale, Q=B.Q * 0, with_lse=True)
+    assert bool(want.isfinite().all())
+    Q = B.Q * 0
+    Q[1, 2, 5], Q[2, 1, 127], Q[5, 0, 0] = size, -size, size
+    hit = (Q != 0).any(2)
+    out, lse, _ = B.call(algo=algo, Q=Q, with_lse=True, scale=scale)
+    none = torch.isneginf(wl)
+    assert bool(out[hit & ~none].isnan().all()) and bool(lse[hit & ~none].isnan().all()) and bool((hit & none).any())
+    assert torch.equal(out[~hit | none], want[~hit | none]) and torch.equal(lse[~hit | none], wl[~hit | none])
