@@ -20,7 +20,7 @@ namespace ssn {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// p is held as 2^(y - m + 7): f16's normal range then reaches down to 2^-21 of a row's largest and its subnormals to
+// p is held as 2^(y - m + 7) (Reference has large logits): f16's normal range then reaches down to 2^-21 of a row's largest and its subnormals to
 // 2^-31. The reference m of a row is raised only where some y - m passes 8, so p stays below 2^15.
 constexpr float kShift = 7.f, kTop = 15.f;
 constexpr float kUnset = -3e38f;                 // m of a row that has met no key
@@ -207,6 +207,26 @@ __device__ __forceinline__ RowScale row_scale(float amax, const Factor& f) {
   const float c = fminf(fmaxf(ldexpf(fabsf(f.m), f.e - sh), 1e-30f), 0x1p100f);
   return {c * ldexpf(amax, sh) < 0x1p107f ? ldexpf(f.m < 0.f ? -1.f : 1.f, sh) : __builtin_nanf(""), c};
 }
+
+// A row's reference as the loops hold it. They take p = 2^(s c - m + 7) from one FMA, whose m has f32's spacing: from 2^25
+// on that alone could lift p beyond f16 or drop the largest term to 0. So where |m| is 2^24 or more, m and c are both
+// divided by a power of two, `up`, that leaves |m| below 2^24: terms near the largest then differ by fewer powers of two
+// than they should, where an f32 logit of that size tells them apart by a few of its steps only. `up` follows each new
+// reference (a row's first keys may have logits of -2^30 and its later ones of 1).
+struct Reference {
+  float m = kUnset, c, up = 1.f;
+  // raised to the logit of the product s, if that is higher; returns what the sums so far are multiplied by
+  __device__ __forceinline__ float raise(float s) {
+    const float now = m * up, row = c * up, to = fmaxf(now, s * row - kShift);
+    int e = 0;
+    if (to > kUnset) (void)frexpf(to, &e);
+    const int k = max(e - 24, 0);
+    m = ldexpf(to, -k);
+    c = ldexpf(row, -k);
+    up = ldexpf(1.f, k);
+    return exp2_hw(now - to);
+  }
+};
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 

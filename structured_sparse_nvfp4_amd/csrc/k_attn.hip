@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
 
   // queries: lane's row col of every 16, d = (DP / 4) kb + 8 j ..
   f16x8 q[NT][KS];
-  float c[NT];
+  Reference ref[NT];
   int lo_r[NT], hi_r[NT];
   const Factor factor = factor_of(L.a.scale, L.a.c.k_ts[h]);
   u32x4 raw[NT][KS];
@@ -206,13 +206,13 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     else scale_rows<kF16>(raw[n], scale.by);
 #pragma unroll
     for (int j = 0; j < KS; ++j) q[n][j] = as_f16x8(raw[n][j]);
-    c[n] = scale.c;
+    ref[n].c = scale.c;
   }
 
   f32x4 o[NT][MV] = {};
-  float mc[NT], l[NT];
+  float l[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) { mc[n] = kUnset; l[n] = 0.f; }
+  for (int n = 0; n < NT; ++n) l[n] = 0.f;
 
   // A tile's keys are replaced by the next tile's as soon as its logits are formed, its values when they are used: what
   // is loaded has a tile's time to arrive.
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
       top[n] = s[n][0][0];
 #pragma unroll
       for (int i = 1; i < 4 * TU; ++i) top[n] = fmaxf(top[n], s[n][i / 4][i % 4]);
-      raise |= top[n] * c[n] - mc[n] > kTop;
+      raise |= top[n] * ref[n].c - ref[n].m > kTop;
     }
     if (__any(raise)) {
 #pragma unroll
@@ -270,9 +270,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
         float m = top[n];
         m = fmaxf(m, __shfl_xor(m, 16, 64));
         m = fmaxf(m, __shfl_xor(m, 32, 64));
-        const float to = fmaxf(mc[n], m * c[n] - kShift);
-        const float f = exp2_hw(mc[n] - to);
-        mc[n] = to;
+        const float f = ref[n].raise(m);
         l[n] *= f;
 #pragma unroll
         for (int v = 0; v < MV; ++v) o[n][v] *= f;
@@ -286,7 +284,7 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          e[i] = exp2_hw(fmaf(s[n][2 * a + i / 4][i % 4], c[n], -mc[n]));
+          e[i] = exp2_hw(fmaf(s[n][2 * a + i / 4][i % 4], ref[n].c, -ref[n].m));
           l[n] += e[i];
         }
         p[n][a] = as_f16x8(u32x4{pk_f16(e[0], e[1]), pk_f16(e[2], e[3]), pk_f16(e[4], e[5]), pk_f16(e[6], e[7])});
@@ -318,10 +316,12 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
   // The waves' results meet in LDS, rows of D padded so that 16 lanes' pieces lie in different banks; then each thread
   // adds up four d of a row over the waves, brought to their common reference. Where all of them would leave LDS for
   // one workgroup a CU only (NT 3), the upper half of the waves goes into the lower first.
+  float mc[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     l[n] += __shfl_xor(l[n], 16, 64);
     l[n] += __shfl_xor(l[n], 32, 64);
+    mc[n] = ref[n].m * ref[n].up;
   }
   auto put = [&](int to) {
 #pragma unroll

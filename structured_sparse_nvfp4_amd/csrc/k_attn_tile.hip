@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   row_keys(L, w, r, lo_r, hi_r);
   const Factor factor = factor_of(L.a.scale, c.k_ts[h]);
   f16x8 q[KS];
-  float cf;
+  Reference ref;
   {
     const int rr = min(r, w.rows - 1), i = div_by(L.gd, rr);
     const uint16_t* src = (const uint16_t*)L.a.Q + (w.q0 + i) * L.a.q_token + (int64_t)(h * L.G + (rr - i * L.G)) * L.a.q_head;
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     else scale_rows<kF16>(x, scale.by);
 #pragma unroll
     for (int s = 0; s < KS; ++s) q[s] = as_f16x8(x[s]);
-    cf = scale.c;
+    ref.c = scale.c;
   }
   if (ta < tb) {
     find_pages(ta);
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   if (first >= w.rows) whi = 0;
 
   f32x16 o[MT] = {};
-  float mc = kUnset, l = 0.f;
+  float l = 0.f;
 
   for (int t = ta; t < tb; ++t) {
     Buf& f = lds[(t - ta) & 1];
@@ -314,10 +314,9 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
     float top = s[0][0];
 #pragma unroll
     for (int i = 1; i < 16 * AT; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-    if (__any(top * cf - mc > kTop)) {
+    if (__any(top * ref.c - ref.m > kTop)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float to = fmaxf(mc, top * cf - kShift), by = exp2_hw(mc - to);
-      mc = to;
+      const float by = ref.raise(top);
       l *= by;
 #pragma unroll
       for (int m = 0; m < MT; ++m) o[m] *= by;
@@ -328,7 +327,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
       float e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        e[i] = exp2_hw(fmaf(s[y / 2][8 * (y & 1) + i], cf, -mc));
+        e[i] = exp2_hw(fmaf(s[y / 2][8 * (y & 1) + i], ref.c, -ref.m));
         l += e[i];
       }
       p[y] = as_f16x8(u32x4{pk_f16(e[0], e[1]), pk_f16(e[2], e[3]), pk_f16(e[4], e[5]), pk_f16(e[6], e[7])});
@@ -343,6 +342,7 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   }
 
   l += __shfl_xor(l, 32, 64);
+  const float mc = ref.m * ref.up;
   if (r >= w.rows) return;
   const int64_t part = ((((int64_t)b * c.heads + h) * L.row_tiles + rt) * L.splits + split) * R + 32 * wave + col;
   const int i0 = div_by(L.gd, r);

@@ -1,11 +1,14 @@
-"""Attention over the 4-bit cache at the ends of its numbers' range: queries that are not finite, scales
-whose product with s_h leaves f32's range, logits that would."""
+"""Attention over the 4-bit cache at the ends of its numbers' range: queries that are not finite, logits of any size,
+scales whose product with s_h leaves f32's range."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import structured_sparse_nvfp4_amd as ssn
-from attn_util import Batch
+from attn_util import HALF, Batch
+from oracle import kv
 
 pytestmark = pytest.mark.gpu
 
@@ -47,6 +50,68 @@ def test_queries_that_are_not_finite(D, Hq, H, lens, qs, bad, algo):
         none = torch.isneginf(wl)
         assert bool(out[hit & ~none].isnan().all()) and bool(lse[hit & ~none].isnan().all())
         assert torch.equal(out[~hit | none], want[~hit | none]) and torch.equal(lse[~hit | none], wl[~hit | none])
+
+
+@both
+@pytest.mark.parametrize("S,D,n", [(200, 64, 2), (300, 128, 1), (77, 256, 3), (9001, 128, 1)])
+@pytest.mark.parametrize("e", [-8, 10, 18, 21, 22, 23, 24, 25, 26, 27, 28, 30, 34, 40, 60, 100])
+def test_logits_of_any_size(e, S, D, n, algo):
+    """Logits scale q0 a with a of {1/2, 1, 2, 3, 4, 6}: from 2^18 on the largest alone is left, whatever the size.
+    The terms are all alike, so what they are rounded to cancels but for its half step of f16 (2^-11); each sum of f32
+    has far fewer than 2^4 steps of 2^-23 to lose here. The logarithm is one logit: its factor of three roundings, the
+    product, the reference's 7 and the last product, below 2^-20 of it together; log n and its rounding where logits are small."""
+    H, G = 2, 3
+    B = Batch([S], [n], H * G, H, D, 16)
+    rng = np.random.default_rng([S, D])
+    a = rng.choice([1.0, 2.0, 3.0, 4.0], (S, H))
+    a[rng.permutation(S - n)[:3]], a[S - n - 5:S - n - 3], a[3] = 6.0, 0.5, 0.5
+    K = torch.zeros((S, H, D), device="cuda")
+    K[:, :, 0], K[:, :, 1] = torch.from_numpy(a).cuda() / 8, 6.0 / 8        # the second makes each block's scale 1
+    V = torch.from_numpy(rng.standard_normal((S, H, D)).astype(np.float32)).cuda()
+    write(B, 0, K, V, 1 / 8)
+    k, v = B.values(0)
+    assert np.array_equal(k[:, :, 0], a / 8)
+    B.Q.zero_()
+    q0 = np.array([1.0, -1.3828125, 1.9921875, -1.0, 1.0078125, -1.9921875]) * 2.0 ** e
+    B.Q[:, :, 0] = torch.from_numpy(q0).to(B.Q.dtype)
+    for scale in (D ** -0.5, 0.3):
+        out, lse, _ = B.call(algo=algo, with_lse=True, scale=scale, out_dtype=torch.float32)
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        if e < 18:
+            B.check(out, lse, scale=float(np.float32(scale)), out_type="f32")
+            continue
+        for i in range(n):
+            for h in range(H * G):
+                z = float(np.float32(scale)) * q0[h] * k[:S - n + i + 1, h // G, 0]
+                top = np.nonzero(z == z.max())[0]
+                vs = v[top, h // G]
+                tol = np.abs(vs).mean(0) * (2.0 ** -11 + 2.0 ** -19) + 2.0 ** -23 * np.abs(vs.mean(0))
+                assert np.all(np.abs(got[i, h] - vs.mean(0)) <= tol), (i, h)
+                assert abs(gl[i, h] - (z.max() + math.log(len(top)))) <= 2.0 ** -20 * abs(z.max()) + 2.0 ** -18, (i, h)
+
+
+@both
+@pytest.mark.parametrize("S,D", [(400, 64), (400, 128), (9001, 128), (333, 256)])
+def test_small_logits_behind_huge_ones(S, D, algo):
+    """The first keys' logits are some -2^27, those of the later ones a few units apart: the later are weighed as if they
+    stood alone."""
+    H, G, n, first = 2, 2, 2, 150
+    B = Batch([S], [n], H * G, H, D, 16)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    K, V = (torch.randn((S, H, D), generator=g, device="cuda") for _ in range(2))
+    K[:, :, 0] = 0
+    K[:first, :, 0] = 6.0
+    write(B, 0, K, V, 1.0)
+    B.Q.copy_(torch.randint(-8, 9, B.Q.shape, generator=g, device="cuda").float() / 64)
+    B.Q[:, :, 0] = -2.0 ** 20
+    out, lse, _ = B.call(algo=algo, with_lse=True, scale=16.0, out_dtype=torch.float32)
+    keep = kv.keeps(S, n, True, 0)
+    keep[:, :first] = False                            # e^(-2^27) is 0
+    k, v = B.values(0)
+    assert np.all(k[first:, :, 0] == 0)
+    want, wl, tol, lt = kv.attention(B.Q.double().cpu().numpy(), k, v, 16.0, keep, HALF["f32"])
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+    assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= lt)
 
 
 @both
