@@ -535,8 +535,12 @@ int kv_nvfp4_read(const int64_t* slots, int64_t T, const uint8_t* k_codes, const
  *   q_offsets  int32 [B + 1] sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1; NULL: Tq / B each.
  *              No two sequences own one query
  *   max_q, max_kv            no sequence has more queries (those beyond are not computed) or tokens (a longer one is taken
- *              as one of max_kv); max_kv is at most max_blocks * page_size and 2^27. They size the launch.
- * B <= 65535.
+ *              as one of max_kv); max_kv is at most max_blocks * page_size and 2^27. They size the launch,
+ *              and max_q chooses the kernel of the whole batch.
+ * B <= 65535, Tq and max_blocks <= 2^31 - 1024, Hq <= 2^20, max_q Hq / Hkv <= 2^30, window in [0, 2^31 - 1024] and only
+ * with causal. A launch has 2^23 workgroups at most: STREAM one for each sequence, key head, set of 16 to 48 rows (of
+ * max_q Hq / Hkv; 65535 of them at most) and part of the keys; MFMA one for each 128 rows and part, or, where that is
+ * too many, Hkv (Tq Hq / Hkv / 128 + B).
  * Rows of out and lse that belong to no sequence, or lie beyond max_q, are left as they were. Logits, softmax
  * statistics and sums are f32; K_hat and V_hat enter unrounded, a softmax term is rounded to 11 bits (f16) before it
  * multiplies V_hat, and so is Q below 2^-39 of its row's largest magnitude.

@@ -673,7 +673,6 @@ namespace {
 
 constexpr int64_t kMaxKvTokens = (int64_t)1 << 26;    // of one append or read: their grids
 constexpr int64_t kMaxSeq = (int64_t)1 << 27;         // of one sequence: 32-bit token numbers
-constexpr int64_t kMaxGrid = (int64_t)1 << 23;        // workgroups of 512 threads at most
 
 int check_cache(const char* fn, const ssn::KvCache& c, int64_t pages, int64_t page_size, int64_t heads, int64_t D) {
   if (D < 32 || D > 256 || D % 32)
@@ -810,8 +809,10 @@ int attn_kv_nvfp4(const void* Q, int q_dtype, int64_t Tq, int Hq, int64_t q_toke
     if (workspace_bytes < need)
       return fail(SSN_E_RANGE, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)need);
   }
-  if (ssn::attn_workgroups(a, tile) > kMaxGrid || (!tile && ssn::attn_workgroups(a, tile) / (B * Hkv) > 65535))
-    return fail(SSN_E_SHAPE, "%s: B * Hkv * rows need more than 2^23 workgroups (65535 sets of rows with STREAM)", fn);
+  const int64_t groups = ssn::attn_workgroups(a, tile);
+  if (groups > ssn::kAttnGrid || (!tile && groups / (B * Hkv) > 65535))
+    return fail(SSN_E_SHAPE, "%s: %s needs %lld workgroups (2^23 at most, with STREAM 65535 a sequence and key head)", fn,
+                tile ? "MFMA" : "STREAM", (long long)groups);
   return hip_status(ssn::launch_attn(a, tile, as_stream(stream)), fn);
 }
 

@@ -43,6 +43,7 @@ struct AttnLaunch {
   AttnArgs a;
   Divisor pd, gd, td, sd;      // by the 16-token units of a page, G, row_tiles and splits
   int G, row_tiles, splits;
+  bool owned;                  // tiles: workgroups for those that Tq allows, not row_tiles a sequence
   int64_t each;                // queries of a sequence without q_offsets
   float* part_o;               // [item][split][R][D]
   float* part_ml;              // [item][split][R][2]
@@ -208,11 +209,11 @@ __device__ __forceinline__ RowScale row_scale(float amax, const Factor& f) {
   return {c * ldexpf(amax, sh) < 0x1p107f ? ldexpf(f.m < 0.f ? -1.f : 1.f, sh) : __builtin_nanf(""), c};
 }
 
-// A row's reference as the loops hold it. They take p = 2^(s c - m + 7) from one FMA, whose m has f32's spacing: from 2^25
+// A row's reference as the loops hold it, less 7. They take p = 2^(s c - m) from one FMA, whose m has f32's spacing: from 2^25
 // on that alone could lift p beyond f16 or drop the largest term to 0. So where |m| is 2^24 or more, m and c are both
 // divided by a power of two, `up`, that leaves |m| below 2^24: terms near the largest then differ by fewer powers of two
-// than they should, where an f32 logit of that size tells them apart by a few of its steps only. `up` follows each new
-// reference (a row's first keys may have logits of -2^30 and its later ones of 1).
+// than they should, those whose logits are within some thirty steps (2^-24) of it. `up` follows each new reference (a
+// row's first keys may have logits of -2^30 and its later ones of 1).
 struct Reference {
   float m = kUnset, c, up = 1.f;
   // raised to the logit of the product s, if that is higher; returns what the sums so far are multiplied by

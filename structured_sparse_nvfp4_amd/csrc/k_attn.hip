@@ -536,10 +536,13 @@ int64_t attn_workspace(const AttnArgs& a) {
   return std::max(workspace_of(a, shape_of(a, false)), workspace_of(a, shape_of(a, true)));
 }
 
-int64_t attn_workgroups(const AttnArgs& a, bool tile) {
-  const Shape s = shape_of(a, tile);
-  return s.items * s.splits;
+// Workgroups: row_tiles a sequence, or, where those are too many, the tiles that Tq queries can have (find_item).
+bool tiles_owned(const AttnArgs& a, const Shape& s, bool tile) { return tile && s.items * s.splits > kAttnGrid; }
+int64_t workgroups_of(const AttnArgs& a, const Shape& s, bool tile) {
+  if (!tiles_owned(a, s, tile)) return s.items * s.splits;
+  return (a.Tq * (a.Hq / a.c.heads) / kTileRows + a.B) * a.c.heads * s.splits;
 }
+int64_t attn_workgroups(const AttnArgs& a, bool tile) { return workgroups_of(a, shape_of(a, tile), tile); }
 
 hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {
   const Shape s = shape_of(a, tile);
@@ -552,12 +555,13 @@ hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t st) {
   L.sd = divisor((uint32_t)s.splits);
   L.each = a.q_offsets ? 0 : a.Tq / a.B;
   L.row_tiles = s.row_tiles;
+  L.owned = tiles_owned(a, s, tile);
   L.splits = s.splits;
   L.part_o = (float*)a.ws;
   L.part_ml = L.part_o + (s.splits > 1 ? s.items * s.splits * s.R * a.c.D : 0);
   const int D = a.c.D;
   if (tile) {
-    const hipError_t e = launch_attn_tile(L, s.items * s.splits, st);
+    const hipError_t e = launch_attn_tile(L, workgroups_of(a, s, tile), st);
     if (e != hipSuccess) return e;
   } else if (D == 64) launch<64, 64>(L, s, st);
   else if (D < 64) launch<64, 0>(L, s, st);

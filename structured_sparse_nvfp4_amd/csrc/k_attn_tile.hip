@@ -87,8 +87,30 @@ __device__ __forceinline__ int wave_max(int x) {
 // off_b + tiles_b with C <= t is found, a lane a sequence, and from there each level holds the same sequences. Beyond 64
 // sequences: the last tiles of all, then those before. False behind the last item. 7 chunks of 214 to 1500 queries
 // over 2251 to 9001 keys: 520 us, 775 in the order of the batch; 16 prompts of 512 72 and 73 to 79.
+//
+// Where row_tiles a sequence would be too many workgroups (a large batch whose max_q is all its queries), sequence b has
+// the items from v_b = floor(q_offsets[b] G / R) + b on: v ascends, v_(b+1) - v_b holds the sequence's tiles, and all
+// of them lie below Tq G / R + B. The last b with v_b <= t is found by 64 probes at once, three times for 65535.
 __device__ __forceinline__ bool find_item(const AttnLaunch& L, int t, int lane, int& b, int& rt, Seq& seq) {
   const int B = (int)L.a.B;
+  if (L.owned) {
+    auto first = [&](int x) {
+      const int64_t q0 = L.a.q_offsets ? max(L.a.q_offsets[x], 0) : x * L.each;
+      return (int)min(q0 * L.G / kTileRows, (int64_t)1 << 30) + x;
+    };
+    b = 0;
+    for (int n = B; n > 1;) {                            // b is in [b, b + n)
+      const int step = (n + 63) / 64;
+      const uint64_t in = __ballot(lane * step < n && first(b + min(lane * step, n - 1)) <= t);
+      const int probe = max(__popcll(in) - 1, 0) * step;
+      b += probe;
+      n = min(step, n - probe);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    rt = t - __builtin_amdgcn_readfirstlane(first(b));
+    seq = find_seq(L, b);
+    return rt >= 0;
+  }
   if (B > 64 || B == 1) {
     const int j = B == 1 ? t : t / B;
     b = t - j * B;

@@ -161,6 +161,7 @@ struct AttnArgs {
 };
 int64_t attn_workspace(const AttnArgs& a);              // bytes for the partial results, 0 if none are made
 bool attn_takes_tile(const AttnArgs& a);                // AUTO's choice
+constexpr int64_t kAttnGrid = (int64_t)1 << 23;         // workgroups of 512 threads at most
 int64_t attn_workgroups(const AttnArgs& a, bool tile);
 hipError_t launch_attn(const AttnArgs& a, bool tile, hipStream_t s);
 

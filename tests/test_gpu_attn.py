@@ -420,3 +420,46 @@ def test_both_ways_agree():
     B.check(a, la, out_type="f32")
     B.check(b, lb, out_type="f32")
     assert float((a - b).abs().max()) <= 2 * 2.0 ** -10 * float(a.abs().max())
+
+
+@pytest.mark.parametrize("B", [1, 2, 5, 64, 65, 130, 4097])
+@pytest.mark.parametrize("uniform", [False, True])
+def test_a_bound_of_queries_far_above_them(B, uniform):
+    """max_q = 2^28, of which no launch could hold the rows: workgroups for the queries there are."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 90 if B > 200 else 400, B)
+    qs = np.full(B, 7) if uniform else rng.integers(0, 5 if B > 200 else 70, B)
+    if not uniform and B > 2:
+        qs[0], qs[1], qs[-1], lens[-1] = 0, 150, 3, 200
+    X = Batch(lens.tolist(), qs.tolist(), 4, 1, 64, 16, seed=B)
+    for algo in (ssn.ALGO_AUTO, TILE):
+        out, lse, used = X.call(algo=algo, uniform=uniform, max_q=1 << 28, with_lse=True)
+        assert used == TILE
+        X.check(out, lse, seqs=range(0, B, 1 + B // 130))
+
+
+def test_a_large_batch_without_its_bound():
+    """2048 sequences of a few queries, 64 key heads: by default max_q is the number of all queries. Rows before the first
+    and behind the last sequence are left."""
+    B, H, D = 2048, 64, 32
+    rng = np.random.default_rng(9)
+    qs = rng.integers(0, 9, B)
+    X = Batch([5] * B, qs.tolist(), H, H, D, 16)
+    T = int(qs.sum())
+    assert B * H * (-(-(T + 24) // 128)) > 1 << 23
+    Q = torch.cat([X.Q[:16], X.Q, X.Q[:8]])
+    X.offsets = X.offsets + 16
+    out, lse = torch.full((T + 24, H, D), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T + 24, H), 7.0, device="cuda")
+    _, _, used = X.call(Q=Q, out=out, lse=lse, max_q=None)
+    assert used == TILE
+    X.check(out, lse, Q=Q, seqs=range(0, B, 97))
+    for t in (out, lse):
+        assert bool((t[:16] == 7).all()) and bool((t[-8:] == 7).all())
+    want, wl, used = X.call(Q=Q, max_q=8, with_lse=True)
+    assert used == STREAM
+    # Both kernels are within their bound of one value. Values: terms of 2^-11 each and half a step of bf16, of at most 2688 s_h < 6.
+    # Logarithms: a logit has D + 24 steps of 2^-23 of at most 16 (scale sum |q k| log2 e), that is 2^-13 of both at most.
+    a, b, la, lb = out[16:-8].float(), want[16:-8].float(), lse[16:-8], wl[16:-8]
+    assert float((a - b).abs().max()) <= 2 * (2.0 ** -11 + 2.0 ** -8) * 6
+    assert torch.equal(torch.isneginf(la), torch.isneginf(lb))
+    assert float((la - lb).nan_to_num(0).abs().max()) <= 2.0 ** -13
