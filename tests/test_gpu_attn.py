@@ -463,3 +463,30 @@ def test_a_large_batch_without_its_bound():
     assert float((a - b).abs().max()) <= 2 * (2.0 ** -11 + 2.0 ** -8) * 6
     assert torch.equal(torch.isneginf(la), torch.isneginf(lb))
     assert float((la - lb).nan_to_num(0).abs().max()) <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("D,rows,algo", [(64, 96, STREAM), (64, 97, TILE), (96, 96, STREAM), (128, 96, STREAM), (128, 97, TILE),
+                                         (160, 32, STREAM), (160, 33, TILE), (256, 32, STREAM), (256, 33, TILE)])
+@pytest.mark.parametrize("n", [1, 2])
+def test_where_the_choice_changes(D, rows, algo, n):
+    """96 rows to a key head (32 beyond a width of 128) are streamed, more are tiles: right on both sides."""
+    if rows % n:
+        rows += 1 if algo == TILE else -1
+    B = Batch([150, 37, 0], [n, n, n], rows // n, 1, D, 16)
+    out, lse, used = B.call(with_lse=True)
+    assert used == algo
+    B.check(out, lse)
+
+
+@both
+@pytest.mark.parametrize("S,parts", [(2000, (2, 16)), (6000, (17, 64)), (12000, (65, 256))])
+@pytest.mark.parametrize("D", [32, 96, 192, 224])
+def test_joins_of_every_width(D, S, parts, algo):
+    """The three forms of the join, where a row's four-value pieces do not divide the lanes that share it."""
+    H, n = 1, 2
+    B = Batch([S], [n], 2, H, D, 16)
+    # both kernels split alike here, and the tiles' 128 rows make the larger workspace
+    count = ssn.lib().attn_kv_nvfp4_workspace_bytes(1, 2, H, D, n, B.table.shape[1] * 16) // (128 * (D + 2) * 4)
+    assert parts[0] <= count <= parts[1]
+    out, lse, _ = B.call(algo=algo, with_lse=True)
+    B.check(out, lse)
