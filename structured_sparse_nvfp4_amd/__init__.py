@@ -862,9 +862,12 @@ def attn_kv_nvfp4(Q, cache, block_table, seq_lens, q_offsets=None, max_q=None, m
     [Tq, Hq, D] (rows may be strided), Hq a multiple of the cache's heads; block_table int32 [B, blocks]; seq_lens int32
     [B], the queries' tokens included; q_offsets int32 [B+1] where sequences have different numbers of queries (else
     Tq / B each). max_q and max_kv bound a sequence's queries and tokens (host numbers that size the launch: Tq, or
-    Tq / B, and the table's width unless given). scale: 1 / sqrt(D) unless given. window > 0: a query keeps its last
+    Tq / B, and the table's width unless given). max_q chooses the kernel of the whole batch too: with q_offsets give it (32
+    single tokens over 8192 keys take 57 us with max_q=1, 149 without), and give a prompt's chunk and decoded tokens
+    calls of their own. scale: 1 / sqrt(D) unless given. window > 0: a query keeps its last
     `window` keys. Returns (out [Tq, Hq, D] of Q's type unless out_dtype is float32, lse f32 [Tq, Hq] if with_lse or
-    given else None, algorithm that ran); rows of no sequence keep what out held, rows without keys are 0."""
+    given else None, algorithm that ran); rows of no sequence keep what out held, rows without keys are 0,
+    rows of queries that are not finite NaN."""
     (Tq, Hq, D) = _size(Q, 3, "Q")
     dev, qdt = Q.device, _code(Q.dtype, "Q", _HALVES)
     at, (P, S, H, Dc) = _kv(dev, cache)

@@ -8,8 +8,9 @@
 // holds one row's logits of several keys, which are its own operand of the second product: P never leaves its
 // registers. K_hat and V_hat without their f32 scale are E2M1 * E4M3: at most six significant bits, in 2^-10 .. 2688,
 // so exact in f16, and f16 is what both products take: p then has 11 bits where bf16 would have 8. A query row is
-// brought into f16's range by a power of two, which its logits' factor takes back: no bit of an f16 or bf16 value is
-// lost down to 2^-39 of the row's largest.
+// brought into f16's range by a power of two, which its logits' factor takes back: its largest magnitude lies in [2^15,
+// 2^16) then, and f16's last bit is 2^-24. So f16 queries are exact, bf16 ones (8 bits) down to 2^-32 of the row's
+// largest; below, they are off by 2^-40 of the largest at most.
 #pragma once
 #include "common.hpp"
 #include "launch.hpp"
@@ -20,8 +21,8 @@ namespace ssn {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// p is held as 2^(y - m + 7) (Reference has large logits): f16's normal range then reaches down to 2^-21 of a row's largest and its subnormals to
-// 2^-31. The reference m of a row is raised only where some y - m passes 8, so p stays below 2^15.
+// p is held as 2^(y - m + 7), large logits aside (Reference): f16's normal range then reaches down to 2^-21 of a row's
+// largest and its subnormals to 2^-31. The reference m of a row is raised only where some y - m passes 8, so p stays below 2^15.
 constexpr float kShift = 7.f, kTop = 15.f;
 constexpr float kUnset = -3e38f;                 // m of a row that has met no key
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;

@@ -14,12 +14,13 @@
 // results k_attn_join adds up.
 //
 // Measured (kernels, D = 128): 32 sequences of 2048 to 8191 keys x 8 heads, 5 queries each, 183 MB of cache in 41 us (4.5
-// TB/s) and 4.7 more to join them; one of 131072 x 8 heads, 151 MB in 31.5 (4.8 TB/s) and 6.4; one of 1000 x 2 heads
-// 9.8. A tile has 16 matrix instructions and some 250 vector ones, 128 of them to make operands of codes; at the first of
-// these the vector units issue 0.55 of the time, a wave waits 0.27 of its own for memory and 0.45 for its turn. The rest is
-// the start (sequence, page, keys: three dependent reads, some 7 us) and sequences of unequal length. Tried without
-// gain: parts of one size however long the sequences are (46 -> 48 us, and 56 where parts cross them), 64 tokens a step,
-// one page a tile, heads of one XCD next to each other.
+// TB/s) and 4.8 more to join them; one of 131072 x 8 heads, 151 MB in 31.4 (4.8 TB/s) and 6.3; one of 1000 x 2 heads
+// 9.9. A tile has 16 matrix instructions and some 250 vector ones, 128 of them to make operands of codes; at the first of
+// these the vector units issue 0.52 of the time, a wave waits 0.27 of its own for memory and 0.45 for its turn: not
+// memory, which streams 6.3 TB/s and more where it is only read, but the waves' turns bound it. The rest is the start
+// (sequence, page, keys: three dependent reads, some 7 us) and sequences of unequal length. Tried without gain: parts of
+// one size however long the sequences are (46 -> 48 us, and 56 where parts cross them), 64 tokens a step, one page a
+// tile, heads of one XCD next to each other.
 #include <algorithm>
 #include <type_traits>
 

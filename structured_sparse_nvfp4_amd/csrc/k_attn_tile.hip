@@ -9,14 +9,17 @@
 //        decoding threads, eight d of four tokens each, rows whose LDS banks do not meet (rows are 16 bytes longer than
 //        their data for that), and a lane of the result runs of DP / 8 consecutive d.
 //
-// Measured: a prompt of 8192 tokens x 40 heads (8 of keys), D = 128, causal, 710 us (970 TFLOP/s; a large matrix product
-// reaches 1158 on this card), 7 chunks of 214 to 1500 queries over 2251 to 9001 keys, 16 heads (4), D = 256, 520 us (855).
+// Measured: a prompt of 8192 tokens x 40 heads (8 of keys), D = 128, causal, 709 us (970 TFLOP/s; a large matrix product
+// reaches 1145 to 1158 on this card), 7 chunks of 214 to 1500 queries over 2251 to 9001 keys, 16 heads (4), D = 256, 520 us (855).
 // Bound by the matrix cores and the vector units together: at D = 128 a wave's tile of 32 keys has 16 matrix
 // instructions, 526 clocks of a SIMD, and some 150 vector instructions (exponentials, maxima, the conversion of p, a
 // quarter of the decoding), some 650; matrix cores 0.48 and vector units 0.63 of the time, a wave waits 0.29 of its own for
-// its turn, and the clock falls to some 2.05 GHz under that load. Tried without gain: the next tile's logits before this
-// one's softmax (733 us where this took 748), 256 rows (756), the overflow of sums in place of the maxima, LDS operands
-// read ahead in a fixed order, 64 rows of two waves.
+// its turn, and the clock falls to some 2.05 GHz under that load. Both products and the LDS rows run over DP, so widths
+// between pay for the next of 64, 128 and 256: that prompt at D = 32 takes 412 us, 64 444 (773 TFLOP/s: half the matrix work
+// for each exponential), 96 673, 160 1256, 192 1291, 224 1340, 256 1362 (1009). With tiles of 64 keys, where D = 128
+// took 748 us, the next tile's logits before this one's softmax took 733; with tiles of 32, at 715, that was not tried
+// again. Tried without gain: 256 rows (756), the overflow of sums in place of the maxima, LDS operands read ahead in a
+// fixed order, 64 rows of two waves.
 #include <algorithm>
 
 #include "attn.hpp"

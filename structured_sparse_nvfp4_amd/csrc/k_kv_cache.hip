@@ -4,9 +4,9 @@
 // (the head's): S = E4M3(amax / (6 s_h)), code = E2M1(x / (s_h S)), every decision exact (nvfp4_block.hpp); read
 // back it is E2M1(code) E4M3(S) s_h, the f32 product rounded once to f32 and from there to a 16-bit type.
 //
-// Both kernels move each value once: 8192 tokens x 8 heads x 128 of bf16 written in 10.8 us (43 MB, 4.0 TB/s, the start and
-// two dependent reads 3 of it; 395 vector instructions for 64 blocks a wave issue 0.72 of the time), read in 9.5 (4.5
-// TB/s); 65536 read in 51 (344 MB, 6.8 TB/s); 8 written in 3.4 and read in 2.8. A workgroup takes tokens of one head, keys or
+// Both kernels move each value once: 8192 tokens x 8 heads x 128 of bf16 written in 10.7 us (43 MB, 4.0 TB/s, the start and
+// two dependent reads 3 of it; 395 vector instructions for 64 blocks a wave issue 0.76 of the time), read in 9.3 (4.6
+// TB/s); 65536 read in 51 (344 MB, 6.8 TB/s); 8 written in 3.4 and read in 2.7. A workgroup takes tokens of one head, keys or
 // values, and its lanes lie along a token's blocks first: the rows it reads are runs of 2 D or 4 D bytes, and the
 // values' scales, whose tokens are innermost, come together where the slots of consecutive tokens are consecutive.
 #include <type_traits>
