@@ -157,6 +157,20 @@ __device__ __forceinline__ uint32_t pk_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
+// What takes a row's sums to its results: m = mantissa(s_h) / sum of the terms, and s_h's power of two last, since s_h / sum
+// may lie among f32's subnormals where a result does not. 0 for a row without keys.
+struct Finish {
+  float m;
+  int e;
+  __device__ __forceinline__ float operator()(float x) const { return ldexpf(x * m, e); }
+};
+__device__ __forceinline__ Finish finish(float ts, float sum) {
+  Finish f;
+  const float m = frexpf(ts, &f.e);
+  f.m = sum != 0.f ? m / sum : 0.f;
+  return f;
+}
+
 // N consecutive values (a multiple of four) of type t at element i
 template <int N>
 __device__ __forceinline__ void store_run(void* p, int t, int64_t i, const float* x) {

@@ -383,8 +383,8 @@ __global__ __launch_bounds__(64 * W, W > 4 ? W / 4 : NT * DP >= 512 ? 1 : NT * D
     } else {
       const int i = div_by(L.gd, r);
       const int64_t head = (w.q0 + i) * L.a.Hq + h * L.G + (r - i * L.G);
-      const float f = any ? L.a.c.v_ts[h] / sum : 0.f;
-      const float x[4] = {acc[0] * f, acc[1] * f, acc[2] * f, acc[3] * f};
+      const Finish f = finish(L.a.c.v_ts[h], sum);
+      const float x[4] = {f(acc[0]), f(acc[1]), f(acc[2]), f(acc[3])};
       store_run<4>(L.a.out, L.a.out_type, head * D + d, x);
       if (L.a.lse && d == 0) L.a.lse[head] = any ? (m + log2f(sum)) * kLn2 : -__builtin_inff();
     }
@@ -463,8 +463,8 @@ __global__ __launch_bounds__(TR == 64 ? 256 : TR) void k_attn_join(AttnLaunch L,
   for (int x = 1; x < groups; ++x) o += acc[rw][t + x * D4];
   const int i0 = div_by(L.gd, r);
   const int64_t head = (seq.q0 + i0) * L.a.Hq + h * L.G + (r - i0 * L.G);
-  const float by = sum != 0.f ? L.a.c.v_ts[h] / sum : 0.f;
-  const float x[4] = {o[0] * by, o[1] * by, o[2] * by, o[3] * by};
+  const Finish f = finish(L.a.c.v_ts[h], sum);
+  const float x[4] = {f(o[0]), f(o[1]), f(o[2]), f(o[3])};
   store_run<4>(L.a.out, L.a.out_type, head * D + d, x);
   if (L.a.lse && t == 0) L.a.lse[head] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -__builtin_inff();
 }

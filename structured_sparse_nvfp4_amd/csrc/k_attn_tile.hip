@@ -378,13 +378,14 @@ __global__ __launch_bounds__(64 * W, WPS) void k_attn_tile(AttnLaunch L) {
   } else if (L.a.lse && half == 0) {
     L.a.lse[head] = l != 0.f ? (mc + log2f(l)) * kLn2 : -__builtin_inff();
   }
-  const float by = L.splits > 1 ? 1.f : l != 0.f ? c.v_ts[h] / l : 0.f;
+  Finish fin = finish(c.v_ts[h], l);
+  if (L.splits > 1) fin = {1.f, 0};
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int d = MT * (8 * u + 4 * half);           // 4 MT consecutive d
     float x[4 * MT];
 #pragma unroll
-    for (int e = 0; e < 4 * MT; ++e) x[e] = o[e % MT][4 * u + e / MT] * by;
+    for (int e = 0; e < 4 * MT; ++e) x[e] = fin(o[e % MT][4 * u + e / MT]);
 #pragma unroll
     for (int e = 0; e < 4 * MT; e += 8) {
       if (d + e >= D) break;

@@ -144,3 +144,21 @@ def test_logits_beyond_f32(scale, size, algo):
     none = torch.isneginf(wl)
     assert bool(out[hit & ~none].isnan().all()) and bool(lse[hit & ~none].isnan().all()) and bool((hit & none).any())
     assert torch.equal(out[~hit | none], want[~hit | none]) and torch.equal(lse[~hit | none], wl[~hit | none])
+
+
+@both
+@pytest.mark.parametrize("S,D,n", [(300, 64, 2), (9001, 128, 1), (5000, 256, 3), (200, 96, 200)])
+@pytest.mark.parametrize("v_scale", [1e-37, -3e-38, 1.1e-36, 1e30])
+def test_values_of_any_size(v_scale, S, D, n, algo):
+    """The values' s_h over the sum of a long row lies among f32's subnormals, the result does not."""
+    B = Batch([S], [n], 4, 2, D, 16)
+    B.cache = B.cache._replace(v_tensor_scale=torch.tensor([1.0, 1.5], device="cuda") * v_scale)
+    B.cache.v_codes.copy_(torch.randint(0, 256, B.cache.v_codes.shape, dtype=torch.uint8, device="cuda") & 0x77)
+    B.Q[:, 0] = 0                                      # every key counts alike
+    B.cache.v_scales.fill_(0x70)                       # 128
+    out, lse, _ = B.call(algo=algo, with_lse=True, out_dtype=torch.float32)
+    k, v = B.values(0)
+    up = 2.0 ** -math.frexp(v_scale)[1]                # the bound is of values some way above 1e-30
+    want, wl, tol, lt = kv.attention(B.Q.double().cpu().numpy(), k, v * up, D ** -0.5, kv.keeps(S, n, True, 0), HALF["f32"])
+    assert np.all(np.abs(out.double().cpu().numpy() * up - want) <= tol)
+    assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= lt)
