@@ -162,3 +162,28 @@ def test_values_of_any_size(v_scale, S, D, n, algo):
     want, wl, tol, lt = kv.attention(B.Q.double().cpu().numpy(), k, v * up, D ** -0.5, kv.keeps(S, n, True, 0), HALF["f32"])
     assert np.all(np.abs(out.double().cpu().numpy() * up - want) <= tol)
     assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= lt)
+
+
+@both
+@pytest.mark.parametrize("size,scale", [(6e-8, 2e6), (1e-6, 1e5), (6e4, 1e-5), (6e4, 1e6), (6e4, 1e25)])
+def test_half_queries_from_end_to_end(size, scale, algo):
+    """f16 queries among the subnormals and next to the largest, with one row of an infinity and one of NaN."""
+    B = Batch([130, 40, 2100], [2, 1, 1], 4, 2, 96, 16, x="f16")
+    Q = (B.Q.float().clamp(-1, 1) * size).half()
+    assert bool(Q.isfinite().all()) and bool(Q.count_nonzero())
+    want, wl, _ = B.call(algo=algo, Q=Q, scale=scale, with_lse=True)
+    assert bool(want.isfinite().all()) and bool(wl.isfinite().all())
+    if abs(size * scale) < 1e6:                        # beyond, one key alone is left, and the bound says nothing of it
+        B.check(want, wl, Q=Q, scale=float(np.float32(scale)))
+    else:
+        top = [np.einsum("hd,shd->hs", Q[t].double().cpu().numpy(), B.values(b)[0].repeat(2, 1))[:, :S].argmax(1)
+               for t, b, S in ((1, 0, 130), (2, 1, 40), (3, 2, 2100))]
+        for i, (t, b) in enumerate(((1, 0), (2, 1), (3, 2))):
+            v = B.values(b)[1].repeat(2, 1)[top[i], np.arange(4)]
+            assert np.all(np.abs(want[t].double().cpu().numpy() - v) <= np.abs(v) * (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -19))
+    bad = Q.clone()
+    bad[1, 2, 95], bad[3, 0, 1] = float("-inf"), float("nan")
+    out, lse, _ = B.call(algo=algo, Q=bad, scale=scale, with_lse=True)
+    hit = ~bad.isfinite().all(2)
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
